@@ -1,4 +1,5 @@
-"""ctypes binding of liblstmstack.so (declared in include/lstm_stack.h).
+"""ctypes binding of liblstmstack.so (declared in include/lstm_stack.h and
+include/lstm_ops.h).
 
 Argument marshalling only: every function here checks nothing the library
 does not check again, computes nothing, and forwards to the C entry point of
@@ -34,6 +35,10 @@ LSTM_MATH_TF32 = 1
 LSTM_GATES_IFGO = 0
 LSTM_GATES_IOFC = 1
 LSTM_BOTH_DIRECTIONS = 2
+LSTM_F32 = 0
+LSTM_BF16 = 1
+LSTM_F16 = 2
+LSTM_E4M3 = 3
 
 _c_float_p = ctypes.POINTER(ctypes.c_float)
 _vp = ctypes.c_void_p
@@ -67,6 +72,7 @@ def load():
             raise LibraryMissing(f"{LIB_PATH} not found; build it with __graft_entry__.build()")
         lib = ctypes.CDLL(LIB_PATH)
         i, sz = ctypes.c_int, ctypes.c_size_t
+        ll, f = ctypes.c_longlong, ctypes.c_float
         sig = {
             "lstm_stack_create": (i, [ctypes.POINTER(_Weights), i, i, i, ctypes.POINTER(_vp)]),
             "lstm_stack_create_ordered": (i, [ctypes.POINTER(_Weights), i, i, i, i,
@@ -103,6 +109,17 @@ def load():
             "lstm_tf32_rate": (i, [i, i, ctypes.POINTER(ctypes.c_double)]),
             "lstm_recurrence_fused": (i, [_vp, i, _vp, _vp, i, _vp, _vp, _vp, i, i, i, _vp]),
             "lstm_stack_set_fused_batches": (i, [_vp, i]),
+            "lstm_causal_conv": (i, [_vp, ll, i, i, i, i, _vp, _vp, i, i, _vp, _vp, i, _vp, _vp,
+                                     _vp, ll, _vp]),
+            "lstm_causal_conv_step": (i, [_vp, ll, i, i, i, i, _vp, _vp, i, _vp, i, _vp, _vp, ll,
+                                          _vp]),
+            "lstm_selective_scan": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll, _vp,
+                                        i, i, i, i, i, i, i, _vp, _vp, i, _vp, _vp, _vp, ll, _vp]),
+            "lstm_selective_scan_step": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll,
+                                             _vp, i, i, i, i, i, i, _vp, i, _vp, _vp, ll, _vp]),
+            "lstm_residual_rms_norm": (i, [_vp, ll, _vp, ll, i, _vp, f, i, i, _vp, ll, _vp, ll, i,
+                                           _vp, i, _vp]),
+            "lstm_token_logprobs": (i, [_vp, ll, i, i, i, _vp, _vp, _vp, i, _vp, _vp, _vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -374,3 +391,277 @@ class LSTMHeads:
             self.close()
         except Exception:
             pass
+
+
+# ---- state-space layer and log probabilities (include/lstm_ops.h) -------------
+#
+# The C entry points take sizes and strides on trust, so these functions check
+# that every tensor has the type, shape and device that the call's sizes say.
+# Matrices are [rows, columns] with consecutive columns and any row stride.
+# Outputs that are not given are allocated for the stream the call runs on.
+
+
+def _element_type(t) -> int:
+    import torch
+    code = {torch.float32: LSTM_F32, torch.bfloat16: LSTM_BF16, torch.float16: LSTM_F16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"element type {t.dtype}, expected float32, bfloat16 or float16")
+    return code
+
+
+def _matrix(name: str, t, rows: int, cols: int, like) -> int:
+    """Row stride of the matrix t [rows, cols] of like's type and device."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, cols)}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} needs consecutive columns, has stride {inner} between them")
+    return stride
+
+
+def _dense(name: str, t, shape: tuple, dtype, device):
+    """Address of the densely packed tensor t (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not densely packed")
+    return t.data_ptr()
+
+
+def _on(stream, device):
+    """Context in which torch allocates for the stream that a call runs on."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(stream, shape, dtype, device):
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(stream, t):
+    """An uninitialised dense tensor of t's shape and type."""
+    return _empty(stream, t.shape, t.dtype, t.device)
+
+
+def _state(t, shape: tuple, dtype, sequences: int, slots, resume, device):
+    """Addresses and slot count of the states' arguments."""
+    import torch
+    if t is None:
+        if slots is not None or resume is not None:
+            raise ValueError("slots and resume need a state")
+        return None, 0, None, None
+    if t.dim() != len(shape) + 1:
+        raise ValueError(f"state has shape {tuple(t.shape)}, expected {('slots', *shape)}")
+    count = t.shape[0]
+    if slots is None and count < sequences:
+        raise ValueError(f"{sequences} sequences without slots, a state of {count}")
+    return (_dense("state", t, (count, *shape), dtype, device), count,
+            _dense("slots", slots, (sequences,), torch.int32, device),
+            _dense("resume", resume, (sequences,), torch.int32, device))
+
+
+def _sequences(sequences, offsets, device):
+    """Number of sequences and the offsets' address."""
+    import torch
+    if offsets is None:
+        return (1 if sequences is None else sequences), None
+    count = offsets.numel() - 1
+    if sequences is not None and sequences != count:
+        raise ValueError(f"{sequences} sequences, offsets for {count}")
+    return count, _dense("offsets", offsets, (count + 1,), torch.int32, device)
+
+
+def lstm_causal_conv(x, w, bias=None, *, silu: bool = True, sequences=None, offsets=None,
+                     state=None, slots=None, resume=None, y=None, stream=None):
+    """Causal depthwise convolution of packed prompts x [tokens, channels];
+    returns y (new unless given) and moves the state, if given, on.
+
+    w [channels, width] and bias [channels] fp32; offsets int32 [sequences + 1]
+    (None: `sequences` prompts of equal length, default one); state
+    [slots, width - 1, channels] of x's type, slots and resume int32
+    [sequences]."""
+    import torch
+    tokens, channels = x.shape
+    device = x.device
+    width = w.shape[-1]
+    dtype = _element_type(x)
+    count, offsets_at = _sequences(sequences, offsets, device)
+    state_at, state_slots, slots_at, resume_at = _state(
+        state, (width - 1, channels), x.dtype, count, slots, resume, device)
+    if y is None:
+        y = _like(stream, x)
+    _check(load().lstm_causal_conv(
+        x.data_ptr(), _matrix("x", x, tokens, channels, x), dtype, tokens, channels, width,
+        _dense("w", w, (channels, width), torch.float32, device),
+        _dense("bias", bias, (channels,), torch.float32, device), int(silu), count, offsets_at,
+        state_at, state_slots, slots_at, resume_at, y.data_ptr(),
+        _matrix("y", y, tokens, channels, x), _stream(stream, device)))
+    return y
+
+
+def lstm_causal_conv_step(x, w, bias, state, *, silu: bool = True, slots=None, y=None,
+                          stream=None):
+    """The next token of every sequence, x [sequences, channels]; returns y
+    (new unless given) and moves the state on.  Arguments as lstm_causal_conv."""
+    import torch
+    sequences, channels = x.shape
+    device = x.device
+    width = w.shape[-1]
+    state_at, state_slots, slots_at, _ = _state(
+        state, (width - 1, channels), x.dtype, sequences, slots, None, device)
+    if y is None:
+        y = _like(stream, x)
+    _check(load().lstm_causal_conv_step(
+        x.data_ptr(), _matrix("x", x, sequences, channels, x), _element_type(x), sequences,
+        channels, width, _dense("w", w, (channels, width), torch.float32, device),
+        _dense("bias", bias, (channels,), torch.float32, device), int(silu), state_at, state_slots,
+        slots_at, y.data_ptr(), _matrix("y", y, sequences, channels, x), _stream(stream, device)))
+    return y
+
+
+def _scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups):
+    """The arguments that both scan entry points begin with, up to softplus."""
+    import torch
+    rows, channels = u.shape
+    device = u.device
+    states = a.shape[-1]
+    return (u.data_ptr(), _matrix("u", u, rows, channels, u),
+            dt.data_ptr(), _matrix("dt", dt, rows, channels, u),
+            _dense("a", a, (channels, states), torch.float32, device),
+            b.data_ptr(), _matrix("b", b, rows, groups * states, u),
+            c.data_ptr(), _matrix("c", c, rows, groups * states, u),
+            _dense("skip", skip, (channels,), torch.float32, device),
+            None if z is None else z.data_ptr(),
+            0 if z is None else _matrix("z", z, rows, channels, u),
+            _dense("dt_bias", dt_bias, (channels,), torch.float32, device), int(softplus))
+
+
+def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, softplus: bool = True,
+                        groups: int = 1, sequences=None, offsets=None, state=None, slots=None,
+                        resume=None, y=None, stream=None):
+    """Selective scan of packed prompts u, dt, z [tokens, channels], b and c
+    [tokens, groups * states]; returns y (new unless given) and moves the
+    state, if given, on.
+
+    a [channels, states] (negative), skip and dt_bias [channels] fp32; offsets
+    int32 [sequences + 1] (None: `sequences` prompts of equal length, default
+    one); state [slots, channels, states] fp32, slots and resume int32
+    [sequences]."""
+    import torch
+    tokens, channels = u.shape
+    device = u.device
+    states = a.shape[-1]
+    count, offsets_at = _sequences(sequences, offsets, device)
+    state_at, state_slots, slots_at, resume_at = _state(
+        state, (channels, states), torch.float32, count, slots, resume, device)
+    if y is None:
+        y = _like(stream, u)
+    _check(load().lstm_selective_scan(
+        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
+        tokens, channels, states, groups, count, offsets_at, state_at, state_slots, slots_at,
+        resume_at, y.data_ptr(), _matrix("y", y, tokens, channels, u), _stream(stream, device)))
+    return y
+
+
+def lstm_selective_scan_step(u, dt, a, b, c, state, *, skip=None, z=None, dt_bias=None,
+                             softplus: bool = True, groups: int = 1, slots=None, y=None,
+                             stream=None):
+    """The next token of every sequence, u, dt, z [sequences, channels]; returns
+    y (new unless given) and moves the state on.  Arguments as
+    lstm_selective_scan."""
+    import torch
+    sequences, channels = u.shape
+    device = u.device
+    states = a.shape[-1]
+    state_at, state_slots, slots_at, _ = _state(
+        state, (channels, states), torch.float32, sequences, slots, None, device)
+    if y is None:
+        y = _like(stream, u)
+    _check(load().lstm_selective_scan_step(
+        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
+        sequences, channels, states, groups, state_at, state_slots, slots_at, y.data_ptr(),
+        _matrix("y", y, sequences, channels, u), _stream(stream, device)))
+    return y
+
+
+def lstm_residual_rms_norm(x, weight, eps: float, *, residual=None, residual_out=None,
+                           quantize: bool = False, group: int = 0, y=None, scales=None,
+                           stream=None):
+    """RMS norm of v = x + residual (x alone without one); returns
+    (y, scales, v).
+
+    y has x's type, or with quantize torch.float8_e4m3fn, and then scales
+    [rows, ceil(cols / group)] fp32 (group 0: one a row) make y * scales stand
+    for the norm; else scales is None.  v is rounded to x's type (residual_out:
+    where to, may be residual); None without a residual."""
+    import torch
+    rows, cols = x.shape
+    device = x.device
+    dtype = _element_type(x)
+    res_at = out_at = None
+    res_stride = out_stride = 0
+    if residual is not None:
+        res_at, res_stride = residual.data_ptr(), _matrix("residual", residual, rows, cols, x)
+        if residual_out is None:
+            residual_out = _like(stream, x)
+        out_at = residual_out.data_ptr()
+        out_stride = _matrix("residual_out", residual_out, rows, cols, x)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if y is None:
+        y = _empty(stream, x.shape, torch.float8_e4m3fn if quantize else x.dtype, device)
+    if quantize:
+        width = -(-cols // group) if group > 0 else 1
+        if scales is None:
+            scales = _empty(stream, (rows, width), torch.float32, device)
+        if y.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"y is {y.dtype}, expected {torch.float8_e4m3fn}")
+        y_stride = _matrix("y", y, rows, cols, y)
+        scales_at = _dense("scales", scales, (rows, width), torch.float32, device)
+    else:
+        y_stride, scales, scales_at = _matrix("y", y, rows, cols, x), None, None
+    _check(load().lstm_residual_rms_norm(
+        x.data_ptr(), _matrix("x", x, rows, cols, x), res_at, res_stride, dtype,
+        _dense("weight", weight, (cols,), torch.float32, device), eps, rows, cols, out_at,
+        out_stride, y.data_ptr(), y_stride, LSTM_E4M3 if quantize else dtype, scales_at, group,
+        _stream(stream, device)))
+    return y, scales, residual_out
+
+
+def lstm_token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = True, stream=None):
+    """Log probabilities of tokens (int64 [rows]) under logits [rows, vocab];
+    returns (logp, entropy, top_logp, top_ids): fp32 [rows], fp32 [rows], fp32
+    and int64 [rows, top]; None for what is not asked for."""
+    import torch
+    rows, vocab = logits.shape
+    device = logits.device
+    logp = h = top_logp = top_ids = None
+    if tokens is not None:
+        logp = _empty(stream, (rows,), torch.float32, device)
+    if entropy:
+        h = _empty(stream, (rows,), torch.float32, device)
+    if top > 0:
+        top_logp = _empty(stream, (rows, top), torch.float32, device)
+        top_ids = _empty(stream, (rows, top), torch.int64, device)
+    _check(load().lstm_token_logprobs(
+        logits.data_ptr(), _matrix("logits", logits, rows, vocab, logits), _element_type(logits),
+        rows, vocab, _dense("tokens", tokens, (rows,), torch.int64, device), _ptr(logp), _ptr(h),
+        top, _ptr(top_logp), _ptr(top_ids), _stream(stream, device)))
+    return logp, h, top_logp, top_ids

@@ -1,0 +1,270 @@
+// Residual addition and root-mean-square norm, in the input's type or in 8
+// bits (e4m3) with a scale per row or per group of columns.
+//
+//   v = x + residual,  n = v / sqrt(mean v^2 + eps) * weight
+//
+// Memory-bound: a handful of operations per element.  One pass: a block holds
+// its row in registers between the sum of squares and the outputs, so every
+// input is read once and every output written once.
+#include <cuda_fp8.h>
+
+#include "ops.cuh"
+
+namespace lstm {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr int kMaxCols = 32768;
+
+struct NormArgs {
+    const void *x;
+    long long x_stride;
+    const void *residual;
+    long long residual_stride;
+    void *residual_out;
+    long long residual_out_stride;
+    const float *weight;
+    float eps;
+    void *y;
+    long long y_stride;
+    float *scales;
+    int group;  // columns of a scale; 0: one scale a row
+    int groups;
+    int rows;
+    int cols;
+};
+
+// The sum or the largest of a block's values, in every thread.
+template <int THREADS, typename F>
+__device__ __forceinline__ float block_reduce(float v, float *scratch, F f)
+{
+    v = warp_reduce(v, f);
+    if (THREADS == 32)
+        return v;
+    __syncthreads();
+    if (threadIdx.x % 32 == 0)
+        scratch[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = scratch[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w)
+        v = f(v, scratch[w]);
+    return v;
+}
+
+// One row per block; thread t holds the vectors t, t + THREADS, ... (K of
+// them).  QUANT: 8-bit output.
+template <typename T, int V, int K, int THREADS, bool QUANT>
+__global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p)
+{
+    __shared__ float scratch[THREADS / 32];
+    extern __shared__ unsigned group_top[];  // V == 1: the groups' largest, as float bits
+    const auto sum = [](float a, float b) { return a + b; };
+    const auto top = [](float a, float b) { return fmaxf(a, b); };
+    const int row = blockIdx.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
+    const T *res = static_cast<const T *>(p.residual) + row * p.residual_stride;
+    T *res_out = static_cast<T *>(p.residual_out) + row * p.residual_out_stride;
+    float v[K][V];
+    float squares = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * THREADS + threadIdx.x) * V;
+        if (c < p.cols) {
+            unpack<T, V>(load_pack<T, V>(x + c), v[k]);
+            if (p.residual) {
+                float r[V];
+                // (residual_out may be residual: not through the read-only path)
+                unpack<T, V>(*reinterpret_cast<const Pack<T, V> *>(res + c), r);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    v[k][i] += r[i];
+                store_pack<T, V>(res_out + c, pack<T, V>(v[k]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[k][i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            squares = fmaf(v[k][i], v[k][i], squares);
+    }
+    squares = block_reduce<THREADS>(squares, scratch, sum);
+    const float norm = rsqrtf(squares / p.cols + p.eps);
+    float most[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * THREADS + threadIdx.x) * V;
+        most[k] = 0.0f;
+        if (c < p.cols) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k][i] = v[k][i] * norm * __ldg(p.weight + c + i);
+                most[k] = fmaxf(most[k], fabsf(v[k][i]));
+            }
+        }
+    }
+    if constexpr (!QUANT) {
+        T *y = static_cast<T *>(p.y) + row * p.y_stride;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * THREADS + threadIdx.x) * V;
+            if (c < p.cols)
+                store_pack<T, V>(y + c, pack<T, V>(v[k]));
+        }
+        return;
+    }
+    if (p.group == 0) {
+#pragma unroll
+        for (int k = 1; k < K; ++k)
+            most[0] = fmaxf(most[0], most[k]);
+        most[0] = block_reduce<THREADS>(most[0], scratch, top);
+#pragma unroll
+        for (int k = 1; k < K; ++k)
+            most[k] = most[0];
+    } else if (V > 1) {
+        // group / V consecutive lanes hold a group
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            for (int m = p.group / V / 2; m; m >>= 1)
+                most[k] = fmaxf(most[k], __shfl_xor_sync(0xffffffffu, most[k], m));
+    } else {
+        // a warp's 32 columns lie in one group; the order of the maxima does
+        // not change the result
+        for (int g = threadIdx.x; g < p.groups; g += THREADS)
+            group_top[g] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float m = warp_reduce(most[k], top);
+            const int c = k * THREADS + threadIdx.x;
+            if (threadIdx.x % 32 == 0 && c < p.cols)
+                atomicMax(group_top + c / p.group, __float_as_uint(m));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = k * THREADS + threadIdx.x;
+            if (c < p.cols)
+                most[k] = __uint_as_float(group_top[c / p.group]);
+        }
+    }
+    __nv_fp8_storage_t *y = static_cast<__nv_fp8_storage_t *>(p.y) + row * p.y_stride;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * THREADS + threadIdx.x) * V;
+        if (c >= p.cols)
+            continue;
+        const float scale = most[k] > 0.0f ? fmaxf(most[k] / kE4m3Max, 0x1p-126f) : 1.0f;
+        const float inverse = 1.0f / scale;
+        Pack<__nv_fp8_storage_t, V> q;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            q.v[i] = __nv_cvt_float_to_fp8(v[k][i] * inverse, __NV_SATFINITE, __NV_E4M3);
+        store_pack(y + c, q);
+        const int group = p.group ? p.group : p.cols;
+        if (c % group == 0)
+            p.scales[static_cast<long long>(row) * p.groups + c / group] = scale;
+    }
+}
+
+template <typename T, int V, int K, int THREADS>
+int launch(const NormArgs &p, bool quant, cudaStream_t stream)
+{
+    const int st = check_launch_injection("lstm_residual_rms_norm");
+    if (st != LSTM_OK)
+        return st;
+    const size_t shared = V == 1 && quant && p.group ? p.groups * sizeof(unsigned) : 0;
+    if (quant)
+        norm_kernel<T, V, K, THREADS, true><<<p.rows, THREADS, shared, stream>>>(p);
+    else
+        norm_kernel<T, V, K, THREADS, false><<<p.rows, THREADS, shared, stream>>>(p);
+    return cuda_status(cudaGetLastError(), "lstm_residual_rms_norm launch");
+}
+
+template <typename T, int V>
+int launch_sized(const NormArgs &p, bool quant, cudaStream_t stream)
+{
+    const int vectors = (p.cols + V - 1) / V;
+    if (vectors <= 128)
+        return launch<T, V, 1, 128>(p, quant, stream);
+    if (vectors <= 512)
+        return launch<T, V, 2, 256>(p, quant, stream);
+    if (vectors <= 2048)
+        return launch<T, V, 4, 512>(p, quant, stream);
+    if (vectors <= 8192)
+        return launch<T, V, 8, 1024>(p, quant, stream);
+    if constexpr (V == 1)
+        return launch<T, V, 32, 1024>(p, quant, stream);
+    return fail(LSTM_E_INVALID, "lstm_residual_rms_norm: %d columns", p.cols);
+}
+
+template <typename T>
+int launch_typed(const NormArgs &p, bool quant, cudaStream_t stream)
+{
+    constexpr int V = Elem<T>::kVector;
+    const int size = sizeof(T);
+    // whole vectors where every row of every matrix starts on one; otherwise
+    // an element at a time
+    const bool wide =
+        p.cols % V == 0 && rows_aligned(p.x, p.x_stride, size) &&
+        (!p.residual || (rows_aligned(p.residual, p.residual_stride, size) &&
+                         rows_aligned(p.residual_out, p.residual_out_stride, size))) &&
+        (quant ? reinterpret_cast<uintptr_t>(p.y) % V == 0 && p.y_stride % V == 0
+               : rows_aligned(p.y, p.y_stride, size));
+    return wide ? launch_sized<T, V>(p, quant, stream) : launch_sized<T, 1>(p, quant, stream);
+}
+
+}  // namespace
+}  // namespace lstm
+
+using namespace lstm;
+
+extern "C" int lstm_residual_rms_norm(const void *x, long long x_stride, const void *residual,
+                                      long long residual_stride, int dtype, const float *weight,
+                                      float eps, int rows, int cols, void *residual_out,
+                                      long long residual_out_stride, void *y, long long y_stride,
+                                      int y_dtype, float *scales, int group, void *stream)
+{
+    const char *what = "lstm_residual_rms_norm";
+    int st;
+    if ((st = check_dtype(what, dtype)))
+        return st;
+    const bool quant = y_dtype == LSTM_E4M3;
+    if (!quant && y_dtype != dtype)
+        return fail(LSTM_E_INVALID, "%s: output type %d (%d, the input's, or %d)", what, y_dtype,
+                    dtype, LSTM_E4M3);
+    if (rows < 0 || cols <= 0 || cols > kMaxCols)
+        return fail(LSTM_E_INVALID, "%s: %d rows, %d columns (1 to %d)", what, rows, cols, kMaxCols);
+    if (quant && group != 0 && group != 32 && group != 64 && group != 128)
+        return fail(LSTM_E_INVALID, "%s: group %d (0, 32, 64 or 128)", what, group);
+    if (!(eps >= 0.0f))
+        return fail(LSTM_E_INVALID, "%s: eps %g", what, eps);
+    if (!residual != !residual_out)
+        return fail(LSTM_E_INVALID, "%s: residual and residual_out go together", what);
+    if (!weight)
+        return fail(LSTM_E_INVALID, "%s: weight is null", what);
+    if (rows == 0)
+        return LSTM_OK;
+    const int size = element_size(dtype);
+    if ((st = check_matrix(what, "x", x, x_stride, rows, cols, size)) ||
+        (st = check_matrix(what, "y", y, y_stride, rows, cols, quant ? 1 : size)) ||
+        (residual &&
+         ((st = check_matrix(what, "residual", residual, residual_stride, rows, cols, size)) ||
+          (st = check_matrix(what, "residual_out", residual_out, residual_out_stride, rows, cols,
+                             size)))) ||
+        (quant && (st = check_matrix(what, "scales", scales, 1, 1, 1, 4))))
+        return st;
+    int device = 0;
+    if ((st = op_device(x, &device)))
+        return st;
+    DeviceGuard guard(device);
+    if (!guard.ok)
+        return fail(LSTM_E_CUDA, "cannot make device %d current", device);
+    NormArgs p = {x, x_stride, residual, residual_stride, residual_out, residual_out_stride, weight,
+                  eps, y, y_stride, scales, quant ? group : 0,
+                  quant && group ? (cols + group - 1) / group : 1, rows, cols};
+    LSTM_WITH_TYPE(dtype, T,
+                   return launch_typed<T>(p, quant, static_cast<cudaStream_t>(stream)));
+}

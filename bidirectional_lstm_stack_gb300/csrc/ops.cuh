@@ -1,0 +1,241 @@
+// Helpers shared by the state-space layer's and the log probabilities'
+// kernels (conv.cu, scan.cu, norm.cu, logprobs.cu): element types and their
+// vectors, the sequences of a packed batch, the states' slots, and the
+// argument checks that the entry points of lstm_ops.h have in common.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "lstm_ops.h"
+
+namespace lstm {
+
+// ---- host: argument checks ---------------------------------------------------
+inline int element_size(int dtype) { return dtype == LSTM_F32 ? 4 : 2; }
+
+inline int check_dtype(const char *what, int dtype)
+{
+    if (dtype != LSTM_F32 && dtype != LSTM_BF16 && dtype != LSTM_F16)
+        return fail(LSTM_E_INVALID, "%s: unknown element type %d", what, dtype);
+    return LSTM_OK;
+}
+
+// A device matrix argument: element-aligned, rows of `cols` elements.
+inline int check_matrix(const char *what, const char *name, const void *p, long long stride,
+                        long long rows, long long cols, int size)
+{
+    if (!p)
+        return fail(LSTM_E_INVALID, "%s: %s is null", what, name);
+    if (reinterpret_cast<uintptr_t>(p) % size)
+        return fail(LSTM_E_INVALID, "%s: %s (%p) is not aligned to its elements", what, name, p);
+    if (rows > 1 && stride < cols)
+        return fail(LSTM_E_INVALID, "%s: %s has row stride %lld, rows of %lld", what, name, stride,
+                    cols);
+    return LSTM_OK;
+}
+
+// Whether every row of the matrix starts on a 16-byte boundary.
+inline bool rows_aligned(const void *p, long long stride, int size)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * size % 16 == 0;
+}
+
+inline int check_sequences(const char *what, int tokens, int sequences, const int *offsets)
+{
+    if (tokens < 0 || sequences < 0 || (tokens > 0 && sequences == 0))
+        return fail(LSTM_E_INVALID, "%s: %d tokens, %d sequences", what, tokens, sequences);
+    if (!offsets && sequences > 0 && tokens % sequences)
+        return fail(LSTM_E_LENGTH,
+                    "%s: %d tokens are no multiple of %d sequences (and no offsets are given)", what,
+                    tokens, sequences);
+    return LSTM_OK;
+}
+
+// The device of pointer p made ready for the library's kernels.  Remembers
+// per host thread which devices are ready, so that a call costs no lock.
+inline int op_device(const void *p, int *device)
+{
+    int st = pointer_device(p, device);
+    if (st != LSTM_OK)
+        return st;
+    thread_local unsigned long long ready = 0;
+    if (*device >= 0 && *device < 64 && (ready >> *device & 1))
+        return LSTM_OK;
+    if ((st = prepare_device(*device)) == LSTM_OK)
+        ready |= 1ull << *device;
+    return st;
+}
+
+// ---- sequences and states ------------------------------------------------------
+// The sequences of a packed batch, as lstm_ops.h describes them.
+struct Sequences {
+    const int *offsets;  // null: all of `length` rows
+    int count;
+    int length;
+    int tokens;
+};
+
+// Where each sequence keeps its state.
+struct Slots {
+    const int *slots;   // null: slot s
+    const int *resume;  // null: none goes on
+    int count;          // 0: no states
+};
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ int sequence_begin(const Sequences &q, int s)
+{
+    if (!q.offsets)
+        return s * q.length;
+    return min(max(__ldg(q.offsets + s), 0), q.tokens);
+}
+__device__ __forceinline__ int sequence_end(const Sequences &q, int s)
+{
+    if (!q.offsets)
+        return (s + 1) * q.length;
+    return min(max(__ldg(q.offsets + s + 1), sequence_begin(q, s)), q.tokens);
+}
+
+// The slot of sequence s, or -1.
+__device__ __forceinline__ int sequence_slot(const Slots &p, int s)
+{
+    if (p.count == 0)
+        return -1;
+    const int slot = p.slots ? __ldg(p.slots + s) : s;
+    return slot >= 0 && slot < p.count ? slot : -1;
+}
+__device__ __forceinline__ bool sequence_resumes(const Slots &p, int s)
+{
+    return p.resume && __ldg(p.resume + s) != 0;
+}
+
+// Sequence-aligned tiles of `tile` rows.  Sequence s owns the tile numbers
+// from base(s) = begin(s) / tile + s on: base(s + 1) - base(s) is at least
+// the tiles its rows need and at least one, so the tile numbers below
+// tiles_bound() cover every sequence, and the owner of a tile is found by
+// bisection over the offsets alone (a few numbers own no rows).  Lengths need
+// not be known on the host.
+__host__ __device__ inline long long tiles_bound(int tokens, int sequences, int tile)
+{
+    return tokens / tile + static_cast<long long>(sequences);
+}
+__device__ __forceinline__ int tile_owner(const Sequences &q, int number, int tile, int *first)
+{
+    int lo = 0, hi = q.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sequence_begin(q, mid) / tile + mid <= number)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    *first = number - (sequence_begin(q, lo) / tile + lo);
+    return lo;
+}
+
+// ---- element types ---------------------------------------------------------------
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+    static constexpr int kVector = 4;  // elements in 16 bytes
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int kVector = 8;
+    static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<__half> {
+    static constexpr int kVector = 8;
+    static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// V consecutive elements: 1, or the 16 bytes of an aligned vector.
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+    T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T *p)
+{
+    Pack<T, V> r;
+    if constexpr (V * sizeof(T) == 16)
+        *reinterpret_cast<uint4 *>(&r) = __ldg(reinterpret_cast<const uint4 *>(p));
+    else
+        r = *reinterpret_cast<const Pack<T, V> *>(p);
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, V> &r)
+{
+    *reinterpret_cast<Pack<T, V> *>(p) = r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Pack<T, V> &r, float (&f)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        f[i] = Elem<T>::get(r.v[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> pack(const float (&f)[V])
+{
+    Pack<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        r.v[i] = Elem<T>::put(f[i]);
+    return r;
+}
+
+// ---- functions ---------------------------------------------------------------------
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// v / (1 + e^-v): e^-v saturates to 0 or infinity, and the quotient by an
+// infinity is 0.
+__device__ __forceinline__ float silu(float v)
+{
+    return __fdividef(v, 1.0f + ex2(-kLog2e * v));
+}
+
+template <typename F>
+__device__ __forceinline__ float warp_reduce(float v, F f)
+{
+#pragma unroll
+    for (int m = 16; m; m >>= 1)
+        v = f(v, __shfl_xor_sync(0xffffffffu, v, m));
+    return v;
+}
+
+#endif  // __CUDACC__
+
+// Runs the statement with T as dtype's element type.
+#define LSTM_WITH_TYPE(dtype, T, ...)        \
+    do {                                     \
+        if ((dtype) == LSTM_F32) {           \
+            using T = float;                 \
+            __VA_ARGS__;                     \
+        } else if ((dtype) == LSTM_BF16) {   \
+            using T = __nv_bfloat16;         \
+            __VA_ARGS__;                     \
+        } else {                             \
+            using T = __half;                \
+            __VA_ARGS__;                     \
+        }                                    \
+    } while (0)
+
+}  // namespace lstm

@@ -1,0 +1,255 @@
+"""The selective scan over packed prompts and over single tokens against its
+float64 definition: types, numbers of channels, states and groups, lengths from
+zero to long ones, states and slots, strides, and refusals."""
+import numpy as np
+import pytest
+import torch
+
+from bidirectional_lstm_stack_gb300 import binding
+from oracle import ops as oracle
+from ops_util import DTYPES, assert_close, f64, gen, normal, slice_of, uniform
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(a):
+    return None if a is None else torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def _inputs(dtype, tokens, channels, states, groups=1, strided=False, seed=1, scale=0.5):
+    g = gen(seed)
+    t = DTYPES[dtype]
+    xz = normal(g, tokens, 2 * channels, dtype=t)
+    dbc = normal(g, tokens, 3 + 2 * groups * states, dtype=t)
+    v = {"u": xz[:, :channels], "z": xz[:, channels:],
+         "dt": normal(g, tokens, channels, scale=scale, dtype=t),
+         "b": dbc[:, 3:3 + groups * states], "c": dbc[:, 3 + groups * states:],
+         "a": -torch.exp(normal(g, channels, states)), "skip": normal(g, channels),
+         "dt_bias": normal(g, channels) - 2.0}
+    if not strided:
+        v = {k: t.contiguous() for k, t in v.items()}
+    return v
+
+
+def _check(dtype, lengths, channels, states=16, *, groups=1, pool=None, slots=None, resume=None,
+           strided=False, uniform_=False, softplus=True, without=(), seed=1, y=None, scale=0.5):
+    tokens, sequences = sum(lengths), len(lengths)
+    v = _inputs(dtype, tokens, channels, states, groups, strided, seed, scale)
+    for k in without:
+        v[k] = None
+    if not softplus:
+        v["dt"], v["dt_bias"] = v["dt"].abs() * 0.2, None
+    state = None if pool is None else normal(gen(seed + 1), pool, channels, states)
+    before = f64(state)
+    offsets = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    got = binding.lstm_selective_scan(
+        v["u"], v["dt"], v["a"], v["b"], v["c"], skip=v["skip"], z=v["z"], dt_bias=v["dt_bias"],
+        softplus=softplus, groups=groups, sequences=sequences,
+        offsets=None if uniform_ else _i32(offsets), state=state, slots=_i32(slots),
+        resume=_i32(resume), y=y)
+    ref, new, bound, new_bound = oracle.selective_scan(
+        f64(v["u"]), f64(v["dt"]), f64(v["a"]), f64(v["b"]), f64(v["c"]), f64(v["skip"]),
+        f64(v["z"]), f64(v["dt_bias"]), softplus, groups, oracle.spans(tokens, sequences, offsets),
+        before, slots, resume)
+    assert_close(got, ref, bound, dtype, "y")
+    if state is not None:
+        assert_close(state, new, new_bound, "f32", "state")
+        return state
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels", [1, 5, 32, 64, 130, 256])
+def test_one_prompt(dtype, channels):
+    _check(dtype, [41], channels)
+
+
+@pytest.mark.parametrize("states", [1, 3, 4, 8, 13, 16, 17, 32, 33, 64, 65, 100, 128])
+def test_numbers_of_states(states):
+    _check("bf16", [30], 40, states, pool=1, resume=[1])
+    _check("f32", [9, 11], 6, states, pool=2, resume=[1, 0])
+
+
+@pytest.mark.parametrize("length", [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300])
+def test_lengths(length):
+    _check("bf16", [length], 64, pool=1, resume=[1])
+    _check("f32", [length], 33, pool=1, resume=[0])
+
+
+@pytest.mark.parametrize("length", [589, 1000, 2500])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_prompts(dtype, length):
+    _check(dtype, [length], 24, pool=1, resume=[1])
+
+
+def test_long_memory():
+    # step sizes so small that the first token still counts at the last
+    _check("f32", [1500], 8, scale=0.01, pool=1, resume=[1])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels", [48, 50])
+def test_packed_prompts(dtype, channels):
+    _check(dtype, [70, 0, 1, 16, 200, 2, 0, 33], channels, pool=9, slots=[3, 0, 8, 7, 5, 1, 2, 6],
+           resume=[1, 1, 1, 0, 1, 0, 0, 1], strided=True)
+
+
+def test_many_short_prompts():
+    _check("bf16", [3, 1, 4, 1, 5, 9, 2, 6] * 12, 64, pool=96, resume=[0, 1, 1] * 32)
+
+
+def test_slots_outside_the_pool_have_no_state():
+    _check("bf16", [25, 26, 27], 40, pool=3, slots=[-1, 1, 3], resume=[1, 1, 1])
+
+
+def test_equal_lengths_without_offsets():
+    _check("f16", [50] * 6, 96, uniform_=True, pool=6, resume=[0, 1, 0, 1, 1, 1])
+
+
+@pytest.mark.parametrize("groups,channels", [(2, 64), (4, 20), (3, 99), (8, 512)])
+def test_groups(groups, channels):
+    _check("bf16", [37, 20], channels, groups=groups, pool=2, resume=[1, 1])
+
+
+@pytest.mark.parametrize("without", [("z",), ("skip",), ("dt_bias",), ("z", "skip", "dt_bias")])
+def test_without_optional_arguments(without):
+    _check("f32", [45], 64, without=without)
+
+
+def test_step_sizes_as_given():
+    _check("bf16", [45], 64, softplus=False, pool=1, resume=[1])
+
+
+def test_step_sizes_far_from_zero():
+    # softplus of large, and of very negative, arguments
+    _check("f32", [40], 32, scale=20.0)
+
+
+def test_other_rows_are_left_alone():
+    y = torch.full((20, 33), 7.0, device="cuda")
+    v = _inputs("f32", 20, 33, 16)
+    binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"], y=y,
+                                offsets=_i32([2, 9, 15]))
+    got = f64(y)
+    assert (got[:2] == 7).all() and (got[15:] == 7).all() and not (got[2:15] == 7).any()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels,states,groups", [(1, 16, 1), (40, 13, 1), (64, 16, 2),
+                                                    (2048, 16, 1), (30, 64, 3), (8, 128, 1),
+                                                    (16, 4, 1), (16, 8, 1), (9, 32, 1), (5, 2, 1)])
+@pytest.mark.parametrize("sequences", [1, 5])
+def test_step(dtype, channels, states, groups, sequences):
+    v = _inputs(dtype, sequences, channels, states, groups, strided=True)
+    state = normal(gen(8), 7, channels, states)
+    slots = [6, -1, 2, 7, 0][:sequences]
+    before = f64(state)
+    y = binding.lstm_selective_scan_step(v["u"], v["dt"], v["a"], v["b"], v["c"], state,
+                                         skip=v["skip"], z=v["z"], dt_bias=v["dt_bias"],
+                                         groups=groups, slots=_i32(slots))
+    ref, new, bound, new_bound = oracle.selective_scan(
+        f64(v["u"]), f64(v["dt"]), f64(v["a"]), f64(v["b"]), f64(v["c"]), f64(v["skip"]),
+        f64(v["z"]), f64(v["dt_bias"]), True, groups, [(s, s + 1) for s in range(sequences)],
+        before, slots, step=True)
+    assert_close(y, ref, bound, dtype, "y")
+    assert_close(state, new, new_bound, "f32", "state")
+
+
+def test_step_of_a_large_batch():
+    v = _inputs("bf16", 300, 96, 16)
+    state = normal(gen(8), 310, 96, 16)
+    slots = torch.randperm(310, generator=torch.Generator().manual_seed(1))[:300].int()
+    before = f64(state)
+    y = binding.lstm_selective_scan_step(v["u"], v["dt"], v["a"], v["b"], v["c"], state,
+                                         skip=v["skip"], z=v["z"], dt_bias=v["dt_bias"],
+                                         slots=slots.cuda())
+    ref, new, bound, new_bound = oracle.selective_scan(
+        f64(v["u"]), f64(v["dt"]), f64(v["a"]), f64(v["b"]), f64(v["c"]), f64(v["skip"]),
+        f64(v["z"]), f64(v["dt_bias"]), True, 1, [(s, s + 1) for s in range(300)], before,
+        slots.tolist(), step=True)
+    assert_close(y, ref, bound, "bf16", "y")
+    assert_close(state, new, new_bound, "f32", "state")
+
+
+def test_prompt_in_parts_and_steps_goes_on_from_its_state():
+    v = _inputs("f32", 90, 48, 16)
+    call = lambda a, b, **k: binding.lstm_selective_scan(
+        v["u"][a:b], v["dt"][a:b], v["a"], v["b"][a:b], v["c"][a:b], skip=v["skip"], z=v["z"][a:b],
+        dt_bias=v["dt_bias"], **k)
+    state, last = torch.empty(1, 48, 16, device="cuda"), torch.empty(1, 48, 16, device="cuda")
+    whole = call(0, 90, state=last)
+    one = _i32([1])
+    parts = [call(0, 33, state=state), call(33, 80, state=state, resume=one)]
+    for t in range(80, 90):
+        parts.append(binding.lstm_selective_scan_step(
+            v["u"][t:t + 1], v["dt"][t:t + 1], v["a"], v["b"][t:t + 1], v["c"][t:t + 1], state,
+            skip=v["skip"], z=v["z"][t:t + 1], dt_bias=v["dt_bias"]))
+    ref, new, bound, new_bound = oracle.selective_scan(
+        *(f64(v[k]) for k in ("u", "dt", "a", "b", "c", "skip", "z", "dt_bias")), True, 1,
+        [(0, 90)], np.zeros((1, 48, 16)))
+    for got, s in ((whole, last), (torch.cat(parts), state)):
+        assert_close(got, ref, bound, "f32")
+        assert_close(s, new, new_bound, "f32")
+
+
+def test_the_same_bits_every_time_and_on_another_stream():
+    v = _inputs("bf16", 700, 64, 16)
+    call = lambda **k: binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"],
+                                                   skip=v["skip"], z=v["z"], **k)
+    ref = call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (None, s, s.cuda_stream):
+        y = call(stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+
+
+def test_in_a_graph():
+    v = _inputs("bf16", 200, 64, 16)
+    state = torch.zeros(1, 64, 16, device="cuda")
+    y = torch.empty_like(v["u"])
+    call = lambda: binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"], state=state,
+                                               resume=one, y=y)
+    one = _i32([1])
+    call()
+    first, after = y.clone(), state.clone()
+    call()
+    second, twice = y.clone(), state.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    state.zero_()
+    graph.replay()
+    assert torch.equal(y, first) and torch.equal(state, after)
+    graph.replay()
+    assert torch.equal(y, second) and torch.equal(state, twice)
+
+
+def test_refusals():
+    v = _inputs("f32", 12, 16, 8)
+
+    def run(**k):
+        first = [k.pop(n, v[n]) for n in ("u", "dt", "a", "b", "c")]
+        return binding.lstm_selective_scan(*first, **k)
+
+    z = lambda *s: torch.zeros(*s, device="cuda")
+    with pytest.raises(binding.LSTMError) as e:
+        run(a=z(16, 129), b=z(12, 129), c=z(12, 129))
+    assert e.value.code == binding.LSTM_E_INVALID
+    with pytest.raises(binding.LSTMError) as e:
+        run(groups=3, b=z(12, 24), c=z(12, 24))
+    assert e.value.code == binding.LSTM_E_INVALID
+    with pytest.raises(binding.LSTMError) as e:
+        run(sequences=5)
+    assert e.value.code == binding.LSTM_E_LENGTH
+    for bad in (dict(u=v["u"].half()), dict(dt=z(12, 15)), dict(dt=z(11, 16)), dict(a=z(15, 8)),
+                dict(a=z(16, 8).double()), dict(b=z(12, 9)), dict(c=v["c"].bfloat16()),
+                dict(z=z(12, 17)), dict(skip=z(17)), dict(dt_bias=z(16).half()),
+                dict(groups=2), dict(state=z(1, 16, 9)), dict(state=z(1, 16, 8).half()),
+                dict(state=z(1, 16, 8), sequences=2), dict(slots=_i32([0])),
+                dict(state=z(1, 16, 8), slots=_i32([0, 1])), dict(offsets=_i32([0, 12]).long()),
+                dict(y=z(12, 15)), dict(a=z(16, 8).cpu())):
+        with pytest.raises(ValueError):
+            run(**bad)
+    with pytest.raises(ValueError):
+        binding.lstm_selective_scan_step(v["u"], v["dt"], v["a"], v["b"], v["c"], z(2, 16, 8))
