@@ -114,7 +114,9 @@ def load():
             "lstm_causal_conv_step": (i, [_vp, ll, i, i, i, i, _vp, _vp, i, _vp, i, _vp, _vp, ll,
                                           _vp]),
             "lstm_selective_scan": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll, _vp,
-                                        i, i, i, i, i, i, i, _vp, _vp, i, _vp, _vp, _vp, ll, _vp]),
+                                        i, i, i, i, i, i, i, _vp, _vp, i, _vp, _vp, _vp, ll, _vp, sz,
+                                        _vp]),
+            "lstm_selective_scan_workspace": (sz, [i, i, i, i, i]),
             "lstm_selective_scan_step": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll,
                                              _vp, i, i, i, i, i, i, _vp, i, _vp, _vp, ll, _vp]),
             "lstm_residual_rms_norm": (i, [_vp, ll, _vp, ll, i, _vp, f, i, i, _vp, ll, _vp, ll, i,
@@ -573,11 +575,22 @@ def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, soft
         state, (channels, states), torch.float32, count, slots, resume, device)
     if y is None:
         y = _like(stream, u)
-    _check(load().lstm_selective_scan(
+    lib = load()
+    size = lib.lstm_selective_scan_workspace(tokens, channels, states, count, offsets is None)
+    workspace = _empty(stream, (size,), torch.uint8, device) if size else None
+    _check(lib.lstm_selective_scan(
         *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
         tokens, channels, states, groups, count, offsets_at, state_at, state_slots, slots_at,
-        resume_at, y.data_ptr(), _matrix("y", y, tokens, channels, u), _stream(stream, device)))
+        resume_at, y.data_ptr(), _matrix("y", y, tokens, channels, u), _ptr(workspace), size,
+        _stream(stream, device)))
     return y
+
+
+def lstm_selective_scan_workspace(tokens: int, channels: int, states: int, sequences: int,
+                                  equal_lengths: bool) -> int:
+    """Bytes of workspace of lstm_selective_scan."""
+    return load().lstm_selective_scan_workspace(tokens, channels, states, sequences,
+                                                int(equal_lengths))
 
 
 def lstm_selective_scan_step(u, dt, a, b, c, state, *, skip=None, z=None, dt_bias=None,

@@ -7,6 +7,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "lstm_ops.h"
 
@@ -67,6 +69,28 @@ inline int op_device(const void *p, int *device)
         ready |= 1ull << *device;
     return st;
 }
+
+// Remembers on which devices a kernel may use more dynamic shared memory than
+// 48 KiB.
+struct SharedMemory {
+    std::atomic<unsigned long long> done{0};
+    template <typename K>
+    int allow(K kernel, size_t bytes)
+    {
+        if (bytes <= 48 * 1024)
+            return LSTM_OK;
+        int device = 0;
+        int st = cuda_status(cudaGetDevice(&device), "current device");
+        if (st != LSTM_OK || (done.load() >> device & 1))
+            return st;
+        st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(bytes)),
+                         "shared memory attribute");
+        if (st == LSTM_OK)
+            done.fetch_or(1ull << device);
+        return st;
+    }
+};
 
 // ---- sequences and states ------------------------------------------------------
 // The sequences of a packed batch, as lstm_ops.h describes them.

@@ -54,82 +54,304 @@ __device__ __forceinline__ float softplus(float v)
 }
 
 constexpr int kThreads = 128;
-constexpr int kStates = 16;  // states a thread holds
-constexpr int kTile = 16;    // tokens whose b and c are staged together
 
-// grid (channel blocks of a group * groups, sequences).  G lanes share a
-// channel, each with kStates of its states.
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) scan_kernel(ScanArgs p)
+// Two fp32 numbers in one 64-bit register: the paired operations do two
+// roundings each in one issue slot.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair make_pair(float x, float y)
 {
-    constexpr int kPadded = kStates * G;
-    __shared__ __align__(16) float sb[kTile][kPadded], sc[kTile][kPadded];
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split_pair(Pair p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair ex2_pair(Pair p)
+{
+    const float2 v = split_pair(p);
+    return make_pair(ex2(v.x), ex2(v.y));
+}
+
+// ---- prompts --------------------------------------------------------------------
+constexpr int kTile = 16;  // tokens staged together
+constexpr int kStep = 4;   // of them computed together
+
+// Spans of `chunk` tokens (chunk tiles, in tile_owner's numbering), and what
+// the first pass leaves for the second: per span, channel and state, the
+// state after the span when it starts from zeros (the sequence's first span:
+// from its own start), and the sum of the span's step sizes.  A sequence's
+// last span has nothing to leave; its place holds the state that the sequence
+// starts from, which the second pass may not read where it is kept, because
+// the last span replaces it.
+struct Spans {
+    int chunk;
+    float *states;  // [numbers][channels][padded]
+    float *sums;    // [numbers][channels]
+};
+
+template <typename T, int CH, int PADDED, bool GATE>
+struct alignas(16) Stage {
+    T u[kTile][CH];
+    T dt[kTile][CH];
+    T z[GATE ? kTile : 1][CH];
+    float b[kTile][PADDED];
+    float c[GATE ? kTile : 1][PADDED];
+};
+
+// grid (span numbers, channel blocks of a group * groups).  G lanes share a
+// channel, each with NS of its states.  FINAL false: the first pass, over the
+// spans that others follow.
+template <typename T, int NS, int G, bool WIDE, bool FINAL>
+__global__ void __launch_bounds__(kThreads) scan_kernel(ScanArgs p, Spans w)
+{
+    constexpr int kChannels = kThreads / G;
+    constexpr int kPadded = NS * G;
+    constexpr int kFetch = kTile * kPadded / kThreads;  // of b, and of c, a thread's share
+    constexpr int V = Elem<T>::kVector;
+    extern __shared__ __align__(16) unsigned char shared[];
+    typedef Stage<T, kChannels, kPadded, FINAL> StageT;
+    StageT *stages = reinterpret_cast<StageT *>(shared);
+
+    if (!FINAL)
+        ptx::griddep_launch_dependents();
+    const int number = blockIdx.x;
+    int span;
+    const int s = tile_owner(p.seq, number, w.chunk, &span);
+    const int seq_begin = sequence_begin(p.seq, s), seq_end = sequence_end(p.seq, s);
+    const int length = seq_end - seq_begin;
+    const int spans = length > 0 ? (length - 1) / w.chunk + 1 : 1;  // (one to keep the state)
+    if (span < 0 || span >= spans || (!FINAL && spans == 1)) {
+        if (FINAL)  // what follows this kernel must not overtake the first pass
+            ptx::griddep_wait();
+        return;
+    }
+    const bool last = span == spans - 1;
+    const int begin = seq_begin + span * w.chunk;
+    const int end = last ? seq_end : begin + w.chunk;
+
     const int per_group = p.channels / p.groups;
-    const int blocks = (per_group + kThreads / G - 1) / (kThreads / G);
-    const int group = blockIdx.x / blocks;
-    const int local = (blockIdx.x % blocks) * (kThreads / G) + threadIdx.x / G;
-    const bool live = local < per_group;
-    const int d = group * per_group + (live ? local : 0);
-    const int n0 = threadIdx.x % G * kStates;
-    const int s = blockIdx.y;
-    const int begin = sequence_begin(p.seq, s), end = sequence_end(p.seq, s);
+    const int blocks = (per_group + kChannels - 1) / kChannels;
+    const int group = blockIdx.y / blocks;
+    const int local0 = (blockIdx.y % blocks) * kChannels;
+    const int here = min(kChannels, per_group - local0);  // channels of this block
+    const int c0 = group * per_group + local0;
+    const int ch = threadIdx.x / G;
+    const bool live = ch < here;
+    const int d = c0 + (live ? ch : 0);
+    const int n0 = threadIdx.x % G * NS;
     const int slot = sequence_slot(p.slots, s);
     float *state = slot < 0 ? nullptr
                             : p.state + (static_cast<long long>(slot) * p.channels + d) * p.states;
     const bool resumes = state && sequence_resumes(p.slots, s);
-    float h[kStates], a[kStates];
+    const long long first = number - span;  // the sequence's first span number
+    float *kept = w.states + (static_cast<long long>(number) * p.channels + d) * kPadded + n0;
+
+    Pair h[NS / 2], a[NS / 2];
+    const float *from = p.a + static_cast<long long>(d) * p.states;
 #pragma unroll
-    for (int n = 0; n < kStates; ++n) {
-        const bool in = n0 + n < p.states;
-        h[n] = resumes && in ? state[n0 + n] : 0.0f;
-        a[n] = in ? kLog2e * __ldg(p.a + static_cast<long long>(d) * p.states + n0 + n) : 0.0f;
+    for (int n = 0; n < NS; n += 2) {
+        const int k = n0 + n;
+        a[n / 2] = make_pair(k < p.states ? kLog2e * __ldg(from + k) : 0.0f,
+                             k + 1 < p.states ? kLog2e * __ldg(from + k + 1) : 0.0f);
+        h[n / 2] = 0;
     }
-    const float skip = p.skip ? __ldg(p.skip + d) : 0.0f;
-    const float dt_bias = p.dt_bias ? __ldg(p.dt_bias + d) : 0.0f;
-    const T *u = static_cast<const T *>(p.u) + d;
-    const T *dt = static_cast<const T *>(p.dt) + d;
-    const T *z = p.z ? static_cast<const T *>(p.z) + d : nullptr;
+    const auto start_from_state = [&]() {
+#pragma unroll
+        for (int n = 0; n < NS; n += 2) {
+            const int k = n0 + n;
+            h[n / 2] = make_pair(k < p.states ? state[k] : 0.0f,
+                                 k + 1 < p.states ? state[k + 1] : 0.0f);
+        }
+    };
+    if (!FINAL && last) {  // nothing follows: keep the sequence's start
+        if (resumes && live) {
+            start_from_state();
+#pragma unroll
+            for (int n = 0; n < NS / 2; n += 2)
+                *reinterpret_cast<ulonglong2 *>(kept + 2 * n) = make_ulonglong2(h[n], h[n + 1]);
+        }
+        return;
+    }
+
+    // staging: u, dt and z as they are, asynchronously; b and c as fp32
+    const T *u = static_cast<const T *>(p.u) + c0;
+    const T *dt = static_cast<const T *>(p.dt) + c0;
+    const T *z = FINAL && p.z ? static_cast<const T *>(p.z) + c0 : nullptr;
     const T *b = static_cast<const T *>(p.b) + group * p.states;
     const T *c = static_cast<const T *>(p.c) + group * p.states;
-    T *y = static_cast<T *>(p.y) + d;
-    for (int t0 = begin; t0 < end; t0 += kTile) {
+    T fetch_b[kFetch], fetch_c[kFetch];
+    const auto fetch = [&](int t0, StageT &st) {
         const int count = min(kTile, end - t0);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kTile * kPadded; i += kThreads) {
-            const int t = i / kPadded, n = i % kPadded;
-            const bool in = t < count && n < p.states;
-            sb[t][n] = in ? Elem<T>::get(b[(t0 + t) * p.b_stride + n]) : 0.0f;
-            sc[t][n] = in ? Elem<T>::get(c[(t0 + t) * p.c_stride + n]) : 0.0f;
+        if (WIDE) {
+            constexpr int kRow = kChannels / V > 0 ? kChannels / V : 1;
+            for (int i = threadIdx.x; i < count * kRow; i += kThreads) {
+                const int t = i / kRow, at = i % kRow * V;
+                if (at < here) {
+                    ptx::cp_async_16(ptx::smem_u32(&st.u[t][at]), u + (t0 + t) * p.u_stride + at, 16);
+                    ptx::cp_async_16(ptx::smem_u32(&st.dt[t][at]), dt + (t0 + t) * p.dt_stride + at,
+                                     16);
+                    if (z)
+                        ptx::cp_async_16(ptx::smem_u32(&st.z[t][at]), z + (t0 + t) * p.z_stride + at,
+                                         16);
+                }
+            }
+            ptx::cp_async_commit();
+        } else {
+            for (int i = threadIdx.x; i < count * kChannels; i += kThreads) {
+                const int t = i / kChannels, at = i % kChannels;
+                if (at < here) {
+                    st.u[t][at] = u[(t0 + t) * p.u_stride + at];
+                    st.dt[t][at] = dt[(t0 + t) * p.dt_stride + at];
+                    if (z)
+                        st.z[t][at] = z[(t0 + t) * p.z_stride + at];
+                }
+            }
         }
-        __syncthreads();
-        for (int t = 0; t < count; ++t) {
-            const float ut = Elem<T>::get(u[(t0 + t) * p.u_stride]);
-            float st = Elem<T>::get(dt[(t0 + t) * p.dt_stride]) + dt_bias;
-            if (p.softplus)
-                st = softplus(st);
-            const float su = st * ut;
-            float v = 0.0f;
 #pragma unroll
-            for (int n = 0; n < kStates; ++n) {
-                h[n] = fmaf(ex2(st * a[n]), h[n], su * sb[t][n0 + n]);
-                v = fmaf(h[n], sc[t][n0 + n], v);
+        for (int k = 0; k < kFetch; ++k) {
+            const int i = k * kThreads + threadIdx.x, t = i / kPadded, n = i % kPadded;
+            const bool in = t < count && n < p.states;
+            fetch_b[k] = in ? b[(t0 + t) * p.b_stride + n] : Elem<T>::put(0.0f);
+            if (FINAL)
+                fetch_c[k] = in ? c[(t0 + t) * p.c_stride + n] : Elem<T>::put(0.0f);
+        }
+    };
+    const auto settle = [&](StageT &st) {
+#pragma unroll
+        for (int k = 0; k < kFetch; ++k) {
+            const int i = k * kThreads + threadIdx.x, t = i / kPadded, n = i % kPadded;
+            st.b[t][n] = Elem<T>::get(fetch_b[k]);
+            if (FINAL)
+                st.c[t][n] = Elem<T>::get(fetch_c[k]);
+        }
+        if (WIDE)
+            ptx::cp_async_wait_all();
+        __syncthreads();
+    };
+
+    int stage = 0;
+    if (begin < end)
+        fetch(begin, stages[0]);
+    const float skip = p.skip ? __ldg(p.skip + d) : 0.0f;
+    const float dt_bias = p.dt_bias ? __ldg(p.dt_bias + d) : 0.0f;
+    T *y = FINAL ? static_cast<T *>(p.y) + d : nullptr;
+    if (FINAL)
+        ptx::griddep_wait();
+    if (FINAL && spans > 1) {
+        // the state that this span starts from: every earlier span carries
+        // the state before it on by e^(a * its step sizes' sum)
+        if (span == 0) {
+            if (resumes) {
+                const float *start =
+                    w.states + ((first + spans - 1) * p.channels + d) * kPadded + n0;
+#pragma unroll
+                for (int n = 0; n < NS; n += 2)
+                    h[n / 2] = *reinterpret_cast<const Pair *>(start + n);
+            }
+        } else {
+            const float *sum = w.sums + first * p.channels + d;
+            const float *left = w.states + (first * p.channels + d) * kPadded + n0;
+            for (int k = 0; k < span; ++k) {
+                const float total = *sum;
+                const Pair by = make_pair(total, total);
+#pragma unroll
+                for (int n = 0; n < NS; n += 2)
+                    h[n / 2] = fma2(ex2_pair(mul2(by, a[n / 2])), h[n / 2],
+                                    *reinterpret_cast<const Pair *>(left + n));
+                sum += p.channels;
+                left += static_cast<long long>(p.channels) * kPadded;
+            }
+        }
+    } else if (resumes && span == 0) {
+        start_from_state();
+    }
+
+    float sum = 0.0f;
+    for (int t0 = begin; t0 < end; t0 += kTile) {
+        StageT &st = stages[stage];
+        settle(st);
+        if (t0 + kTile < end)
+            fetch(t0 + kTile, stages[stage ^ 1]);
+        stage ^= 1;
+        const int count = min(kTile, end - t0);
+#pragma unroll 1
+        for (int t = 0; t < count; t += kStep) {
+            float step[kStep], add[kStep], in[kStep];
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+                const bool real = t + j < count;  // (others change nothing)
+                in[j] = Elem<T>::get(st.u[t + j][ch]);
+                float v = Elem<T>::get(st.dt[t + j][ch]) + dt_bias;
+                if (p.softplus)
+                    v = softplus(v);
+                step[j] = real ? v : 0.0f;
+                add[j] = real ? v * in[j] : 0.0f;
+                sum += step[j];
             }
 #pragma unroll
-            for (int m = 1; m < G; m <<= 1)
-                v += __shfl_xor_sync(0xffffffffu, v, m);
-            if (live && n0 == 0) {
-                v = fmaf(skip, ut, v);
-                if (z)
-                    v *= silu(Elem<T>::get(z[(t0 + t) * p.z_stride]));
-                y[(t0 + t) * p.y_stride] = Elem<T>::put(v);
+            for (int j = 0; j < kStep; ++j) {
+                const Pair by = make_pair(step[j], step[j]), plus = make_pair(add[j], add[j]);
+                Pair out = 0;
+#pragma unroll
+                for (int n = 0; n < NS / 2; n += 2) {
+                    const ulonglong2 bn = *reinterpret_cast<const ulonglong2 *>(&st.b[t + j][n0 + 2 * n]);
+                    h[n] = fma2(ex2_pair(mul2(by, a[n])), h[n], mul2(plus, bn.x));
+                    h[n + 1] = fma2(ex2_pair(mul2(by, a[n + 1])), h[n + 1], mul2(plus, bn.y));
+                    if (FINAL) {
+                        const ulonglong2 cn =
+                            *reinterpret_cast<const ulonglong2 *>(&st.c[t + j][n0 + 2 * n]);
+                        out = fma2(h[n], cn.x, out);
+                        out = fma2(h[n + 1], cn.y, out);
+                    }
+                }
+                if (FINAL) {
+                    const float2 halves = split_pair(out);
+                    float v = halves.x + halves.y;
+#pragma unroll
+                    for (int m = 1; m < G; m <<= 1)
+                        v += __shfl_xor_sync(0xffffffffu, v, m);
+                    v = fmaf(skip, in[j], v);
+                    if (z)
+                        v *= silu(Elem<T>::get(st.z[t + j][ch]));
+                    if (t + j < count && live && n0 == 0)
+                        y[(t0 + t + j) * p.y_stride] = Elem<T>::put(v);
+                }
             }
         }
     }
-    if (state && live) {
+    if (!live)
+        return;
+    if (!FINAL) {
 #pragma unroll
-        for (int n = 0; n < kStates; ++n)
+        for (int n = 0; n < NS / 2; n += 2)
+            *reinterpret_cast<ulonglong2 *>(kept + 2 * n) = make_ulonglong2(h[n], h[n + 1]);
+        if (n0 == 0)
+            w.sums[static_cast<long long>(number) * p.channels + d] = sum;
+    } else if (last && state) {
+#pragma unroll
+        for (int n = 0; n < NS; n += 2) {
+            const float2 v = split_pair(h[n / 2]);
             if (n0 + n < p.states)
-                state[n0 + n] = h[n];
+                state[n0 + n] = v.x;
+            if (n0 + n + 1 < p.states)
+                state[n0 + n + 1] = v.y;
+        }
     }
 }
 
@@ -228,24 +450,108 @@ int launch_step(const ScanArgs &p, cudaStream_t stream)
     return cuda_status(cudaGetLastError(), "lstm_selective_scan_step launch");
 }
 
-template <typename T, int G>
-int launch_prompts(const ScanArgs &p, cudaStream_t stream)
+// How a call's prompts are worked on: the same for its workspace's size and
+// for its launches.
+struct Plan {
+    int states;       // a thread's
+    int lanes;        // a channel's
+    int chunk;        // tokens of a span
+    long long spans;  // span numbers
+    bool split;       // whether a sequence may have several spans
+    size_t bytes;     // of workspace
+};
+
+Plan make_plan(int tokens, int channels, int states, int sequences, bool equal)
 {
+    Plan r;
+    r.states = states <= 8 ? 8 : 16;
+    r.lanes = 1;
+    while (r.states * r.lanes < states)
+        r.lanes *= 2;
+    // Splitting sequences into spans reads them twice and takes their
+    // exponentials twice, so it pays where the sequences alone leave the
+    // machine empty.
+    const long long threads = static_cast<long long>(channels) * r.lanes;
+    const long long wanted = 152 * 256;
+    long long chunk = tokens;
+    if (sequences * threads < wanted) {
+        chunk = tokens * threads / wanted;
+        chunk = (chunk + kTile - 1) / kTile * kTile;
+        if (chunk < 2 * kTile)
+            chunk = 2 * kTile;
+    }
+    const long long longest = equal ? tokens / (sequences > 0 ? sequences : 1) : tokens;
+    r.split = chunk < longest;
+    // whole sequences: spans longer than all tokens together number just them
+    r.chunk = r.split ? static_cast<int>(chunk) : tokens + 1;
+    r.spans = r.split ? tiles_bound(tokens, sequences, r.chunk) : sequences;
+    r.bytes = r.split ? static_cast<size_t>(r.spans) * channels * (r.states * r.lanes + 1) * 4 : 0;
+    return r;
+}
+
+template <typename T, int NS, int G, bool WIDE>
+int launch_prompts(const ScanArgs &p, const Plan &plan, void *workspace, cudaStream_t stream)
+{
+    constexpr int kChannels = kThreads / G;
     const int per_group = p.channels / p.groups;
     const long long blocks =
-        static_cast<long long>((per_group + kThreads / G - 1) / (kThreads / G)) * p.groups;
-    if (p.seq.count > 65535 || blocks > 0x7fffffffll)
-        return fail(LSTM_E_OVERFLOW, "lstm_selective_scan: %d sequences, %d channels", p.seq.count,
-                    p.channels);
-    const int st = check_launch_injection("lstm_selective_scan");
-    if (st != LSTM_OK)
+        static_cast<long long>((per_group + kChannels - 1) / kChannels) * p.groups;
+    if (plan.spans > 0x7fffffffll || blocks > 65535)
+        return fail(LSTM_E_OVERFLOW, "lstm_selective_scan: %d sequences, %d tokens, %d channels",
+                    p.seq.count, p.seq.tokens, p.channels);
+    Spans w = {plan.chunk, static_cast<float *>(workspace), nullptr};
+    w.sums = w.states + plan.spans * p.channels * NS * G;
+    const dim3 grid(static_cast<unsigned>(plan.spans), static_cast<unsigned>(blocks));
+    constexpr size_t kShared = 2 * sizeof(Stage<T, kChannels, NS * G, true>);
+    constexpr size_t kSharedFirst = 2 * sizeof(Stage<T, kChannels, NS * G, false>);
+    static SharedMemory allowed, allowed_first;
+    int st;
+    if ((st = allowed.allow(scan_kernel<T, NS, G, WIDE, true>, kShared)) ||
+        (st = allowed_first.allow(scan_kernel<T, NS, G, WIDE, false>, kSharedFirst)))
         return st;
-    scan_kernel<T, G><<<dim3(static_cast<unsigned>(blocks), p.seq.count), kThreads, 0, stream>>>(p);
-    return cuda_status(cudaGetLastError(), "lstm_selective_scan launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    if (plan.split) {
+        if ((st = check_launch_injection("lstm_selective_scan")))
+            return st;
+        cfg.dynamicSmemBytes = kSharedFirst;
+        if ((st = cuda_status(cudaLaunchKernelEx(&cfg, scan_kernel<T, NS, G, WIDE, false>, p, w),
+                              "lstm_selective_scan launch")))
+            return st;
+    }
+    if ((st = check_launch_injection("lstm_selective_scan")))
+        return st;
+    cfg.dynamicSmemBytes = kShared;
+    // the second pass may start while the first one ends; it waits for it
+    // before it reads what that left
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.split ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, scan_kernel<T, NS, G, WIDE, true>, p, w),
+                       "lstm_selective_scan launch");
+}
+
+template <typename T, int NS, int G>
+int launch_aligned(const ScanArgs &p, const Plan &plan, void *workspace, cudaStream_t stream)
+{
+    constexpr int V = Elem<T>::kVector;
+    const int size = sizeof(T);
+    // 16-byte copies where every row of u, dt and z, and every group of
+    // channels, starts on a 16-byte boundary
+    const bool wide = p.channels / p.groups % V == 0 && rows_aligned(p.u, p.u_stride, size) &&
+                      rows_aligned(p.dt, p.dt_stride, size) &&
+                      (!p.z || rows_aligned(p.z, p.z_stride, size));
+    return wide ? launch_prompts<T, NS, G, true>(p, plan, workspace, stream)
+                : launch_prompts<T, NS, G, false>(p, plan, workspace, stream);
 }
 
 template <typename T>
-int launch_typed(const ScanArgs &p, bool step, cudaStream_t stream)
+int launch_typed(const ScanArgs &p, bool step, const Plan &plan, void *workspace,
+                 cudaStream_t stream)
 {
     if (step) {
         if (p.states <= 4)
@@ -260,16 +566,22 @@ int launch_typed(const ScanArgs &p, bool step, cudaStream_t stream)
             return launch_step<T, 16>(p, stream);
         return launch_step<T, 32>(p, stream);
     }
-    if (p.states <= kStates)
-        return launch_prompts<T, 1>(p, stream);
-    if (p.states <= 2 * kStates)
-        return launch_prompts<T, 2>(p, stream);
-    if (p.states <= 4 * kStates)
-        return launch_prompts<T, 4>(p, stream);
-    return launch_prompts<T, 8>(p, stream);
+    if (plan.states == 8)
+        return launch_aligned<T, 8, 1>(p, plan, workspace, stream);
+    switch (plan.lanes) {
+    case 1:
+        return launch_aligned<T, 16, 1>(p, plan, workspace, stream);
+    case 2:
+        return launch_aligned<T, 16, 2>(p, plan, workspace, stream);
+    case 4:
+        return launch_aligned<T, 16, 4>(p, plan, workspace, stream);
+    default:
+        return launch_aligned<T, 16, 8>(p, plan, workspace, stream);
+    }
 }
 
-int scan(const char *what, ScanArgs &p, int dtype, int rows, bool step, void *stream)
+int scan(const char *what, ScanArgs &p, int dtype, int rows, bool step, void *workspace,
+         size_t workspace_bytes, void *stream)
 {
     int st;
     if ((st = check_dtype(what, dtype)))
@@ -303,16 +615,37 @@ int scan(const char *what, ScanArgs &p, int dtype, int rows, bool step, void *st
         return st;
     if (p.seq.count == 0)
         return LSTM_OK;
+    Plan plan = {};
+    if (!step) {
+        plan = make_plan(rows, p.channels, p.states, p.seq.count, !p.seq.offsets);
+        if (plan.bytes > 0 && !workspace)
+            return fail(LSTM_E_INVALID, "%s: workspace is null", what);
+        if (workspace_bytes < plan.bytes)
+            return fail(LSTM_E_LENGTH, "%s: workspace has %zu bytes, needs %zu", what,
+                        workspace_bytes, plan.bytes);
+        if ((st = check_aligned(workspace, "workspace")))
+            return st;
+    }
     DeviceGuard guard(device);
     if (!guard.ok)
         return fail(LSTM_E_CUDA, "cannot make device %d current", device);
-    LSTM_WITH_TYPE(dtype, T, return launch_typed<T>(p, step, static_cast<cudaStream_t>(stream)));
+    LSTM_WITH_TYPE(dtype, T, return launch_typed<T>(p, step, plan, workspace,
+                                                    static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
 }  // namespace lstm
 
 using namespace lstm;
+
+extern "C" size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int sequences,
+                                                int equal_lengths)
+{
+    if (tokens <= 0 || channels <= 0 || states <= 0 || states > LSTM_SCAN_MAX_STATES ||
+        sequences <= 0)
+        return 0;
+    return make_plan(tokens, channels, states, sequences, equal_lengths != 0).bytes;
+}
 
 extern "C" int lstm_selective_scan(const void *u, long long u_stride, const void *dt,
                                    long long dt_stride, const float *a, const void *b,
@@ -322,7 +655,8 @@ extern "C" int lstm_selective_scan(const void *u, long long u_stride, const void
                                    int channels, int states, int groups, int sequences,
                                    const int *offsets, float *state, int state_slots,
                                    const int *slots, const int *resume, void *y,
-                                   long long y_stride, void *stream)
+                                   long long y_stride, void *workspace, size_t workspace_bytes,
+                                   void *stream)
 {
     const int st = check_sequences("lstm_selective_scan", tokens, sequences, offsets);
     if (st != LSTM_OK)
@@ -331,7 +665,8 @@ extern "C" int lstm_selective_scan(const void *u, long long u_stride, const void
                   dt_bias, softplus != 0, channels, states, groups, state,
                   {offsets, sequences, sequences ? tokens / sequences : 0, tokens},
                   {slots, resume, state_slots}, y, y_stride};
-    return scan("lstm_selective_scan", p, dtype, tokens, false, stream);
+    return scan("lstm_selective_scan", p, dtype, tokens, false, workspace, workspace_bytes,
+                stream);
 }
 
 extern "C" int lstm_selective_scan_step(const void *u, long long u_stride, const void *dt,
@@ -348,5 +683,5 @@ extern "C" int lstm_selective_scan_step(const void *u, long long u_stride, const
     ScanArgs p = {u, u_stride, dt, dt_stride, a, b, b_stride, c, c_stride, skip, z, z_stride,
                   dt_bias, softplus != 0, channels, states, groups, state,
                   {nullptr, sequences, 1, sequences}, {slots, nullptr, state_slots}, y, y_stride};
-    return scan("lstm_selective_scan_step", p, dtype, sequences, true, stream);
+    return scan("lstm_selective_scan_step", p, dtype, sequences, true, nullptr, 0, stream);
 }

@@ -100,14 +100,21 @@ int lstm_causal_conv_step(const void *x, long long x_stride, int dtype, int sequ
  *   skip, dt_bias : device [channels] fp32, or NULL for zeros
  *   state       : device [state_slots][channels][states] fp32, the h; NULL:
  *                 no states (state_slots, slots and resume are then not read)
- * Errors as lstm_causal_conv. */
+ *   workspace   : device, 16-byte aligned, workspace_bytes long and at least
+ *                 lstm_selective_scan_workspace(tokens, channels, states,
+ *                 sequences, offsets == NULL) bytes (0: may be NULL); its
+ *                 contents need not be kept between calls, but two calls that
+ *                 may run at the same time need one each
+ * Errors as lstm_causal_conv, LSTM_E_LENGTH for a workspace that is too short. */
+size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int sequences,
+                                     int equal_lengths);
 int lstm_selective_scan(const void *u, long long u_stride, const void *dt, long long dt_stride,
                         const float *a, const void *b, long long b_stride, const void *c,
                         long long c_stride, const float *skip, const void *z, long long z_stride,
                         const float *dt_bias, int softplus, int dtype, int tokens, int channels,
                         int states, int groups, int sequences, const int *offsets, float *state,
                         int state_slots, const int *slots, const int *resume, void *y,
-                        long long y_stride, void *stream);
+                        long long y_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The next token of every sequence: row s of u, dt, b, c, z and y is sequence
  * s's, and its state moves on by one token.  Arguments and errors as

@@ -22,7 +22,7 @@ def test_every_declared_symbol_is_exported_and_bound(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(lstm_[a-z0-9_]+)\s*\(", text))
     assert names == {"lstm_causal_conv", "lstm_causal_conv_step", "lstm_selective_scan",
-                     "lstm_selective_scan_step", "lstm_residual_rms_norm", "lstm_token_logprobs"}
+                     "lstm_selective_scan_step", "lstm_selective_scan_workspace", "lstm_residual_rms_norm", "lstm_token_logprobs"}
     for n in names:
         assert hasattr(lib, n) and callable(getattr(binding, n))
 
@@ -52,7 +52,7 @@ def _scan(lib, u=64, dt=64, a=64, b=64, c=64, z=None, z_stride=0, b_stride=8, u_
           tokens=4, channels=16, states=8, groups=1, sequences=1, state=None, slots=0, y=64):
     return lib.lstm_selective_scan(u, u_stride, dt, 16, a, b, b_stride, c, 8, None, z, z_stride,
                                    None, 1, dtype, tokens, channels, states, groups, sequences,
-                                   None, state, slots, None, None, y, 16, None)
+                                   None, state, slots, None, None, y, 16, None, 0, None)
 
 
 @pytest.mark.parametrize("bad", [
