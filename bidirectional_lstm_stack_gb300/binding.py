@@ -116,7 +116,7 @@ def load():
             "lstm_selective_scan": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll, _vp,
                                         i, i, i, i, i, i, i, _vp, _vp, i, _vp, _vp, _vp, ll, _vp, sz,
                                         _vp]),
-            "lstm_selective_scan_workspace": (sz, [i, i, i, i, i]),
+            "lstm_selective_scan_workspace": (sz, [i, i, i, i, i, i]),
             "lstm_selective_scan_step": (i, [_vp, ll, _vp, ll, _vp, _vp, ll, _vp, ll, _vp, _vp, ll,
                                              _vp, i, i, i, i, i, i, _vp, i, _vp, _vp, ll, _vp]),
             "lstm_residual_rms_norm": (i, [_vp, ll, _vp, ll, i, _vp, f, i, i, _vp, ll, _vp, ll, i,
@@ -576,7 +576,8 @@ def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, soft
     if y is None:
         y = _like(stream, u)
     lib = load()
-    size = lib.lstm_selective_scan_workspace(tokens, channels, states, count, offsets is None)
+    size = lib.lstm_selective_scan_workspace(tokens, channels, states, groups, count,
+                                             offsets is None)
     workspace = _empty(stream, (size,), torch.uint8, device) if size else None
     _check(lib.lstm_selective_scan(
         *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
@@ -586,10 +587,10 @@ def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, soft
     return y
 
 
-def lstm_selective_scan_workspace(tokens: int, channels: int, states: int, sequences: int,
-                                  equal_lengths: bool) -> int:
+def lstm_selective_scan_workspace(tokens: int, channels: int, states: int, groups: int,
+                                  sequences: int, equal_lengths: bool) -> int:
     """Bytes of workspace of lstm_selective_scan."""
-    return load().lstm_selective_scan_workspace(tokens, channels, states, sequences,
+    return load().lstm_selective_scan_workspace(tokens, channels, states, groups, sequences,
                                                 int(equal_lengths))
 
 

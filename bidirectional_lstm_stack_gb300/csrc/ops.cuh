@@ -229,11 +229,18 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 1 / x for x not below fp32's normal range (infinity gives 0).
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // v / (1 + e^-v): e^-v saturates to 0 or infinity, and the quotient by an
 // infinity is 0.
 __device__ __forceinline__ float silu(float v)
 {
-    return __fdividef(v, 1.0f + ex2(-kLog2e * v));
+    return v * reciprocal(1.0f + ex2(-kLog2e * v));
 }
 
 template <typename F>

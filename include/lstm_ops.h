@@ -102,12 +102,12 @@ int lstm_causal_conv_step(const void *x, long long x_stride, int dtype, int sequ
  *                 no states (state_slots, slots and resume are then not read)
  *   workspace   : device, 16-byte aligned, workspace_bytes long and at least
  *                 lstm_selective_scan_workspace(tokens, channels, states,
- *                 sequences, offsets == NULL) bytes (0: may be NULL); its
- *                 contents need not be kept between calls, but two calls that
- *                 may run at the same time need one each
+ *                 groups, sequences, offsets == NULL) bytes (0: may be NULL);
+ *                 its contents need not be kept between calls, but two calls
+ *                 that may run at the same time need one each
  * Errors as lstm_causal_conv, LSTM_E_LENGTH for a workspace that is too short. */
-size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int sequences,
-                                     int equal_lengths);
+size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int groups,
+                                     int sequences, int equal_lengths);
 int lstm_selective_scan(const void *u, long long u_stride, const void *dt, long long dt_stride,
                         const float *a, const void *b, long long b_stride, const void *c,
                         long long c_stride, const float *skip, const void *z, long long z_stride,

@@ -81,6 +81,25 @@ def test_long_prompts(dtype, length):
     _check(dtype, [length], 24, pool=1, resume=[1])
 
 
+@pytest.mark.parametrize("lengths,channels,states,equal", [
+    ([600], 4096, 16, True), ([24] * 32, 2048, 16, True), ([150] * 4, 1024, 16, True),
+    ([90, 7, 300, 0, 41, 200, 1, 64, 128, 33] * 2, 1024, 16, False),
+    ([33, 700, 2, 90, 400], 500, 16, False), ([260] * 2, 1024, 64, True),
+    ([20, 300, 45] * 6, 640, 64, False), ([500, 64, 1], 1026, 8, False),
+    ([40] * 20, 1024, 4, True), ([170, 80], 259, 5, False), ([33, 65, 129], 2048, 32, False)])
+def test_large_layers(lengths, channels, states, equal):
+    """Sizes on both sides of where the work is divided otherwise."""
+    n = len(lengths)
+    _check("bf16", lengths, channels, states, uniform_=equal, pool=n + 1,
+           slots=[(3 * k + 1) % (n + 1) if (n + 1) % 3 else n - k for k in range(n)],
+           resume=[k % 3 != 0 for k in range(n)])
+
+
+def test_large_layers_in_fp32():
+    _check("f32", [100, 350, 20], 1024, pool=3, resume=[1, 0, 1])
+    _check("f32", [130, 1, 257], 771, pool=3, resume=[1, 1, 1])
+
+
 def test_long_memory():
     # step sizes so small that the first token still counts at the last
     _check("f32", [1500], 8, scale=0.01, pool=1, resume=[1])
