@@ -108,6 +108,8 @@ struct Slots {
     int count;          // 0: no states
 };
 
+typedef unsigned long long Pair;  // two fp32 numbers in one 64-bit register
+
 #ifdef __CUDACC__
 
 __device__ __forceinline__ int sequence_begin(const Sequences &q, int s)
@@ -219,6 +221,21 @@ __device__ __forceinline__ Pack<T, V> pack(const float (&f)[V])
     return r;
 }
 
+// V consecutive fp32 weights (16-byte aligned where V > 1).
+template <int V>
+__device__ __forceinline__ void load_weights(const float *p, float (&w)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(w + i) = __ldg(reinterpret_cast<const float4 *>(p + i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            w[i] = __ldg(p + i);
+    }
+}
+
 // ---- functions ---------------------------------------------------------------------
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -241,6 +258,74 @@ __device__ __forceinline__ float reciprocal(float x)
 __device__ __forceinline__ float silu(float v)
 {
     return v * reciprocal(1.0f + ex2(-kLog2e * v));
+}
+
+// ---- pairs -------------------------------------------------------------------------
+// The paired operations do two roundings each in one issue slot.  They are
+// volatile so that the compiler keeps them in the order they are written in,
+// which hides their latencies.
+__device__ __forceinline__ Pair make_pair(float x, float y)
+{
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split_pair(Pair p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm volatile("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair ex2_pair(Pair p)
+{
+    const float2 v = split_pair(p);
+    float x, y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v.y));
+    return make_pair(x, y);
+}
+__device__ __forceinline__ Pair reciprocal_pair(Pair p)
+{
+    const float2 v = split_pair(p);
+    float x, y;
+    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
+    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v.y));
+    return make_pair(x, y);
+}
+
+// v / (1 + e^-v) in place for K pairs, side by side, so that none waits for its
+// own result
+template <int K>
+__device__ __forceinline__ void silu_pairs(Pair (&v)[K])
+{
+    Pair e[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        e[k] = mul2(v[k], make_pair(-kLog2e, -kLog2e));
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        e[k] = add2(ex2_pair(e[k]), make_pair(1.0f, 1.0f));
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        v[k] = mul2(v[k], reciprocal_pair(e[k]));
 }
 
 template <typename F>

@@ -11,8 +11,6 @@
 
 namespace lstm {
 
-typedef unsigned long long Pair;  // two fp32 numbers in one 64-bit register
-
 struct ScanArgs {
     const void *u;
     long long u_stride;
@@ -89,56 +87,6 @@ int launch_scan_step(const ScanArgs &p, int dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
 
-// The paired operations do two roundings each in one issue slot.  They are
-// volatile so that the compiler keeps them in the order they are written in,
-// which hides their latencies.
-__device__ __forceinline__ Pair make_pair(float x, float y)
-{
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 split_pair(Pair p)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b)
-{
-    Pair r;
-    asm volatile("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b)
-{
-    Pair r;
-    asm volatile("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
-{
-    Pair r;
-    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ Pair ex2_pair(Pair p)
-{
-    const float2 v = split_pair(p);
-    float x, y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v.y));
-    return make_pair(x, y);
-}
-__device__ __forceinline__ Pair reciprocal_pair(Pair p)
-{
-    const float2 v = split_pair(p);
-    float x, y;
-    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
-    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v.y));
-    return make_pair(x, y);
-}
-
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], and
 // log(1 + e) = e q(e) with q of degree 8, fitted by least squares whose
 // weights are moved to where the relative error is largest (Lawson's method)
@@ -173,22 +121,6 @@ __device__ __forceinline__ void softplus_pairs(Pair (&v)[K])
     for (int k = 0; k < K; ++k)
         v[k] = fma2(q[k], e[k], v[k]);
 }
-// v / (1 + e^-v), likewise
-template <int K>
-__device__ __forceinline__ void silu_pairs(Pair (&v)[K])
-{
-    Pair e[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        e[k] = mul2(v[k], make_pair(-kLog2e, -kLog2e));
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        e[k] = add2(ex2_pair(e[k]), make_pair(1.0f, 1.0f));
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        v[k] = mul2(v[k], reciprocal_pair(e[k]));
-}
-
 #endif  // __CUDACC__
 
 }  // namespace lstm
