@@ -32,6 +32,7 @@ enum : unsigned {
     kFaultEpilogue = 1u << 3,
     kFaultDrain = 1u << 4,
     kFaultRecurrence = 1u << 5,
+    kFaultScanStep = 1u << 6,
 };
 
 // The device fault word of the current device (a __device__ variable;
@@ -266,6 +267,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+// This CTA's shared memory -> global, `bytes` (a multiple of 16, both
+// addresses 16-byte aligned).  Tracked by bulk groups.
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     reinterpret_cast<uint64_t>(dst)),
+                 "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void bulk_commit_group()

@@ -173,19 +173,26 @@ def test_step(dtype, channels, states, groups, sequences):
     assert_close(state, new, new_bound, "f32", "state")
 
 
-def test_step_of_a_large_batch():
-    v = _inputs("bf16", 300, 96, 16)
-    state = normal(gen(8), 310, 96, 16)
-    slots = torch.randperm(310, generator=torch.Generator().manual_seed(1))[:300].int()
+@pytest.mark.parametrize("dtype,sequences,channels,states,groups", [
+    ("bf16", 300, 96, 16, 1), ("bf16", 300, 500, 16, 1), ("f32", 70, 1300, 16, 1),
+    ("f16", 2000, 130, 4, 1), ("bf16", 700, 200, 8, 1), ("bf16", 300, 130, 32, 1),
+    ("bf16", 90, 256, 64, 4), ("f32", 40, 256, 128, 1), ("bf16", 600, 256, 16, 2),
+    ("bf16", 600, 130, 16, 2), ("bf16", 700, 129, 13, 1), ("bf16", 9000, 8, 16, 1)])
+def test_step_of_a_large_batch(dtype, sequences, channels, states, groups):
+    v = _inputs(dtype, sequences, channels, states, groups, strided=True)
+    state = normal(gen(8), sequences + 10, channels, states)
+    slots = torch.randperm(sequences + 10, generator=torch.Generator().manual_seed(1))[:sequences].int()
+    slots[5::17] = -1
     before = f64(state)
     y = binding.lstm_selective_scan_step(v["u"], v["dt"], v["a"], v["b"], v["c"], state,
                                          skip=v["skip"], z=v["z"], dt_bias=v["dt_bias"],
-                                         slots=slots.cuda())
+                                         groups=groups, slots=slots.cuda())
     ref, new, bound, new_bound = oracle.selective_scan(
         f64(v["u"]), f64(v["dt"]), f64(v["a"]), f64(v["b"]), f64(v["c"]), f64(v["skip"]),
-        f64(v["z"]), f64(v["dt_bias"]), True, 1, [(s, s + 1) for s in range(300)], before,
-        slots.tolist(), step=True)
-    assert_close(y, ref, bound, "bf16", "y")
+        f64(v["z"]), f64(v["dt_bias"]), True, groups, [(s, s + 1) for s in range(sequences)],
+        before, slots.tolist(), step=True)
+    assert binding.lstm_fault_status() == 0
+    assert_close(y, ref, bound, dtype, "y")
     assert_close(state, new, new_bound, "f32", "state")
 
 
