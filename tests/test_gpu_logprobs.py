@@ -31,7 +31,7 @@ def _tokens(g, rows, vocab):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 31, 32, 33, 100, 257, 2048, 2049, 5000, 16384,
+@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 31, 32, 33, 100, 257, 512, 513, 2048, 2049, 4096, 4097, 5000, 16384,
                                    50021])
 def test_row_lengths(dtype, vocab):
     g = gen(vocab)
