@@ -403,47 +403,48 @@ class LSTMHeads:
 # Outputs that are not given are allocated for the stream the call runs on.
 
 
+# Small calls last about as long on the host as on the GPU, so the common case
+# of every check is one condition, and what is wrong is sorted out apart.
+
+_element_types = {}
+
+
 def _element_type(t) -> int:
-    import torch
-    code = {torch.float32: LSTM_F32, torch.bfloat16: LSTM_BF16, torch.float16: LSTM_F16}.get(t.dtype)
+    code = _element_types.get(t.dtype)
     if code is None:
-        raise ValueError(f"element type {t.dtype}, expected float32, bfloat16 or float16")
+        import torch
+        _element_types.update({torch.float32: LSTM_F32, torch.bfloat16: LSTM_BF16,
+                               torch.float16: LSTM_F16})
+        code = _element_types.get(t.dtype)
+        if code is None:
+            raise ValueError(f"element type {t.dtype}, expected float32, bfloat16 or float16")
     return code
 
 
-def _matrix(name: str, t, rows: int, cols: int, like) -> int:
-    """Row stride of the matrix t [rows, cols] of like's type and device."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, cols)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-    stride, inner = t.stride()
-    if inner != 1 and cols > 1:
-        raise ValueError(f"{name} needs consecutive columns, has stride {inner} between them")
-    return stride
+def _matrix(name: str, t, shape: tuple, dtype, index: int) -> int:
+    """Row stride of the matrix t of the given shape, type and CUDA device."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index:
+        stride = t.stride()
+        if stride[1] == 1 or shape[1] <= 1:
+            return stride[0]
+        raise ValueError(f"{name} needs consecutive columns, has stride {stride[1]} between them")
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} "
+                     f"on cuda:{index}")
 
 
-def _dense(name: str, t, shape: tuple, dtype, device):
+def _dense(name: str, t, shape: tuple, dtype, index: int):
     """Address of the densely packed tensor t (None for None)."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not densely packed")
-    return t.data_ptr()
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected densely packed "
+                     f"{dtype} {shape} on cuda:{index}")
 
 
 def _on(stream, device):
     """Context in which torch allocates for the stream that a call runs on."""
-    import contextlib
-
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
@@ -457,29 +458,49 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, index: int):
+    """cudaStream_t of the stream (None: the device's current one)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _like(stream, t):
     """An uninitialised dense tensor of t's shape and type."""
+    if stream is None:
+        import torch
+        return torch.empty_like(t)
     return _empty(stream, t.shape, t.dtype, t.device)
 
 
-def _state(t, shape: tuple, dtype, sequences: int, slots, resume, device):
+def _rows(name: str, t):
+    """Rows, columns and CUDA device of the matrix that gives a call its sizes."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected two dimensions")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
+    return shape[0], shape[1], index
+
+
+def _state(t, shape: tuple, dtype, sequences: int, slots, resume, index: int):
     """Addresses and slot count of the states' arguments."""
     import torch
     if t is None:
         if slots is not None or resume is not None:
             raise ValueError("slots and resume need a state")
         return None, 0, None, None
-    if t.dim() != len(shape) + 1:
-        raise ValueError(f"state has shape {tuple(t.shape)}, expected {('slots', *shape)}")
-    count = t.shape[0]
+    count = t.shape[0] if t.dim() > 0 else 0
     if slots is None and count < sequences:
         raise ValueError(f"{sequences} sequences without slots, a state of {count}")
-    return (_dense("state", t, (count, *shape), dtype, device), count,
-            _dense("slots", slots, (sequences,), torch.int32, device),
-            _dense("resume", resume, (sequences,), torch.int32, device))
+    return (_dense("state", t, (count, *shape), dtype, index), count,
+            _dense("slots", slots, (sequences,), torch.int32, index),
+            _dense("resume", resume, (sequences,), torch.int32, index))
 
 
-def _sequences(sequences, offsets, device):
+def _sequences(sequences, offsets, index: int):
     """Number of sequences and the offsets' address."""
     import torch
     if offsets is None:
@@ -487,7 +508,7 @@ def _sequences(sequences, offsets, device):
     count = offsets.numel() - 1
     if sequences is not None and sequences != count:
         raise ValueError(f"{sequences} sequences, offsets for {count}")
-    return count, _dense("offsets", offsets, (count + 1,), torch.int32, device)
+    return count, _dense("offsets", offsets, (count + 1,), torch.int32, index)
 
 
 def lstm_causal_conv(x, w, bias=None, *, silu: bool = True, sequences=None, offsets=None,
@@ -500,21 +521,19 @@ def lstm_causal_conv(x, w, bias=None, *, silu: bool = True, sequences=None, offs
     [slots, width - 1, channels] of x's type, slots and resume int32
     [sequences]."""
     import torch
-    tokens, channels = x.shape
-    device = x.device
-    width = w.shape[-1]
-    dtype = _element_type(x)
-    count, offsets_at = _sequences(sequences, offsets, device)
-    state_at, state_slots, slots_at, resume_at = _state(
-        state, (width - 1, channels), x.dtype, count, slots, resume, device)
+    tokens, channels, index = _rows("x", x)
+    shape, dtype, code, width = (tokens, channels), x.dtype, _element_type(x), w.shape[-1]
+    count, offsets_at = _sequences(sequences, offsets, index)
+    state_at, state_slots, slots_at, resume_at = _state(state, (width - 1, channels), dtype, count,
+                                                        slots, resume, index)
     if y is None:
         y = _like(stream, x)
-    _check(load().lstm_causal_conv(
-        x.data_ptr(), _matrix("x", x, tokens, channels, x), dtype, tokens, channels, width,
-        _dense("w", w, (channels, width), torch.float32, device),
-        _dense("bias", bias, (channels,), torch.float32, device), int(silu), count, offsets_at,
+    _check((_lib or load()).lstm_causal_conv(
+        x.data_ptr(), _matrix("x", x, shape, dtype, index), code, tokens, channels, width,
+        _dense("w", w, (channels, width), torch.float32, index),
+        _dense("bias", bias, (channels,), torch.float32, index), silu, count, offsets_at,
         state_at, state_slots, slots_at, resume_at, y.data_ptr(),
-        _matrix("y", y, tokens, channels, x), _stream(stream, device)))
+        _matrix("y", y, shape, dtype, index), _raw_stream(stream, index)))
     return y
 
 
@@ -523,36 +542,36 @@ def lstm_causal_conv_step(x, w, bias, state, *, silu: bool = True, slots=None, y
     """The next token of every sequence, x [sequences, channels]; returns y
     (new unless given) and moves the state on.  Arguments as lstm_causal_conv."""
     import torch
-    sequences, channels = x.shape
-    device = x.device
-    width = w.shape[-1]
-    state_at, state_slots, slots_at, _ = _state(
-        state, (width - 1, channels), x.dtype, sequences, slots, None, device)
+    sequences, channels, index = _rows("x", x)
+    shape, dtype, code, width = (sequences, channels), x.dtype, _element_type(x), w.shape[-1]
+    state_at, state_slots, slots_at, _ = _state(state, (width - 1, channels), dtype, sequences,
+                                                slots, None, index)
     if y is None:
         y = _like(stream, x)
-    _check(load().lstm_causal_conv_step(
-        x.data_ptr(), _matrix("x", x, sequences, channels, x), _element_type(x), sequences,
-        channels, width, _dense("w", w, (channels, width), torch.float32, device),
-        _dense("bias", bias, (channels,), torch.float32, device), int(silu), state_at, state_slots,
-        slots_at, y.data_ptr(), _matrix("y", y, sequences, channels, x), _stream(stream, device)))
+    _check((_lib or load()).lstm_causal_conv_step(
+        x.data_ptr(), _matrix("x", x, shape, dtype, index), code, sequences, channels, width,
+        _dense("w", w, (channels, width), torch.float32, index),
+        _dense("bias", bias, (channels,), torch.float32, index), silu, state_at, state_slots,
+        slots_at, y.data_ptr(), _matrix("y", y, shape, dtype, index),
+        _raw_stream(stream, index)))
     return y
 
 
-def _scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups):
+def _scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index):
     """The arguments that both scan entry points begin with, up to softplus."""
     import torch
-    rows, channels = u.shape
-    device = u.device
+    rows, channels = shape
     states = a.shape[-1]
-    return (u.data_ptr(), _matrix("u", u, rows, channels, u),
-            dt.data_ptr(), _matrix("dt", dt, rows, channels, u),
-            _dense("a", a, (channels, states), torch.float32, device),
-            b.data_ptr(), _matrix("b", b, rows, groups * states, u),
-            c.data_ptr(), _matrix("c", c, rows, groups * states, u),
-            _dense("skip", skip, (channels,), torch.float32, device),
+    dtype, f32, shared = u.dtype, torch.float32, (rows, groups * states)
+    return (u.data_ptr(), _matrix("u", u, shape, dtype, index),
+            dt.data_ptr(), _matrix("dt", dt, shape, dtype, index),
+            _dense("a", a, (channels, states), f32, index),
+            b.data_ptr(), _matrix("b", b, shared, dtype, index),
+            c.data_ptr(), _matrix("c", c, shared, dtype, index),
+            _dense("skip", skip, (channels,), f32, index),
             None if z is None else z.data_ptr(),
-            0 if z is None else _matrix("z", z, rows, channels, u),
-            _dense("dt_bias", dt_bias, (channels,), torch.float32, device), int(softplus))
+            0 if z is None else _matrix("z", z, shape, dtype, index),
+            _dense("dt_bias", dt_bias, (channels,), f32, index), softplus)
 
 
 def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, softplus: bool = True,
@@ -567,23 +586,22 @@ def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, soft
     one); state [slots, channels, states] fp32, slots and resume int32
     [sequences]."""
     import torch
-    tokens, channels = u.shape
-    device = u.device
-    states = a.shape[-1]
-    count, offsets_at = _sequences(sequences, offsets, device)
-    state_at, state_slots, slots_at, resume_at = _state(
-        state, (channels, states), torch.float32, count, slots, resume, device)
+    tokens, channels, index = _rows("u", u)
+    shape, code, states = (tokens, channels), _element_type(u), a.shape[-1]
+    count, offsets_at = _sequences(sequences, offsets, index)
+    state_at, state_slots, slots_at, resume_at = _state(state, (channels, states), torch.float32,
+                                                        count, slots, resume, index)
     if y is None:
         y = _like(stream, u)
-    lib = load()
+    lib = _lib or load()
     size = lib.lstm_selective_scan_workspace(tokens, channels, states, groups, count,
                                              offsets is None)
-    workspace = _empty(stream, (size,), torch.uint8, device) if size else None
+    workspace = _empty(stream, (size,), torch.uint8, u.device) if size else None
     _check(lib.lstm_selective_scan(
-        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
+        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index), code,
         tokens, channels, states, groups, count, offsets_at, state_at, state_slots, slots_at,
-        resume_at, y.data_ptr(), _matrix("y", y, tokens, channels, u), _ptr(workspace), size,
-        _stream(stream, device)))
+        resume_at, y.data_ptr(), _matrix("y", y, shape, u.dtype, index), _ptr(workspace), size,
+        _raw_stream(stream, index)))
     return y
 
 
@@ -601,17 +619,16 @@ def lstm_selective_scan_step(u, dt, a, b, c, state, *, skip=None, z=None, dt_bia
     y (new unless given) and moves the state on.  Arguments as
     lstm_selective_scan."""
     import torch
-    sequences, channels = u.shape
-    device = u.device
-    states = a.shape[-1]
-    state_at, state_slots, slots_at, _ = _state(
-        state, (channels, states), torch.float32, sequences, slots, None, device)
+    sequences, channels, index = _rows("u", u)
+    shape, code, states = (sequences, channels), _element_type(u), a.shape[-1]
+    state_at, state_slots, slots_at, _ = _state(state, (channels, states), torch.float32, sequences,
+                                                slots, None, index)
     if y is None:
         y = _like(stream, u)
-    _check(load().lstm_selective_scan_step(
-        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups), _element_type(u),
+    _check((_lib or load()).lstm_selective_scan_step(
+        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index), code,
         sequences, channels, states, groups, state_at, state_slots, slots_at, y.data_ptr(),
-        _matrix("y", y, sequences, channels, u), _stream(stream, device)))
+        _matrix("y", y, shape, u.dtype, index), _raw_stream(stream, index)))
     return y
 
 
@@ -626,36 +643,34 @@ def lstm_residual_rms_norm(x, weight, eps: float, *, residual=None, residual_out
     for the norm; else scales is None.  v is rounded to x's type (residual_out:
     where to, may be residual); None without a residual."""
     import torch
-    rows, cols = x.shape
-    device = x.device
-    dtype = _element_type(x)
+    rows, cols, index = _rows("x", x)
+    shape, dtype, code = (rows, cols), x.dtype, _element_type(x)
     res_at = out_at = None
     res_stride = out_stride = 0
     if residual is not None:
-        res_at, res_stride = residual.data_ptr(), _matrix("residual", residual, rows, cols, x)
+        res_at, res_stride = residual.data_ptr(), _matrix("residual", residual, shape, dtype, index)
         if residual_out is None:
             residual_out = _like(stream, x)
         out_at = residual_out.data_ptr()
-        out_stride = _matrix("residual_out", residual_out, rows, cols, x)
+        out_stride = _matrix("residual_out", residual_out, shape, dtype, index)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
+    y_dtype = torch.float8_e4m3fn if quantize else dtype
     if y is None:
-        y = _empty(stream, x.shape, torch.float8_e4m3fn if quantize else x.dtype, device)
+        y = _empty(stream, shape, y_dtype, x.device) if quantize else _like(stream, x)
+    scales_at = None
     if quantize:
-        width = -(-cols // group) if group > 0 else 1
+        wide = (rows, -(-cols // group) if group > 0 else 1)
         if scales is None:
-            scales = _empty(stream, (rows, width), torch.float32, device)
-        if y.dtype != torch.float8_e4m3fn:
-            raise ValueError(f"y is {y.dtype}, expected {torch.float8_e4m3fn}")
-        y_stride = _matrix("y", y, rows, cols, y)
-        scales_at = _dense("scales", scales, (rows, width), torch.float32, device)
+            scales = _empty(stream, wide, torch.float32, x.device)
+        scales_at = _dense("scales", scales, wide, torch.float32, index)
     else:
-        y_stride, scales, scales_at = _matrix("y", y, rows, cols, x), None, None
-    _check(load().lstm_residual_rms_norm(
-        x.data_ptr(), _matrix("x", x, rows, cols, x), res_at, res_stride, dtype,
-        _dense("weight", weight, (cols,), torch.float32, device), eps, rows, cols, out_at,
-        out_stride, y.data_ptr(), y_stride, LSTM_E4M3 if quantize else dtype, scales_at, group,
-        _stream(stream, device)))
+        scales = None
+    _check((_lib or load()).lstm_residual_rms_norm(
+        x.data_ptr(), _matrix("x", x, shape, dtype, index), res_at, res_stride, code,
+        _dense("weight", weight, (cols,), torch.float32, index), eps, rows, cols, out_at,
+        out_stride, y.data_ptr(), _matrix("y", y, shape, y_dtype, index),
+        LSTM_E4M3 if quantize else code, scales_at, group, _raw_stream(stream, index)))
     return y, scales, residual_out
 
 
@@ -664,7 +679,7 @@ def lstm_token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = Tr
     returns (logp, entropy, top_logp, top_ids): fp32 [rows], fp32 [rows], fp32
     and int64 [rows, top]; None for what is not asked for."""
     import torch
-    rows, vocab = logits.shape
+    rows, vocab, index = _rows("logits", logits)
     device = logits.device
     logp = h = top_logp = top_ids = None
     if tokens is not None:
@@ -674,8 +689,8 @@ def lstm_token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = Tr
     if top > 0:
         top_logp = _empty(stream, (rows, top), torch.float32, device)
         top_ids = _empty(stream, (rows, top), torch.int64, device)
-    _check(load().lstm_token_logprobs(
-        logits.data_ptr(), _matrix("logits", logits, rows, vocab, logits), _element_type(logits),
-        rows, vocab, _dense("tokens", tokens, (rows,), torch.int64, device), _ptr(logp), _ptr(h),
-        top, _ptr(top_logp), _ptr(top_ids), _stream(stream, device)))
+    _check((_lib or load()).lstm_token_logprobs(
+        logits.data_ptr(), _matrix("logits", logits, (rows, vocab), logits.dtype, index),
+        _element_type(logits), rows, vocab, _dense("tokens", tokens, (rows,), torch.int64, index),
+        _ptr(logp), _ptr(h), top, _ptr(top_logp), _ptr(top_ids), _raw_stream(stream, index)))
     return logp, h, top_logp, top_ids
