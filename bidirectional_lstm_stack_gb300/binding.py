@@ -105,6 +105,7 @@ def load():
             "lstm_test_recurrence_timeout": (i, [i, ctypes.c_uint, i]),
             "lstm_test_projection_timeout": (i, [i, ctypes.c_uint, i]),
             "lstm_test_heads_timeout": (i, [i, ctypes.c_uint, i]),
+            "lstm_test_scan_step_timeout": (i, [i, ctypes.c_uint, i]),
             "lstm_recurrence_floor": (i, [_vp, _vp, _vp, _vp, i, i, i, _vp]),
             "lstm_tf32_rate": (i, [i, i, ctypes.POINTER(ctypes.c_double)]),
             "lstm_recurrence_fused": (i, [_vp, i, _vp, _vp, i, _vp, _vp, _vp, i, i, i, _vp]),

@@ -24,6 +24,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "lstm_ops.h"
 
 namespace lstm {
 
@@ -1093,6 +1094,11 @@ extern "C" int lstm_test_recurrence_timeout(int withhold, unsigned int wait_limi
 extern "C" int lstm_test_projection_timeout(int withhold, unsigned int wait_limit_us, int device)
 {
     return set_timeout_test(kTestProjection, "projection", withhold, wait_limit_us, device);
+}
+
+extern "C" int lstm_test_scan_step_timeout(int withhold, unsigned int wait_limit_us, int device)
+{
+    return set_timeout_test(kTestScanStep, "scan step", withhold, wait_limit_us, device);
 }
 
 extern "C" int lstm_test_heads_timeout(int withhold, unsigned int wait_limit_us, int device)

@@ -55,13 +55,19 @@ int check_launch_injection(const char *what);
 // as kernel parameters: every bounded wait gives up after wait_limit_ns, and
 // with `withhold` the kernel starves its own waits (the recurrence: CTA 0 of
 // every cluster pushes no h; the projection and the heads: the producer
-// loads nothing).  Defaults: 2 s, no withholding.
+// loads nothing; the scan step: no tile is copied in).  Defaults: 2 s, no withholding.
 constexpr unsigned long long kDefaultWaitLimitNs = 2000000000ull;
 struct KernelTest {
     unsigned long long wait_limit_ns = kDefaultWaitLimitNs;
     int withhold = 0;
 };
-enum TestKernel { kTestRecurrence = 0, kTestProjection = 1, kTestHeads = 2, kTestKernels = 3 };
+enum TestKernel {
+    kTestRecurrence = 0,
+    kTestProjection = 1,
+    kTestHeads = 2,
+    kTestScanStep = 3,
+    kTestKernels = 4
+};
 // The settings of `kernel` on the current device.
 KernelTest kernel_test(int kernel);
 // Sets them on the current device.

@@ -206,33 +206,32 @@ int launch_sized(const NormArgs &p, int rows, bool quant, cudaStream_t stream)
     const int vectors = (p.cols + V - 1) / V;
     if constexpr (V == 1) {
         // single elements: several a thread (2047 columns of bf16, 8192 rows:
-        // 512 threads of four 57 us, 1024 of two 80)
+        // 256 threads of eight 42 us, 512 of four 50, 1024 of two 80)
         if (vectors <= 512)
             return launch<T, 1, 2, 256>(p, rows, quant, stream);
         if (vectors <= 2048)
-            return launch<T, 1, 4, 512>(p, rows, quant, stream);
+            return launch<T, 1, 8, 256>(p, rows, quant, stream);
         if (vectors <= 8192)
             return launch<T, 1, 8, 1024>(p, rows, quant, stream);
         return launch<T, 1, 32, 1024>(p, rows, quant, stream);
     } else {
-    // One vector a thread while a block has threads for it: with more, fewer
-    // loads are on their way at a time (4096 columns of bf16, 12288 rows to
-    // e4m3: 512 threads 60 us, 256 of two vectors 68, 128 of four 86).
-    if (vectors <= 64)
-        return launch<T, V, 1, 64>(p, rows, quant, stream);
-    if (vectors <= 128)
-        return launch<T, V, 1, 128>(p, rows, quant, stream);
-    if (vectors <= 256)
-        return launch<T, V, 1, 256>(p, rows, quant, stream);
-    if (vectors <= 512)
-        return launch<T, V, 1, 512>(p, rows, quant, stream);
-    if (vectors <= 1024)
-        return launch<T, V, 1, 1024>(p, rows, quant, stream);
-    if (vectors <= 2048)
-        return launch<T, V, 2, 1024>(p, rows, quant, stream);
-    if (vectors <= 4096)
-        return launch<T, V, 4, 1024>(p, rows, quant, stream);
-    return launch<T, V, kMaxCols / V / 1024, 1024>(p, rows, quant, stream);
+        // One vector a thread while a block has threads for it: with more,
+        // fewer loads are on their way at a time (4096 columns of bf16, 12288
+        // rows to e4m3: 512 threads 60 us, 256 of two vectors 68, 128 of four
+        // 86).
+        if (vectors <= 64)
+            return launch<T, V, 1, 64>(p, rows, quant, stream);
+        if (vectors <= 128)
+            return launch<T, V, 1, 128>(p, rows, quant, stream);
+        if (vectors <= 256)
+            return launch<T, V, 1, 256>(p, rows, quant, stream);
+        if (vectors <= 512)
+            return launch<T, V, 1, 512>(p, rows, quant, stream);
+        if (vectors <= 1024)
+            return launch<T, V, 1, 1024>(p, rows, quant, stream);
+        if (vectors <= 2048)
+            return launch<T, V, 2, 1024>(p, rows, quant, stream);
+        return launch<T, V, kMaxCols / V / 1024, 1024>(p, rows, quant, stream);
     }
 }
 

@@ -48,6 +48,8 @@ inline int check_sequences(const char *what, int tokens, int sequences, const in
 {
     if (tokens < 0 || sequences < 0 || (tokens > 0 && sequences == 0))
         return fail(LSTM_E_INVALID, "%s: %d tokens, %d sequences", what, tokens, sequences);
+    if (tokens > 0x7fffff00)  // (token numbers a tile beyond the last still count)
+        return fail(LSTM_E_OVERFLOW, "%s: %d tokens", what, tokens);
     if (!offsets && sequences > 0 && tokens % sequences)
         return fail(LSTM_E_LENGTH,
                     "%s: %d tokens are no multiple of %d sequences (and no offsets are given)", what,

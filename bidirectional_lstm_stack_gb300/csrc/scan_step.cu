@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs p)
 constexpr int kTiles = 4;
 
 template <typename T, int NS, int L>
-__global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, unsigned *fault)
+__global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, unsigned *fault,
+                                                                     KernelTest test)
 {
     constexpr int kAcross = kThreads / L;  // channels of a block
     constexpr int kQuads = NS / 4, kStates = NS * L;
@@ -166,6 +167,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, u
     };
     int fetched = 0;
     const auto fetch = [&](int k, int slot) {  // by one thread
+        if (test.withhold)
+            return;
         fetched = k + 1;
         if (slot >= 0) {
             ptx::mbar_arrive_expect_tx(&full[k % kTiles], bytes);
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, u
         const float ut = Elem<T>::get(x.u), su = st * ut;
         float *tile = tiles[k % kTiles] + threadIdx.x * NS;
         if (!ptx::mbar_wait_bounded(&full[k % kTiles], k / kTiles & 1, &abort, fault, kFaultScanStep,
-                                    kDefaultWaitLimitNs))
+                                    test.wait_limit_ns))
             break;
         float out = 0.0f;
 #pragma unroll
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, u
     if (threadIdx.x == 0) {
         // after a wait that ran out: copies that were asked for may still land
         for (; abort && k < fetched; ++k)
-            ptx::mbar_wait_drain(&full[k % kTiles], k / kTiles & 1, fault, kDefaultWaitLimitNs);
+            ptx::mbar_wait_drain(&full[k % kTiles], k / kTiles & 1, fault, test.wait_limit_ns);
         ptx::bulk_wait_group<0>();
     }
 }
@@ -319,7 +322,7 @@ int launch_tiles(const ScanArgs &p, cudaStream_t stream)
     rows = rows < p.seq.count ? rows : p.seq.count;
     scan_step_tiles_kernel<T, NS, L>
         <<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(rows)), kThreads, 0, stream>>>(
-            p, fault);
+            p, fault, kernel_test(kTestScanStep));
     return cuda_status(cudaGetLastError(), "lstm_selective_scan_step launch");
 }
 

@@ -118,7 +118,9 @@ int lstm_selective_scan(const void *u, long long u_stride, const void *dt, long 
 
 /* The next token of every sequence: row s of u, dt, b, c, z and y is sequence
  * s's, and its state moves on by one token.  Arguments and errors as
- * lstm_selective_scan; state is required. */
+ * lstm_selective_scan; state is required.  A copy of states that does not
+ * arrive within two seconds sets the library's fault word (lstm_fault_status);
+ * the call's outputs and states are then unspecified. */
 int lstm_selective_scan_step(const void *u, long long u_stride, const void *dt,
                              long long dt_stride, const float *a, const void *b,
                              long long b_stride, const void *c, long long c_stride,
@@ -166,6 +168,11 @@ int lstm_residual_rms_norm(const void *x, long long x_stride, const void *residu
 int lstm_token_logprobs(const void *logits, long long stride, int dtype, int rows, int vocab,
                         const long long *tokens, float *logp, float *entropy, int top,
                         float *top_logp, long long *top_ids, void *stream);
+
+/* Failure-injection hook, as lstm_test_recurrence_timeout: with withhold != 0
+ * lstm_selective_scan_step asks for no copies of states where it works on whole
+ * tiles of them, so that the waits for them run out. */
+int lstm_test_scan_step_timeout(int withhold, unsigned int wait_limit_us, int device);
 
 #ifdef __cplusplus
 }

@@ -196,6 +196,59 @@ def test_step_of_a_large_batch(dtype, sequences, channels, states, groups):
     assert_close(state, new, new_bound, "f32", "state")
 
 
+def test_a_step_whose_states_do_not_arrive_is_reported():
+    lib = binding.load()
+    v = _inputs("bf16", 300, 128, 16)
+    state = normal(gen(8), 300, 128, 16)
+    before = state.clone()
+    call = lambda: binding.lstm_selective_scan_step(v["u"], v["dt"], v["a"], v["b"], v["c"], state)
+    try:
+        assert lib.lstm_test_scan_step_timeout(1, 1000, 0) == 0
+        call()
+        assert binding.lstm_fault_status() == 1 << 6
+        assert torch.equal(state, before)
+    finally:
+        assert lib.lstm_test_scan_step_timeout(0, 0, 0) == 0
+    # the context stays usable
+    y = call()
+    ref, new, bound, new_bound = oracle.selective_scan(
+        f64(v["u"]), f64(v["dt"]), f64(v["a"]), f64(v["b"]), f64(v["c"]), None, None, None, True, 1,
+        [(s, s + 1) for s in range(300)], f64(before), step=True)
+    assert binding.lstm_fault_status() == 0
+    assert_close(y, ref, bound, "bf16")
+    assert_close(state, new, new_bound, "f32")
+
+
+def test_launch_failures_are_reported():
+    lib = binding.load()
+    v = _inputs("bf16", 400, 64, 16)
+    call = lambda: binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"])
+    ref = call()
+    try:
+        for skip in range(3):  # two passes and what carries the states between them
+            lib.lstm_test_fail_launches(skip, 1)
+            with pytest.raises(binding.LSTMError) as e:
+                call()
+            assert e.value.code == binding.LSTM_E_CUDA
+    finally:
+        lib.lstm_test_fail_launches(0, 0)
+    assert torch.equal(call(), ref)
+
+
+def test_a_workspace_that_is_too_short_is_refused():
+    lib = binding.load()
+    size = binding.lstm_selective_scan_workspace(400, 64, 16, 1, 1, True)
+    assert size > 0
+    z = torch.zeros(400 * 64, device="cuda")
+    at, s = z.data_ptr(), torch.cuda.current_stream().cuda_stream
+    call = lambda w, n: lib.lstm_selective_scan(
+        at, 64, at, 64, at, at, 16, at, 16, None, None, 0, None, 1, 0, 400, 64, 16, 1, 1, None, None,
+        0, None, None, at, 64, w, n, s)
+    assert call(None, 0) == binding.LSTM_E_INVALID
+    assert call(at, size - 1) == binding.LSTM_E_LENGTH
+    assert call(at + 4, size) == binding.LSTM_E_INVALID
+
+
 def test_prompt_in_parts_and_steps_goes_on_from_its_state():
     v = _inputs("f32", 90, 48, 16)
     call = lambda a, b, **k: binding.lstm_selective_scan(

@@ -22,9 +22,11 @@ def test_every_declared_symbol_is_exported_and_bound(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b(lstm_[a-z0-9_]+)\s*\(", text))
     assert names == {"lstm_causal_conv", "lstm_causal_conv_step", "lstm_selective_scan",
-                     "lstm_selective_scan_step", "lstm_selective_scan_workspace", "lstm_residual_rms_norm", "lstm_token_logprobs"}
+                     "lstm_selective_scan_step", "lstm_selective_scan_workspace", "lstm_residual_rms_norm", "lstm_token_logprobs",
+                     "lstm_test_scan_step_timeout"}
     for n in names:
-        assert hasattr(lib, n) and callable(getattr(binding, n))
+        assert hasattr(lib, n)
+        assert n.startswith("lstm_test_") or callable(getattr(binding, n))
 
 
 def _conv(lib, x=64, x_stride=16, dtype=0, tokens=4, channels=16, width=4, w=64, sequences=1,
@@ -110,3 +112,12 @@ def test_logprobs_refuses(lib, bad):
 def test_logprobs_sizes(lib):
     assert _logprobs(lib, vocab=(1 << 30) + 1, stride=1 << 31) == binding.LSTM_E_OVERFLOW
     assert _logprobs(lib, logits=None, rows=0) == binding.LSTM_OK
+
+
+def test_very_many_tokens(lib):
+    assert _conv(lib, tokens=0x7fffffff) == binding.LSTM_E_OVERFLOW
+    assert _scan(lib, tokens=0x7fffffff) == binding.LSTM_E_OVERFLOW
+
+
+def test_timeout_hook_refuses_limits_above_two_seconds(lib):
+    assert lib.lstm_test_scan_step_timeout(1, 2000001, 0) == INVALID
