@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
 // e^(a * its step sizes' sum).  A thread follows one state of a channel pair
 // over a sequence's spans, loading kCarry of them together.  grid (sequences *
 // channel blocks * NS).
-constexpr int kCarry = 8;
+constexpr int kCarry = 16;
 template <int NS, int G>
 __global__ void __launch_bounds__(kScanThreads) carry_kernel(ScanArgs p, Spans w)
 {
