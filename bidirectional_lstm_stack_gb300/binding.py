@@ -463,7 +463,9 @@ def _raw_stream(stream, index: int):
     """cudaStream_t of the stream (None: the device's current one)."""
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+        # (what current_stream() asks, without the object around it)
+        ask = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return ask(index) if ask else torch.cuda.current_stream(index).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -218,7 +218,7 @@ using namespace lstm;
 extern "C" size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int groups,
                                                 int sequences, int equal_lengths)
 {
-    if (tokens <= 0 || channels <= 0 || states <= 0 || states > LSTM_SCAN_MAX_STATES ||
+    if (tokens < 0 || channels <= 0 || states <= 0 || states > LSTM_SCAN_MAX_STATES ||
         groups <= 0 || sequences <= 0)
         return 0;
     return make_plan(tokens, channels, states, groups, sequences, equal_lengths != 0).bytes;

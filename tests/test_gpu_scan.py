@@ -75,6 +75,24 @@ def test_lengths(length):
     _check("f32", [length], 33, pool=1, resume=[0])
 
 
+def test_only_empty_prompts():
+    # states that are not gone on from become zeros, the others stay
+    n = 400
+    state = normal(gen(1), n, 64, 16)
+    before = state.clone()
+    resume = torch.arange(n, device="cuda").int() % 2
+    v = _inputs("bf16", 1, 64, 16)
+    y = binding.lstm_selective_scan(v["u"][:0], v["dt"][:0], v["a"], v["b"][:0], v["c"][:0],
+                                    offsets=_i32([0] * (n + 1)), state=state, resume=resume)
+    assert y.shape == (0, 64)
+    assert torch.equal(state[1::2], before[1::2]) and (state[::2] == 0).all()
+    conv = normal(gen(2), n, 3, 64)
+    kept = conv.clone()
+    binding.lstm_causal_conv(torch.empty(0, 64, device="cuda"), torch.ones(64, 4, device="cuda"),
+                             offsets=_i32([0] * (n + 1)), state=conv, resume=resume)
+    assert torch.equal(conv[1::2], kept[1::2]) and (conv[::2] == 0).all()
+
+
 @pytest.mark.parametrize("length", [589, 1000, 2500])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_prompts(dtype, length):
