@@ -5,8 +5,9 @@ Argument marshalling only: every function here checks nothing the library
 does not check again, computes nothing, and forwards to the C entry point of
 the same name.  Device buffers are torch CUDA tensors (their ``data_ptr``),
 streams are torch streams (their ``cuda_stream`` handle; default: the current
-stream of the tensor's device).  If the library is missing, every call raises
-``LibraryMissing``: there is no fallback.
+stream of the tensor's device).  The functions of lstm_ops.h go through the
+compiled module ``_native``, which checks tensors and allocates outputs.  If the
+library is missing, every call raises ``LibraryMissing``: there is no fallback.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ import numpy as np
 from .synthetic import FEATURES, HIDDEN, LAYERS
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblstmstack.so")
+NATIVE_PATH = os.path.join(os.path.dirname(LIB_PATH), "_native.so")
 GATE_COLUMNS = 8 * HIDDEN
 OUTPUT = 2 * HIDDEN
 
@@ -402,116 +404,25 @@ class LSTMHeads:
 # that every tensor has the type, shape and device that the call's sizes say.
 # Matrices are [rows, columns] with consecutive columns and any row stride.
 # Outputs that are not given are allocated for the stream the call runs on.
+# Small calls last longer on the host than on the GPU, so checks, outputs and
+# the call itself are compiled (csrc/python_ops.cpp): a decode step of one
+# sequence takes 7.6 us from Python, through ctypes it took 25.
+
+_ops = None
 
 
-# Small calls last about as long on the host as on the GPU, so the common case
-# of every check is one condition, and what is wrong is sorted out apart.
-
-_element_types = {}
-
-
-def _element_type(t) -> int:
-    code = _element_types.get(t.dtype)
-    if code is None:
-        import torch
-        _element_types.update({torch.float32: LSTM_F32, torch.bfloat16: LSTM_BF16,
-                               torch.float16: LSTM_F16})
-        code = _element_types.get(t.dtype)
-        if code is None:
-            raise ValueError(f"element type {t.dtype}, expected float32, bfloat16 or float16")
-    return code
-
-
-def _matrix(name: str, t, shape: tuple, dtype, index: int) -> int:
-    """Row stride of the matrix t of the given shape, type and CUDA device."""
-    if t.shape == shape and t.dtype is dtype and t.get_device() == index:
-        stride = t.stride()
-        if stride[1] == 1 or shape[1] <= 1:
-            return stride[0]
-        raise ValueError(f"{name} needs consecutive columns, has stride {stride[1]} between them")
-    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} "
-                     f"on cuda:{index}")
-
-
-def _dense(name: str, t, shape: tuple, dtype, index: int):
-    """Address of the densely packed tensor t (None for None)."""
-    if t is None:
-        return None
-    if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected densely packed "
-                     f"{dtype} {shape} on cuda:{index}")
-
-
-def _on(stream, device):
-    """Context in which torch allocates for the stream that a call runs on."""
-    import torch
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    return torch.cuda.stream(stream)
-
-
-def _empty(stream, shape, dtype, device):
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with _on(stream, device):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _raw_stream(stream, index: int):
-    """cudaStream_t of the stream (None: the device's current one)."""
-    if stream is None:
-        import torch
-        # (what current_stream() asks, without the object around it)
-        ask = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return ask(index) if ask else torch.cuda.current_stream(index).cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _like(stream, t):
-    """An uninitialised dense tensor of t's shape and type."""
-    if stream is None:
-        import torch
-        return torch.empty_like(t)
-    return _empty(stream, t.shape, t.dtype, t.device)
-
-
-def _rows(name: str, t):
-    """Rows, columns and CUDA device of the matrix that gives a call its sizes."""
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected two dimensions")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
-    return shape[0], shape[1], index
-
-
-def _state(t, shape: tuple, dtype, sequences: int, slots, resume, index: int):
-    """Addresses and slot count of the states' arguments."""
-    import torch
-    if t is None:
-        if slots is not None or resume is not None:
-            raise ValueError("slots and resume need a state")
-        return None, 0, None, None
-    count = t.shape[0] if t.dim() > 0 else 0
-    if slots is None and count < sequences:
-        raise ValueError(f"{sequences} sequences without slots, a state of {count}")
-    return (_dense("state", t, (count, *shape), dtype, index), count,
-            _dense("slots", slots, (sequences,), torch.int32, index),
-            _dense("resume", resume, (sequences,), torch.int32, index))
-
-
-def _sequences(sequences, offsets, index: int):
-    """Number of sequences and the offsets' address."""
-    import torch
-    if offsets is None:
-        return (1 if sequences is None else sequences), None
-    count = offsets.numel() - 1
-    if sequences is not None and sequences != count:
-        raise ValueError(f"{sequences} sequences, offsets for {count}")
-    return count, _dense("offsets", offsets, (count + 1,), torch.int32, index)
+def _load_ops():
+    """Imports the compiled calls (once)."""
+    global _ops
+    load()
+    import torch  # noqa: F401  (whose libraries the module is linked to)
+    try:
+        from . import _native
+    except ImportError as e:
+        raise LibraryMissing(f"{NATIVE_PATH}: {e}; build it with __graft_entry__.build()") from e
+    _native.set_error(LSTMError)
+    _ops = _native
+    return _ops
 
 
 def lstm_causal_conv(x, w, bias=None, *, silu: bool = True, sequences=None, offsets=None,
@@ -523,58 +434,15 @@ def lstm_causal_conv(x, w, bias=None, *, silu: bool = True, sequences=None, offs
     (None: `sequences` prompts of equal length, default one); state
     [slots, width - 1, channels] of x's type, slots and resume int32
     [sequences]."""
-    import torch
-    tokens, channels, index = _rows("x", x)
-    shape, dtype, code, width = (tokens, channels), x.dtype, _element_type(x), w.shape[-1]
-    count, offsets_at = _sequences(sequences, offsets, index)
-    state_at, state_slots, slots_at, resume_at = _state(state, (width - 1, channels), dtype, count,
-                                                        slots, resume, index)
-    if y is None:
-        y = _like(stream, x)
-    _check((_lib or load()).lstm_causal_conv(
-        x.data_ptr(), _matrix("x", x, shape, dtype, index), code, tokens, channels, width,
-        _dense("w", w, (channels, width), torch.float32, index),
-        _dense("bias", bias, (channels,), torch.float32, index), silu, count, offsets_at,
-        state_at, state_slots, slots_at, resume_at, y.data_ptr(),
-        _matrix("y", y, shape, dtype, index), _raw_stream(stream, index)))
-    return y
+    return (_ops or _load_ops()).causal_conv(x, w, bias, silu, sequences, offsets, state, slots,
+                                             resume, y, stream)
 
 
 def lstm_causal_conv_step(x, w, bias, state, *, silu: bool = True, slots=None, y=None,
                           stream=None):
     """The next token of every sequence, x [sequences, channels]; returns y
     (new unless given) and moves the state on.  Arguments as lstm_causal_conv."""
-    import torch
-    sequences, channels, index = _rows("x", x)
-    shape, dtype, code, width = (sequences, channels), x.dtype, _element_type(x), w.shape[-1]
-    state_at, state_slots, slots_at, _ = _state(state, (width - 1, channels), dtype, sequences,
-                                                slots, None, index)
-    if y is None:
-        y = _like(stream, x)
-    _check((_lib or load()).lstm_causal_conv_step(
-        x.data_ptr(), _matrix("x", x, shape, dtype, index), code, sequences, channels, width,
-        _dense("w", w, (channels, width), torch.float32, index),
-        _dense("bias", bias, (channels,), torch.float32, index), silu, state_at, state_slots,
-        slots_at, y.data_ptr(), _matrix("y", y, shape, dtype, index),
-        _raw_stream(stream, index)))
-    return y
-
-
-def _scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index):
-    """The arguments that both scan entry points begin with, up to softplus."""
-    import torch
-    rows, channels = shape
-    states = a.shape[-1]
-    dtype, f32, shared = u.dtype, torch.float32, (rows, groups * states)
-    return (u.data_ptr(), _matrix("u", u, shape, dtype, index),
-            dt.data_ptr(), _matrix("dt", dt, shape, dtype, index),
-            _dense("a", a, (channels, states), f32, index),
-            b.data_ptr(), _matrix("b", b, shared, dtype, index),
-            c.data_ptr(), _matrix("c", c, shared, dtype, index),
-            _dense("skip", skip, (channels,), f32, index),
-            None if z is None else z.data_ptr(),
-            0 if z is None else _matrix("z", z, shape, dtype, index),
-            _dense("dt_bias", dt_bias, (channels,), f32, index), softplus)
+    return (_ops or _load_ops()).causal_conv_step(x, w, bias, state, silu, slots, y, stream)
 
 
 def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, softplus: bool = True,
@@ -588,24 +456,8 @@ def lstm_selective_scan(u, dt, a, b, c, *, skip=None, z=None, dt_bias=None, soft
     int32 [sequences + 1] (None: `sequences` prompts of equal length, default
     one); state [slots, channels, states] fp32, slots and resume int32
     [sequences]."""
-    import torch
-    tokens, channels, index = _rows("u", u)
-    shape, code, states = (tokens, channels), _element_type(u), a.shape[-1]
-    count, offsets_at = _sequences(sequences, offsets, index)
-    state_at, state_slots, slots_at, resume_at = _state(state, (channels, states), torch.float32,
-                                                        count, slots, resume, index)
-    if y is None:
-        y = _like(stream, u)
-    lib = _lib or load()
-    size = lib.lstm_selective_scan_workspace(tokens, channels, states, groups, count,
-                                             offsets is None)
-    workspace = _empty(stream, (size,), torch.uint8, u.device) if size else None
-    _check(lib.lstm_selective_scan(
-        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index), code,
-        tokens, channels, states, groups, count, offsets_at, state_at, state_slots, slots_at,
-        resume_at, y.data_ptr(), _matrix("y", y, shape, u.dtype, index), _ptr(workspace), size,
-        _raw_stream(stream, index)))
-    return y
+    return (_ops or _load_ops()).selective_scan(u, dt, a, b, c, skip, z, dt_bias, softplus, groups,
+                                                sequences, offsets, state, slots, resume, y, stream)
 
 
 def lstm_selective_scan_workspace(tokens: int, channels: int, states: int, groups: int,
@@ -621,18 +473,8 @@ def lstm_selective_scan_step(u, dt, a, b, c, state, *, skip=None, z=None, dt_bia
     """The next token of every sequence, u, dt, z [sequences, channels]; returns
     y (new unless given) and moves the state on.  Arguments as
     lstm_selective_scan."""
-    import torch
-    sequences, channels, index = _rows("u", u)
-    shape, code, states = (sequences, channels), _element_type(u), a.shape[-1]
-    state_at, state_slots, slots_at, _ = _state(state, (channels, states), torch.float32, sequences,
-                                                slots, None, index)
-    if y is None:
-        y = _like(stream, u)
-    _check((_lib or load()).lstm_selective_scan_step(
-        *_scan_arguments(u, dt, a, b, c, skip, z, dt_bias, softplus, groups, shape, index), code,
-        sequences, channels, states, groups, state_at, state_slots, slots_at, y.data_ptr(),
-        _matrix("y", y, shape, u.dtype, index), _raw_stream(stream, index)))
-    return y
+    return (_ops or _load_ops()).selective_scan_step(u, dt, a, b, c, state, skip, z, dt_bias,
+                                                     softplus, groups, slots, y, stream)
 
 
 def lstm_residual_rms_norm(x, weight, eps: float, *, residual=None, residual_out=None,
@@ -645,55 +487,12 @@ def lstm_residual_rms_norm(x, weight, eps: float, *, residual=None, residual_out
     [rows, ceil(cols / group)] fp32 (group 0: one a row) make y * scales stand
     for the norm; else scales is None.  v is rounded to x's type (residual_out:
     where to, may be residual); None without a residual."""
-    import torch
-    rows, cols, index = _rows("x", x)
-    shape, dtype, code = (rows, cols), x.dtype, _element_type(x)
-    res_at = out_at = None
-    res_stride = out_stride = 0
-    if residual is not None:
-        res_at, res_stride = residual.data_ptr(), _matrix("residual", residual, shape, dtype, index)
-        if residual_out is None:
-            residual_out = _like(stream, x)
-        out_at = residual_out.data_ptr()
-        out_stride = _matrix("residual_out", residual_out, shape, dtype, index)
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    y_dtype = torch.float8_e4m3fn if quantize else dtype
-    if y is None:
-        y = _empty(stream, shape, y_dtype, x.device) if quantize else _like(stream, x)
-    scales_at = None
-    if quantize:
-        wide = (rows, -(-cols // group) if group > 0 else 1)
-        if scales is None:
-            scales = _empty(stream, wide, torch.float32, x.device)
-        scales_at = _dense("scales", scales, wide, torch.float32, index)
-    else:
-        scales = None
-    _check((_lib or load()).lstm_residual_rms_norm(
-        x.data_ptr(), _matrix("x", x, shape, dtype, index), res_at, res_stride, code,
-        _dense("weight", weight, (cols,), torch.float32, index), eps, rows, cols, out_at,
-        out_stride, y.data_ptr(), _matrix("y", y, shape, y_dtype, index),
-        LSTM_E4M3 if quantize else code, scales_at, group, _raw_stream(stream, index)))
-    return y, scales, residual_out
+    return (_ops or _load_ops()).residual_rms_norm(x, weight, eps, residual, residual_out,
+                                                   quantize, group, y, scales, stream)
 
 
 def lstm_token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = True, stream=None):
     """Log probabilities of tokens (int64 [rows]) under logits [rows, vocab];
     returns (logp, entropy, top_logp, top_ids): fp32 [rows], fp32 [rows], fp32
     and int64 [rows, top]; None for what is not asked for."""
-    import torch
-    rows, vocab, index = _rows("logits", logits)
-    device = logits.device
-    logp = h = top_logp = top_ids = None
-    if tokens is not None:
-        logp = _empty(stream, (rows,), torch.float32, device)
-    if entropy:
-        h = _empty(stream, (rows,), torch.float32, device)
-    if top > 0:
-        top_logp = _empty(stream, (rows, top), torch.float32, device)
-        top_ids = _empty(stream, (rows, top), torch.int64, device)
-    _check((_lib or load()).lstm_token_logprobs(
-        logits.data_ptr(), _matrix("logits", logits, (rows, vocab), logits.dtype, index),
-        _element_type(logits), rows, vocab, _dense("tokens", tokens, (rows,), torch.int64, index),
-        _ptr(logp), _ptr(h), top, _ptr(top_logp), _ptr(top_ids), _raw_stream(stream, index)))
-    return logp, h, top_logp, top_ids
+    return (_ops or _load_ops()).token_logprobs(logits, tokens, top, entropy, stream)

@@ -1,15 +1,19 @@
-"""Builds liblstmstack.so in-tree from csrc/*.cu for sm_103a.
+"""Builds liblstmstack.so in-tree from csrc/*.cu for sm_103a, and the Python
+module _native.so from csrc/*.cpp.
 
 Each translation unit compiles in parallel with nvcc into ``_build/`` at the
-repository root; the shared library is linked next to this file.  No cmake,
-no torch extension machinery: the library has a plain C ABI.
+repository root; both are linked next to this file.  No cmake, no torch
+extension machinery: the library has a plain C ABI, and the module, which
+takes torch tensors, is linked to the installed torch.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblstmstack.so")
+NATIVE = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]
@@ -28,8 +33,21 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
-def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+def _torch() -> str:
+    """Folder of the installed torch (found, not imported)."""
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _torch_flags():
+    torch = _torch()
+    home = os.path.dirname(os.path.dirname(_nvcc()))
+    paths = [os.path.join(torch, "include"), os.path.join(home, "include"),
+             sysconfig.get_paths()["include"]]
+    return [f for path in paths for f in ("-isystem", path)]
+
+
+def sources(ending: str = ".cu"):
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(ending))
 
 
 def _headers():
@@ -42,14 +60,23 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     newest_header = max(os.path.getmtime(h) for h in _headers())
+    # (another torch is another set of headers)
+    newest_torch = max(newest_header, os.path.getmtime(os.path.join(_torch(), "version.py")))
     jobs = []
-    objs = []
-    for src in sources():
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        objs.append(obj)
-        if (force or not os.path.exists(obj) or os.path.getmtime(obj) < os.path.getmtime(src)
-                or os.path.getmtime(obj) < newest_header):
-            jobs.append([nvcc, *ARCH, *FLAGS, *(extra or []), "-c", src, "-o", obj])
+
+    def objects(srcs, flags, newest):
+        objs = []
+        for src in srcs:
+            obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
+            objs.append(obj)
+            if (force or not os.path.exists(obj) or os.path.getmtime(obj) < os.path.getmtime(src)
+                    or os.path.getmtime(obj) < newest):
+                jobs.append([nvcc, *ARCH, *FLAGS, *flags, *(extra or []), "-c", src, "-o", obj])
+        return objs
+
+    objs = objects(sources(), [], newest_header)
+    kernels = len(jobs)
+    native = objects(sources(".cpp"), _torch_flags(), newest_torch)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -61,10 +88,18 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         for log in ex.map(run, jobs):
             if verbose and log:
                 print(log)
-    if force or jobs or not os.path.exists(LIB):
-        tmp = LIB + f".{os.getpid()}.tmp"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-        os.replace(tmp, LIB)
+    def link(out, args):
+        tmp = out + f".{os.getpid()}.tmp"
+        run([nvcc, *ARCH, "-shared", "-o", tmp, *args])
+        os.replace(tmp, out)
+
+    if force or kernels or not os.path.exists(LIB):
+        link(LIB, objs)
+    if force or len(jobs) > kernels or not os.path.exists(NATIVE):
+        # (torch's libraries are loaded before the module is)
+        link(NATIVE, [*native, "-L", PKG, "-llstmstack", "-Xlinker", "-rpath,$ORIGIN", "-L",
+                      os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                      "-lc10", "-lc10_cuda"])
     return LIB
 
 

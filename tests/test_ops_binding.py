@@ -1,0 +1,141 @@
+"""What binding.py's functions of include/lstm_ops.h refuse before the library
+is called, and how they take their arguments."""
+import inspect
+import sys
+import threading
+
+import pytest
+import torch
+
+from bidirectional_lstm_stack_gb300 import binding
+from bidirectional_lstm_stack_gb300 import build as build_mod
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build_mod.build()
+
+
+def _calls(m):
+    """Each function with m as the matrix that gives the call its sizes."""
+    v = torch.zeros(8)
+    return [lambda: binding.lstm_causal_conv(m, torch.zeros(8, 4)),
+            lambda: binding.lstm_causal_conv_step(m, torch.zeros(8, 4), None, torch.zeros(2, 3, 8)),
+            lambda: binding.lstm_selective_scan(m, m, torch.zeros(8, 16), m, m),
+            lambda: binding.lstm_selective_scan_step(m, m, torch.zeros(8, 16), m, m,
+                                                     torch.zeros(2, 8, 16)),
+            lambda: binding.lstm_residual_rms_norm(m, v, 1e-5),
+            lambda: binding.lstm_token_logprobs(m)]
+
+
+@pytest.mark.parametrize("function", range(6))
+@pytest.mark.parametrize("bad,error", [(torch.zeros(2, 8), ValueError), (torch.zeros(8), ValueError),
+                                       (torch.zeros(()), ValueError), (None, TypeError),
+                                       ([[0.0]], TypeError), (torch.zeros(1, 2, 8), ValueError)])
+def test_a_matrix_on_the_host_or_no_matrix_is_refused(function, bad, error):
+    with pytest.raises(error):
+        _calls(bad)[function]()
+
+
+def test_names_and_defaults():
+    for name in ("lstm_causal_conv", "lstm_causal_conv_step", "lstm_selective_scan",
+                 "lstm_selective_scan_step", "lstm_residual_rms_norm", "lstm_token_logprobs"):
+        f = getattr(binding, name)
+        assert "stream" in inspect.signature(f).parameters and f.__doc__
+        with pytest.raises(TypeError):
+            f()
+
+
+def test_a_module_that_is_not_built_is_missing(monkeypatch):
+    monkeypatch.setattr(binding, "_ops", None)
+    monkeypatch.delattr(sys.modules["bidirectional_lstm_stack_gb300"], "_native", raising=False)
+    monkeypatch.setitem(sys.modules, "bidirectional_lstm_stack_gb300._native", None)
+    with pytest.raises(binding.LibraryMissing):
+        binding.lstm_token_logprobs(torch.zeros(2, 8))
+
+
+@pytest.mark.gpu
+def test_arguments_that_are_wrong_beside_a_good_matrix():
+    x, w, v = torch.zeros(4, 8).cuda(), torch.zeros(8, 4).cuda(), torch.ones(8).cuda()
+    conv, norm, logp = (binding.lstm_causal_conv, binding.lstm_residual_rms_norm,
+                        binding.lstm_token_logprobs)
+    for call, error in [(lambda: conv(x, None), TypeError),
+                        (lambda: conv(x, torch.tensor(1.0).cuda()), ValueError),
+                        (lambda: conv(x, w.cpu()), ValueError),
+                        (lambda: conv(x, w, bias=[0.0] * 8), TypeError),
+                        (lambda: conv(x, w, sequences="1"), TypeError),
+                        (lambda: conv(x, w, sequences=1 << 40), ValueError),
+                        (lambda: conv(x, w, stream="0"), AttributeError),
+                        (lambda: conv(x, w, state=torch.tensor(0.0).cuda()), ValueError),
+                        (lambda: conv(x, w, offsets=torch.zeros(0, dtype=torch.int32).cuda()),
+                         binding.LSTMError),
+                        (lambda: conv(x.double(), w), ValueError),
+                        (lambda: conv(x, w, y=torch.zeros(4, 8)), ValueError),
+                        (lambda: norm(x, v, None), TypeError),
+                        (lambda: norm(x, v, "1"), TypeError),
+                        (lambda: norm(x, v, 1e-5, group=1 << 40, quantize=True), ValueError),
+                        (lambda: norm(x, v, 1e-5, residual=x.half()), ValueError),
+                        (lambda: logp(x, torch.zeros(4).cuda()), ValueError),
+                        (lambda: logp(x, top=1 << 40), ValueError)]:
+        with pytest.raises(error):
+            call()
+    y, scales, out = norm(x, v, 1)
+    assert scales is None and out is None and y.shape == x.shape
+    assert all(t is None for t in logp(x, entropy=False)[2:])
+
+
+@pytest.mark.gpu
+def test_given_outputs_are_what_is_returned():
+    x, w, v = torch.randn(4, 8).cuda(), torch.randn(8, 4).cuda(), torch.ones(8).cuda()
+    y = torch.empty_like(x)
+    got = binding.lstm_causal_conv(x, w, y=y)
+    assert got.data_ptr() == y.data_ptr() and torch.equal(y, binding.lstm_causal_conv(x, w))
+    r = torch.randn(4, 8).cuda()
+    expected = r + x
+    assert binding.lstm_residual_rms_norm(x, v, 1e-5, residual=r,
+                                          residual_out=r)[2].data_ptr() == r.data_ptr()
+    assert torch.equal(r, expected)
+
+
+@pytest.mark.gpu
+def test_calls_of_two_threads():
+    x, w = torch.randn(256, 64).cuda(), torch.randn(64, 4).cuda()
+    expected = binding.lstm_causal_conv(x, w)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        for _ in range(200):
+            y = binding.lstm_causal_conv(x, w, stream=stream)
+        stream.synchronize()
+        if not torch.equal(y, expected):
+            wrong.append(y)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+@pytest.mark.gpu
+def test_outputs_do_not_leak():
+    x, w = torch.randn(256, 64).cuda(), torch.randn(64, 4).cuda()
+    v = torch.ones(64).cuda()
+
+    def work():
+        binding.lstm_causal_conv(x, w)
+        binding.lstm_residual_rms_norm(x, v, 1e-5, residual=x, quantize=True)
+        binding.lstm_token_logprobs(x, top=3)
+        with pytest.raises(binding.LSTMError):
+            binding.lstm_causal_conv(x, w, sequences=3)  # (256 rows are no three equal prompts)
+
+    work()
+    before = torch.cuda.memory_allocated()
+    refs = sys.getrefcount(x), sys.getrefcount(None)
+    for _ in range(50):
+        work()
+    assert torch.cuda.memory_allocated() == before
+    assert sys.getrefcount(x) == refs[0] and abs(sys.getrefcount(None) - refs[1]) < 50
