@@ -11,19 +11,25 @@
 // first run is the only reader of its old state and the writer of its new one,
 // so a state can be updated in place.
 //
-// 12288 tokens x 4096 channels of bf16 in 24 prompts: 44 us, 4.6 TB/s of the
-// inputs and outputs, 68 % of the card's copy rate; the rest is the loads'
-// latency, which the registers of a window of W rows and its weights leave 24
-// warps an SM to cover.
+// 12288 tokens x 4096 channels of bf16 in 24 prompts: 37 us, 5.4 TB/s of the
+// inputs and outputs, 80 % of the card's copy rate; 4096 x 4096, which the L2
+// holds, 13.3.  What bounds it now is as much the instructions (without the
+// activation 36 and 11.5 us).  With rows loaded four ahead into registers
+// instead of a ring in shared memory, and conditions at every token, they
+// took 44 and 17.
 #include "ops.cuh"
 
 namespace lstm {
 namespace {
 
-constexpr int kAhead = 4;  // tokens loaded together, ahead of the four being worked on
+constexpr int kGroup = 4;  // tokens loaded and worked on together
+// Rows of a thread's ring; all but kGroup of them are on their way while it
+// works, 57 KB an SM of 16-bit types (12288 x 4096 bf16 37.4 us, 32 x 589 x 256
+// fp32 5.4; with 8 rows 38.1 and 5.7).
+constexpr int kRing = 12;
 // A thread's channels: four (of fp32 16 bytes, of 16-bit types 8).  Eight would
-// take 128 registers and leave a quarter of the threads to cover the loads
-// (12288 x 4096 bf16: 44 us with four, 57 with eight).
+// take 128 registers and leave a quarter of the threads (12288 x 4096 bf16,
+// before the ring: 44 us with four, 57 with eight).
 constexpr int kVector = 4;
 constexpr int kThreads = 128;
 
@@ -136,10 +142,21 @@ __device__ __forceinline__ Pack<T, V> zeros()
     return r;
 }
 
+template <typename T, int V>
+__device__ __forceinline__ void copy_async(Pack<T, V> *dst, const T *src)
+{
+    if constexpr (sizeof(Pack<T, V>) == 16)
+        ptx::cp_async_16(ptx::smem_u32(dst), src, 16);
+    else if constexpr (sizeof(Pack<T, V>) == 8)
+        ptx::cp_async_8(ptx::smem_u32(dst), src, 8);
+    else
+        ptx::cp_async_4(ptx::smem_u32(dst), src, 4);
+}
+
 // grid (tiles / blockDim.y, channel vectors / blockDim.x): thread (x, y) of a
 // block takes the channel vector x and the run y.
-template <typename T, int V, int W, int RUN>
-__global__ void __launch_bounds__(kThreads, 6) conv_kernel(ConvArgs a, int tiles)
+template <typename T, int V, int W, int RUN, bool SILU>
+__global__ void __launch_bounds__(kThreads, 7) conv_kernel(ConvArgs a, int tiles)
 {
     const int d = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     const int number = blockIdx.x * blockDim.y + threadIdx.y;
@@ -195,35 +212,89 @@ __global__ void __launch_bounds__(kThreads, 6) conv_kernel(ConvArgs a, int tiles
     const int end = min(t0 + RUN, length);
     x += t0 * a.x_stride;
     y += t0 * a.y_stride;
-    // the next rows are loaded before the present ones are worked on
-    Pack<T, V> rows[kAhead], next[kAhead];
+    // One output, of the row given; the window moves on.
+    const auto token = [&](const Pack<T, V> &row) {
+        read<T, V>(row, line[W - 1]);
+        store_pack<T, V>(y, convolve<T, V, W>(line, taps, SILU));
+        y += a.y_stride;
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-        if (t0 + j < end)
-            rows[j] = load_pack<T, V>(x + j * a.x_stride);
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < Lane<V>::kCount; ++i)
+                line[k][i] = line[k + 1][i];
+    };
+    if constexpr (sizeof(Pack<T, V>) >= 4) {
+        // Rows come through a ring of the thread's own places in shared memory,
+        // which holds more of them than registers could: no barriers, and a
+        // place is written again only after the row in it has been used.
+        constexpr int kRows = RUN < kRing ? RUN : kRing;
+        __shared__ Pack<T, V> ring[kRows][kThreads];
+        const int me = threadIdx.y * blockDim.x + threadIdx.x;
+        int fetched = t0, into = 0, from = 0;
+        const auto fetch = [&] {
+            const int left = end - fetched;
+            if (left >= kGroup) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    copy_async(&ring[into + j][me], x);
+                    x += a.x_stride;
+                }
+            } else {
 #pragma unroll 1
-    for (int t = t0; t < end; t += kAhead) {
-        x += kAhead * a.x_stride;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (t + kAhead + j < end)
-                next[j] = load_pack<T, V>(x + j * a.x_stride);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (t + j < end) {
-                read<T, V>(rows[j], line[W - 1]);
-                store_pack<T, V>(y, convolve<T, V, W>(line, taps, a.silu));
+                for (int j = 0; j < left; ++j) {
+                    copy_async(&ring[into + j][me], x);
+                    x += a.x_stride;
+                }
             }
-            y += a.y_stride;
+            ptx::cp_async_commit();
+            fetched += kGroup;
+            into = into + kGroup < kRows ? into + kGroup : 0;
+        };
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k)
+        for (int g = 1; g < kRows / kGroup; ++g)
+            fetch();
+#pragma unroll 1
+        for (int t = t0; t < end; t += kGroup) {
+            fetch();
+            ptx::cp_async_wait<kRows / kGroup - 1>();
+            if (t + kGroup <= end) {
+                Pack<T, V> rows[kGroup];
 #pragma unroll
-                for (int i = 0; i < Lane<V>::kCount; ++i)
-                    line[k][i] = line[k + 1][i];
+                for (int j = 0; j < kGroup; ++j)
+                    rows[j] = ring[from + j][me];
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    token(rows[j]);
+            } else {
+#pragma unroll 1
+                for (int j = 0; t + j < end; ++j)
+                    token(ring[from + j][me]);
+            }
+            from = from + kGroup < kRows ? from + kGroup : 0;
         }
+    } else {
+        // (no asynchronous copy is this small) the next rows are loaded before
+        // the present ones are worked on
+        Pack<T, V> rows[kGroup], next[kGroup];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            rows[j] = next[j];
+        for (int j = 0; j < kGroup; ++j)
+            if (t0 + j < end)
+                rows[j] = load_pack<T, V>(x + j * a.x_stride);
+#pragma unroll 1
+        for (int t = t0; t < end; t += kGroup) {
+            x += kGroup * a.x_stride;
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (t + kGroup + j < end)
+                    next[j] = load_pack<T, V>(x + j * a.x_stride);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (t + j < end)
+                    token(rows[j]);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                rows[j] = next[j];
+        }
     }
 }
 
@@ -278,7 +349,8 @@ int launch_run(const ConvArgs &a, cudaStream_t stream)
     const int st = check_launch_injection("lstm_causal_conv");
     if (st != LSTM_OK)
         return st;
-    conv_kernel<T, V, W, RUN><<<dim3(static_cast<unsigned>(grid), columns), block, 0, stream>>>(
+    const auto kernel = a.silu ? conv_kernel<T, V, W, RUN, true> : conv_kernel<T, V, W, RUN, false>;
+    kernel<<<dim3(static_cast<unsigned>(grid), columns), block, 0, stream>>>(
         a, static_cast<int>(tiles));
     return cuda_status(cudaGetLastError(), "lstm_causal_conv launch");
 }
@@ -301,11 +373,12 @@ int launch(const ConvArgs &a, bool step, cudaStream_t stream)
     }
     // Long runs find their sequence and read the rows before them less often;
     // short ones make more threads where there is little to do.  Measured in
-    // bf16, runs of 64, 16 and 4 tokens: 12288 x 4096 44, 50 and 98 us, 2048 x
-    // 2048 14, 6 and 9 us, 512 x 1024 14, 5 and 3 us.
+    // bf16, runs of 32, 16 and 4 tokens (64): 12288 x 4096 37, 42 and 79 us (38),
+    // 4096 x 4096 13.4, 14.6 and 25 us (14.4), 2048 x 2048 5.6, 5.1 and 6.7 us
+    // (6.9), 512 x 1024 4.5, 3.5 and 2.9 us (6.6).
     const long long vector_tokens = static_cast<long long>(vectors) * a.seq.tokens;
     if (vector_tokens >= 1 << 21)
-        return launch_run<T, V, W, 64>(a, stream);
+        return launch_run<T, V, W, 32>(a, stream);
     if (vector_tokens >= 1 << 18)
         return launch_run<T, V, W, 16>(a, stream);
     return launch_run<T, V, W, 4>(a, stream);
