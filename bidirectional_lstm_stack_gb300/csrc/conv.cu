@@ -4,8 +4,8 @@
 //   y[t][d] = act(bias[d] + sum_k w[d][k] x[t - (W-1) + k][d]),  W <= 4
 //
 // Memory-bound: a token's channel costs 2 W + 5 operations and moves two
-// elements.  A thread owns four neighbouring channels (or one, where rows are
-// not 16-byte aligned) and a run of RUN tokens: it slides the window through
+// elements.  A thread owns four neighbouring channels (or two or one, where
+// rows are not aligned) and a run of RUN tokens: it slides the window through
 // registers, so each input is loaded once but for the W - 1 rows that a run
 // reads from the one before it.  Runs never cross sequences, and a sequence's
 // first run is the only reader of its old state and the writer of its new one,
@@ -338,11 +338,12 @@ int launch_run(const ConvArgs &a, cudaStream_t stream)
 {
     const int vectors = (a.channels + V - 1) / V;
     const long long tiles = tiles_bound(a.seq.tokens, a.seq.count, RUN);
-    // narrow rows: several runs to a block, so that its threads have work
-    const int across = vectors >= kThreads ? kThreads : (vectors + 31) / 32 * 32;
+    // a row's vectors in equal parts of at most kThreads, and of narrow rows
+    // several runs to a block, so that its threads have work
+    const int columns = (vectors + kThreads - 1) / kThreads;
+    const int across = (vectors + columns - 1) / columns;
     const dim3 block(across, kThreads / across);
     const long long grid = (tiles + block.y - 1) / block.y;
-    const int columns = (vectors + across - 1) / across;
     if (tiles > 0x7fffffffll || columns > 65535)
         return fail(LSTM_E_OVERFLOW, "lstm_causal_conv: %d tokens, %d sequences, %d channels",
                     a.seq.tokens, a.seq.count, a.channels);
@@ -375,35 +376,50 @@ int launch(const ConvArgs &a, bool step, cudaStream_t stream)
     // short ones make more threads where there is little to do.  Measured in
     // bf16, runs of 32, 16 and 4 tokens (64): 12288 x 4096 37, 42 and 79 us (38),
     // 4096 x 4096 13.4, 14.6 and 25 us (14.4), 2048 x 2048 5.6, 5.1 and 6.7 us
-    // (6.9), 512 x 1024 4.5, 3.5 and 2.9 us (6.6).
+    // (6.9), 512 x 1024 4.5, 3.5 and 2.9 us (6.6); between 16 and 4 1024 x 2048
+    // 4.1 and 4.4 us, 1024 x 1024 3.8 and 3.3 us.
     const long long vector_tokens = static_cast<long long>(vectors) * a.seq.tokens;
     if (vector_tokens >= 1 << 21)
         return launch_run<T, V, W, 32>(a, stream);
-    if (vector_tokens >= 1 << 18)
+    if (vector_tokens >= 1 << 19)
         return launch_run<T, V, W, 16>(a, stream);
     return launch_run<T, V, W, 4>(a, stream);
+}
+
+template <typename T, int V>
+int launch_width(const ConvArgs &a, int width, bool step, cudaStream_t stream)
+{
+    switch (width) {
+    case 2:
+        return launch<T, V, 2>(a, step, stream);
+    case 3:
+        return launch<T, V, 3>(a, step, stream);
+    default:
+        return launch<T, V, 4>(a, step, stream);
+    }
 }
 
 template <typename T>
 int launch_typed(const ConvArgs &a, int width, bool step, cudaStream_t stream)
 {
-    constexpr int V = kVector;
     const int size = sizeof(T);
     // whole vectors where every row of x, y and the states, and the weights,
-    // start on one; otherwise a channel at a time
-    const bool wide = a.channels % V == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 &&
-                      (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0 &&
-                      rows_aligned(a.x, a.x_stride, size) &&
-                      rows_aligned(a.y, a.y_stride, size) &&
-                      (!a.state || rows_aligned(a.state, a.channels, size));
-    switch (width) {
-    case 2:
-        return wide ? launch<T, V, 2>(a, step, stream) : launch<T, 1, 2>(a, step, stream);
-    case 3:
-        return wide ? launch<T, V, 3>(a, step, stream) : launch<T, 1, 3>(a, step, stream);
-    default:
-        return wide ? launch<T, V, 4>(a, step, stream) : launch<T, 1, 4>(a, step, stream);
-    }
+    // start on one; else pairs of 16-bit channels, the least that an asynchronous
+    // copy takes; else a channel at a time (8192 rows of bf16: 2044 channels 14 us,
+    // 2046 15 us in pairs and 24 singly, 2047 24 us)
+    const auto fits = [&](int v) {
+        return a.channels % v == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 &&
+               (v < 4 || (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) &&
+               rows_aligned(a.x, a.x_stride, size, v * size) &&
+               rows_aligned(a.y, a.y_stride, size, v * size) &&
+               (!a.state || rows_aligned(a.state, a.channels, size, v * size));
+    };
+    if (fits(kVector))
+        return launch_width<T, kVector>(a, width, step, stream);
+    if constexpr (sizeof(T) == 2)
+        if (fits(2))
+            return launch_width<T, 2>(a, width, step, stream);
+    return launch_width<T, 1>(a, width, step, stream);
 }
 
 int check_conv(const char *what, ConvArgs &a, int dtype, int rows, int width, int *device)

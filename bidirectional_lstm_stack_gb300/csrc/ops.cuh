@@ -38,10 +38,10 @@ inline int check_matrix(const char *what, const char *name, const void *p, long 
     return LSTM_OK;
 }
 
-// Whether every row of the matrix starts on a 16-byte boundary.
-inline bool rows_aligned(const void *p, long long stride, int size)
+// Whether every row of the matrix starts on a multiple of `bytes` (a power of two).
+inline bool rows_aligned(const void *p, long long stride, int size, int bytes = 16)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * size % 16 == 0;
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && stride * size % bytes == 0;
 }
 
 inline int check_sequences(const char *what, int tokens, int sequences, const int *offsets)

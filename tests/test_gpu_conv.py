@@ -116,6 +116,35 @@ def test_prompt_then_steps_equal_one_prompt():
     assert torch.equal(torch.cat(parts), whole)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels", [60, 62, 63])
+@pytest.mark.parametrize("offset", [0, 1, 2, 4])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_rows_of_every_alignment(dtype, channels, offset, width):
+    """Columns of a wider matrix as input and as output, tokens and steps."""
+    g = gen(channels + offset)
+    wide = normal(g, 45, 136, dtype=DTYPES[dtype])
+    out = torch.zeros(45, 136, device="cuda", dtype=DTYPES[dtype])
+    x, y = wide[:, offset:offset + channels], out[:, 68 + offset:68 + offset + channels]
+    w, b = normal(g, channels, width, scale=0.5), normal(g, channels, scale=0.3)
+    state = normal(g, 45, width - 1, channels, dtype=DTYPES[dtype])
+    before = f64(state)
+    binding.lstm_causal_conv(x, w, b, y=y, state=state, resume=torch.ones(1, dtype=torch.int32,
+                                                                          device="cuda"))
+    ref, new, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True, [(0, 45)], before, None, [1])
+    assert_close(y, ref, bound, dtype, "y")
+    np.testing.assert_array_equal(f64(state), new)
+    rest = out.clone()
+    rest[:, 68 + offset:68 + offset + channels] = 0
+    assert not rest.any()
+    before = f64(state)
+    binding.lstm_causal_conv_step(x, w, b, state, y=y)
+    ref, new, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True,
+                                         [(i, i + 1) for i in range(45)], before, None, [1] * 45)
+    assert_close(y, ref, bound, dtype, "y of the step")
+    np.testing.assert_array_equal(f64(state), new)
+
+
 def test_on_another_stream():
     g = gen(2)
     x, w = normal(g, 300, 128), normal(g, 128, 4)
