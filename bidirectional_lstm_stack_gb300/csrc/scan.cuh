@@ -40,7 +40,8 @@ struct ScanArgs {
 // in tile_owner's numbering).  The first pass leaves, per span, channel and
 // state, the state after the span when it starts from zeros (the sequence's
 // first span: from its own start), and per span and channel the sum of the
-// span's step sizes.  A sequence's last span has nothing to leave; its place
+// span's step sizes; carry_kernel joins them into the state that each span
+// starts from.  A sequence's last span has nothing to leave; its place
 // holds the state that the sequence starts from, which the second pass may
 // not read where it is kept, because the last span replaces it.
 //
