@@ -97,7 +97,15 @@ template <int V, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs &a, int d, Taps<V, W> &taps)
 {
     float w[V * W], bias[V] = {};
-    load_weights<V * W>(a.w + static_cast<long long>(d) * W, w);
+    const float *from = a.w + static_cast<long long>(d) * W;
+    if constexpr (V > 1) {
+        load_weights<V * W>(from, w);
+    } else {
+        // taken for weights at any element as well, so no vector of a channel's taps
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            w[k] = __ldg(from + k);
+    }
     if (a.bias)
         load_weights<V>(a.bias + d, bias);
 #pragma unroll
@@ -405,7 +413,8 @@ int launch_typed(const ConvArgs &a, int width, bool step, cudaStream_t stream)
     const int size = sizeof(T);
     // whole vectors where every row of x, y and the states, and the weights,
     // start on one; else pairs of 16-bit channels, the least that an asynchronous
-    // copy takes; else a channel at a time (8192 rows of bf16: 2044 channels 14 us,
+    // copy takes; else a channel at a time, with nothing on more than an element's
+    // boundary (8192 rows of bf16: 2044 channels 14 us,
     // 2046 15 us in pairs and 24 singly, 2047 24 us)
     const auto fits = [&](int v) {
         return a.channels % v == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 &&

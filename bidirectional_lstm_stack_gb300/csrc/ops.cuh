@@ -223,7 +223,7 @@ __device__ __forceinline__ Pack<T, V> pack(const float (&f)[V])
     return r;
 }
 
-// V consecutive fp32 weights (16-byte aligned where V > 1).
+// V consecutive fp32 weights, 16-byte aligned where V is a multiple of 4.
 template <int V>
 __device__ __forceinline__ void load_weights(const float *p, float (&w)[V])
 {

@@ -32,6 +32,15 @@ def slice_of(t, pad_left, pad_right):
     return view
 
 
+def at_element(t, offset):
+    """The same values, densely packed, `offset` elements into an allocation that is
+    NaN elsewhere."""
+    flat = torch.full((t.numel() + 8,), float("nan"), dtype=t.dtype, device=t.device)
+    view = flat[offset:offset + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
 def f64(t):
     return None if t is None else t.detach().cpu().double().numpy()
 

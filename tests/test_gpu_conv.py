@@ -7,7 +7,7 @@ import torch
 
 from bidirectional_lstm_stack_gb300 import binding
 from oracle import ops as oracle
-from ops_util import DTYPES, assert_close, f64, gen, normal, slice_of
+from ops_util import DTYPES, assert_close, at_element, f64, gen, normal, slice_of
 
 pytestmark = pytest.mark.gpu
 
@@ -139,6 +139,29 @@ def test_rows_of_every_alignment(dtype, channels, offset, width):
     assert not rest.any()
     before = f64(state)
     binding.lstm_causal_conv_step(x, w, b, state, y=y)
+    ref, new, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True,
+                                         [(i, i + 1) for i in range(45)], before, None, [1] * 45)
+    assert_close(y, ref, bound, dtype, "y of the step")
+    np.testing.assert_array_equal(f64(state), new)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("width", [2, 3, 4])
+@pytest.mark.parametrize("channels", [64, 62, 63])
+def test_weights_at_any_element(dtype, offset, width, channels):
+    """Weights and bias that are views into a larger buffer of parameters."""
+    g = gen(channels + offset)
+    x = normal(g, 45, channels, dtype=DTYPES[dtype])
+    w = at_element(normal(g, channels, width, scale=0.5), offset)
+    b = at_element(normal(g, channels, scale=0.3), (offset + 1) % 4)
+    assert w.data_ptr() % 16 == 4 * offset
+    y = binding.lstm_causal_conv(x, w, b)
+    ref, _, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True, [(0, 45)])
+    assert_close(y, ref, bound, dtype, "y")
+    state = normal(g, 45, width - 1, channels, dtype=DTYPES[dtype])
+    before = f64(state)
+    y = binding.lstm_causal_conv_step(x, w, b, state)
     ref, new, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True,
                                          [(i, i + 1) for i in range(45)], before, None, [1] * 45)
     assert_close(y, ref, bound, dtype, "y of the step")
