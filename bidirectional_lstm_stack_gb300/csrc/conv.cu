@@ -499,6 +499,9 @@ extern "C" int lstm_causal_conv_step(const void *x, long long x_stride, int dtyp
 {
     if (!state)
         return fail(LSTM_E_INVALID, "lstm_causal_conv_step: state is null");
+    const int st = check_sequences("lstm_causal_conv_step", sequences, sequences, nullptr);
+    if (st != LSTM_OK)
+        return st;
     ConvArgs a = {x, x_stride, w, bias, y, y_stride, state, {nullptr, sequences, 1, sequences},
                   {slots, nullptr, state_slots}, channels, silu != 0};
     return conv("lstm_causal_conv_step", a, dtype, sequences, width, true, stream);

@@ -44,12 +44,19 @@ inline bool rows_aligned(const void *p, long long stride, int size, int bytes = 
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0 && stride * size % bytes == 0;
 }
 
+// The most tokens and sequences of a call.  Kernels count both in 32 bits: token
+// numbers a tile beyond the last, the sum of two sequence numbers (tile_owner's
+// bisection) and a sequence number some grids beyond the last must stay below 2^31.
+constexpr int kMostTokens = 0x7fffff00;
+constexpr int kMostSequences = LSTM_MAX_SEQUENCES;
+
 inline int check_sequences(const char *what, int tokens, int sequences, const int *offsets)
 {
     if (tokens < 0 || sequences < 0 || (tokens > 0 && sequences == 0))
         return fail(LSTM_E_INVALID, "%s: %d tokens, %d sequences", what, tokens, sequences);
-    if (tokens > 0x7fffff00)  // (token numbers a tile beyond the last still count)
-        return fail(LSTM_E_OVERFLOW, "%s: %d tokens", what, tokens);
+    if (tokens > kMostTokens || sequences > kMostSequences)
+        return fail(LSTM_E_OVERFLOW, "%s: %d tokens, %d sequences (at most %d, %d)", what, tokens,
+                    sequences, kMostTokens, kMostSequences);
     if (!offsets && sequences > 0 && tokens % sequences)
         return fail(LSTM_E_LENGTH,
                     "%s: %d tokens are no multiple of %d sequences (and no offsets are given)", what,

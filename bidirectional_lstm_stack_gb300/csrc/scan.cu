@@ -219,7 +219,7 @@ extern "C" size_t lstm_selective_scan_workspace(int tokens, int channels, int st
                                                 int sequences, int equal_lengths)
 {
     if (tokens < 0 || channels <= 0 || states <= 0 || states > LSTM_SCAN_MAX_STATES ||
-        groups <= 0 || sequences <= 0)
+        groups <= 0 || sequences <= 0 || tokens > kMostTokens || sequences > kMostSequences)
         return 0;
     return make_plan(tokens, channels, states, groups, sequences, equal_lengths != 0).bytes;
 }
@@ -257,6 +257,9 @@ extern "C" int lstm_selective_scan_step(const void *u, long long u_stride, const
 {
     if (!state)
         return fail(LSTM_E_INVALID, "lstm_selective_scan_step: state is null");
+    const int st = check_sequences("lstm_selective_scan_step", sequences, sequences, nullptr);
+    if (st != LSTM_OK)
+        return st;
     ScanArgs p = {u, u_stride, dt, dt_stride, a, b, b_stride, c, c_stride, skip, z, z_stride,
                   dt_bias, softplus != 0, channels, states, groups, state,
                   {nullptr, sequences, 1, sequences}, {slots, nullptr, state_slots}, y, y_stride};

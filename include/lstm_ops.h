@@ -28,7 +28,8 @@
  * (device int32 [sequences + 1], not decreasing, from 0 to tokens; bounds
  * outside 0..tokens are clamped), or with offsets NULL every sequence has
  * tokens / sequences rows (tokens must be a multiple of sequences).  Lengths
- * may be zero.
+ * may be zero.  A call has at most LSTM_MAX_SEQUENCES sequences and 2^31 - 256
+ * tokens (more: LSTM_E_OVERFLOW).
  *
  * States.  A pool of `state_slots` states holds what a sequence needs to go
  * on with its next tokens.  Sequence s has slot slots[s] (device int32
@@ -56,6 +57,7 @@ enum {
     LSTM_E4M3 = 3 /* 8 bits, 4 of exponent; lstm_residual_rms_norm's output only */
 };
 
+#define LSTM_MAX_SEQUENCES (1 << 30)
 #define LSTM_CONV_MAX_WIDTH 4
 #define LSTM_SCAN_MAX_STATES 128
 #define LSTM_TOP_MAX 32

@@ -119,5 +119,37 @@ def test_very_many_tokens(lib):
     assert _scan(lib, tokens=0x7fffffff) == binding.LSTM_E_OVERFLOW
 
 
+def _conv_step(lib, sequences):
+    return lib.lstm_causal_conv_step(64, 16, 0, sequences, 16, 4, 64, None, 1, 64, 8, None, 64, 16,
+                                     None)
+
+
+def _scan_step(lib, sequences):
+    return lib.lstm_selective_scan_step(64, 16, 64, 16, 64, 64, 8, 64, 8, None, None, 0, None, 1, 0,
+                                        sequences, 16, 8, 1, 64, 8, None, 64, 16, None)
+
+
+MOST = 1 << 30
+
+
+@pytest.mark.parametrize("call", [
+    lambda lib, n: _conv(lib, tokens=n, sequences=n),
+    lambda lib, n: _conv(lib, tokens=4, sequences=n, offsets=64),
+    lambda lib, n: _scan(lib, tokens=n, sequences=n), _conv_step, _scan_step],
+    ids=["conv", "conv with offsets", "scan", "conv step", "scan step"])
+def test_very_many_sequences(lib, call):
+    """Sequence numbers are added up and stepped over in 32 bits: beyond 2^30 the search for a
+    tile's sequence would go negative and not end, next to 2^31 a step's rows would."""
+    for n in (MOST + 1, 0x7fffffff):
+        assert call(lib, n) == binding.LSTM_E_OVERFLOW
+        assert f"{n} sequences" in binding.lstm_stack_last_error()
+    assert call(lib, MOST) != binding.LSTM_E_OVERFLOW  # (made-up pointers: refused for those)
+    assert call(lib, -1) == INVALID
+
+
+def test_workspace_of_sizes_that_are_refused(lib):
+    assert binding.lstm_selective_scan_workspace(MOST + 1, 64, 16, 1, MOST + 1, False) == 0
+
+
 def test_timeout_hook_refuses_limits_above_two_seconds(lib):
     assert lib.lstm_test_scan_step_timeout(1, 2000001, 0) == INVALID
