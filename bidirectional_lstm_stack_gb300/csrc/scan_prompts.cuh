@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
         for (int j = 0; j < kTokens; ++j) {
             Pair even = 0, odd = 0;
             if (FINAL && (G == 1 || n0 == 0))
-                even = mul2(skip, in[j]);
+                even = p.skip ? mul2(skip, in[j]) : 0;  // (0 times an infinity is no 0)
 #pragma unroll
             for (int n = 0; n < NS; n += 2) {
                 const ulonglong2 bn = *reinterpret_cast<const ulonglong2 *>(&st.b[t + j][n0_staged + n]);

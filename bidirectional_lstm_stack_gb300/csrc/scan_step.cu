@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs p)
         for (int m = 1; m < L; m <<= 1)
             v += __shfl_xor_sync(0xffffffffu, v, m);
         if (live && n0 == 0) {
-            v = fmaf(skip, ut, v);
+            if (p.skip)  // (0 times an infinity is no 0)
+                v = fmaf(skip, ut, v);
             if (p.z)
                 v *= silu(Elem<T>::get(x.z));
             static_cast<T *>(p.y)[s * p.y_stride + d] = Elem<T>::put(v);
@@ -284,7 +285,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_tiles_kernel(ScanArgs p, u
         for (int m = 1; m < L; m <<= 1)
             out += __shfl_xor_sync(0xffffffffu, out, m);
         if (live && n0 == 0) {
-            out = fmaf(skip, ut, out);
+            if (p.skip)
+                out = fmaf(skip, ut, out);
             if (z)
                 out *= silu(Elem<T>::get(x.z));
             *y = Elem<T>::put(out);

@@ -161,6 +161,46 @@ def test_step_sizes_far_from_zero():
     _check("f32", [40], 32, scale=20.0)
 
 
+def _check_infinities(dtype, channels, states, tokens, step, skip, least=-8.0, at=(5, 9), gated=False):
+    """An infinite input of two channels against the definition: b and c positive, so that the
+    infinities of its states add up to one.  Everything else stays finite."""
+    v = _inputs(dtype, tokens, channels, states)
+    v["u"][at[0], 3 % channels], v["u"][at[1], 17 % channels] = float("inf"), float("-inf")
+    v["a"].clamp_(min=least)
+    v["b"].abs_()
+    v["c"].abs_()
+    v["skip"] = v["skip"].abs() + 0.1 if skip else None
+    v["z"] = v["z"].abs() + 0.1 if gated else None
+    state = normal(gen(3), tokens if step else 1, channels, states)
+    before = f64(state)
+    call = binding.lstm_selective_scan_step if step else binding.lstm_selective_scan
+    first = [v[k] for k in ("u", "dt", "a", "b", "c")] + ([state] if step else [])
+    y = call(*first, skip=v["skip"], z=v["z"], **({} if step else {"state": state}))
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, new, bound, new_bound = oracle.selective_scan(
+            *(f64(v[k]) for k in ("u", "dt", "a", "b", "c", "skip", "z")), None, True, 1,
+            [(t, t + 1) for t in range(tokens)] if step else [(0, tokens)], before, step=step)
+    assert np.isposinf(ref).any() and np.isneginf(ref).any() and not np.isnan(ref).any()
+    for got, expected, off, t in ((y, ref, bound, dtype), (state, new, new_bound, "f32")):
+        finite = np.isfinite(expected)
+        np.testing.assert_array_equal(f64(got)[~finite], expected[~finite])
+        assert_close(torch.where(torch.from_numpy(finite), got.cpu(), torch.zeros_like(got).cpu()),
+                     np.where(finite, expected, 0.0), np.where(finite, off, 0.0), t)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels,states", [(40, 4), (40, 16), (40, 128)])
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("skip", [False, True])
+def test_an_infinite_input_stays_an_infinity(dtype, channels, states, step, skip):
+    _check_infinities(dtype, channels, states, 24, step, skip)
+
+
+@pytest.mark.parametrize("skip", [False, True])
+def test_an_infinite_input_in_a_large_batch_of_steps(skip):
+    _check_infinities("bf16", 128, 16, 300, True, skip, gated=True)
+
+
 def test_other_rows_are_left_alone():
     y = torch.full((20, 33), 7.0, device="cuda")
     v = _inputs("f32", 20, 33, 16)
