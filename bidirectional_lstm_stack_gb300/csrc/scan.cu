@@ -88,8 +88,9 @@ Plan make_plan(int tokens, int channels, int states, int groups, int sequences, 
         r.lanes = 1;
         while (r.states * r.lanes < states)
             r.lanes *= 2;
-        // no more than half of the padded states unused, and at most 4 lanes
-        // of fewer than 16 states (16 of 4 would leave no channels to a block)
+        // no more than half of the places unused (place_state relies on it), and
+        // at most 4 lanes of fewer than 16 states (16 of 4 would leave no channels
+        // to a block)
         if (r.states >= 2 * states && r.states > 4)
             continue;
         if (r.lanes > 4 && r.states < 16)

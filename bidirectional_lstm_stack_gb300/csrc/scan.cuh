@@ -88,6 +88,21 @@ int launch_scan_step(const ScanArgs &p, int dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
 
+// The prompts' lanes have places for a power of two of states, at most twice as
+// many as there are (four for a single one).  The places beyond the last state
+// hold the first ones again, and a state's output is shared out evenly among its
+// places, by halves (quarters), which is exact.  (Zeros in them would be NaN after
+// an infinite input.)  The state of place n:
+__device__ __forceinline__ int place_state(int n, int states)
+{
+    return n < states ? n : states > 1 ? n - states : 0;
+}
+// 1 / the number of places of place n's state, of `places` in all.
+__device__ __forceinline__ float place_share(int n, int states, int places)
+{
+    return states == 1 ? 1.0f / places : place_state(n, states) + states < places ? 0.5f : 1.0f;
+}
+
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], and
 // log(1 + e) = e q(e) with q of degree 8, fitted by least squares whose
 // weights are moved to where the relative error is largest (Lawson's method)

@@ -106,20 +106,19 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
     Pair h[NS], a[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        const bool in = n0 + n < p.states;
-        a[n] = make_pair(
-            in ? kLog2e * __ldg(p.a + static_cast<long long>(d0) * p.states + n0 + n) : 0.0f,
-            in ? kLog2e * __ldg(p.a + static_cast<long long>(d1) * p.states + n0 + n) : 0.0f);
+        const int k = place_state(n0 + n, p.states);
+        a[n] = make_pair(kLog2e * __ldg(p.a + static_cast<long long>(d0) * p.states + k),
+                         kLog2e * __ldg(p.a + static_cast<long long>(d1) * p.states + k));
         h[n] = 0;
     }
-    float *state0 = p.state + (static_cast<long long>(slot) * p.channels + d0) * p.states + n0;
-    float *state1 = p.state + (static_cast<long long>(slot) * p.channels + d1) * p.states + n0;
+    float *state0 = p.state + (static_cast<long long>(slot) * p.channels + d0) * p.states;
+    float *state1 = p.state + (static_cast<long long>(slot) * p.channels + d1) * p.states;
     const auto start_from_state = [&]() {
         if (quads) {
 #pragma unroll
             for (int n = 0; n < NS / 4 * 4; n += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(state0 + n);
-                const float4 y = *reinterpret_cast<const float4 *>(state1 + n);
+                const float4 x = *reinterpret_cast<const float4 *>(state0 + n0 + n);
+                const float4 y = *reinterpret_cast<const float4 *>(state1 + n0 + n);
                 h[n] = make_pair(x.x, y.x);
                 h[n + 1] = make_pair(x.y, y.y);
                 h[n + 2] = make_pair(x.z, y.z);
@@ -127,9 +126,10 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
             }
         } else {
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-                if (n0 + n < p.states)
-                    h[n] = make_pair(state0[n], state1[n]);
+            for (int n = 0; n < NS; ++n) {
+                const int k = place_state(n0 + n, p.states);
+                h[n] = make_pair(state0[k], state1[k]);
+            }
         }
     };
     // staging: u, dt and z as they are, asynchronously; b and c as fp32
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
     const T *z = FINAL && p.z ? static_cast<const T *>(p.z) + c0 : nullptr;
     const T *b = static_cast<const T *>(p.b) + group * p.states;
     const T *c = static_cast<const T *>(p.c) + group * p.states;
-    // a thread's k-th b and c: row fetch_t + row(k), column fetch_n + col(k)
+    // a thread's k-th b and c: row fetch_t + row(k), place fetch_n + col(k)
     constexpr int kFetchRows = kScanThreads / kPadded;
     constexpr int kWide = kPadded / kScanThreads > 0 ? kPadded / kScanThreads : 1;
     const auto row = [](int k) { return kFetchRows ? k * kFetchRows : k / kWide; };
@@ -180,14 +180,15 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
                 }
             }
         }
-        const T *from_b = b + (t0 + fetch_t) * p.b_stride + fetch_n;
-        const T *from_c = c + (t0 + fetch_t) * p.c_stride + fetch_n;
+        const T *from_b = b + (t0 + fetch_t) * p.b_stride;
+        const T *from_c = c + (t0 + fetch_t) * p.c_stride;
 #pragma unroll
         for (int k = 0; k < kFetch; ++k) {
-            const bool in = fetch_t + row(k) < count && fetch_n + col(k) < p.states;
-            fetch_b[k] = in ? from_b[row(k) * p.b_stride + col(k)] : Elem<T>::put(0.0f);
+            const bool in = fetch_t + row(k) < count;
+            const int n = place_state(fetch_n + col(k), p.states);
+            fetch_b[k] = in ? from_b[row(k) * p.b_stride + n] : Elem<T>::put(0.0f);
             if (FINAL)
-                fetch_c[k] = in ? from_c[row(k) * p.c_stride + col(k)] : Elem<T>::put(0.0f);
+                fetch_c[k] = in ? from_c[row(k) * p.c_stride + n] : Elem<T>::put(0.0f);
         }
     };
     const auto settle = [&](StageT &st) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
                 const float x = Elem<T>::get(fetch_b[k]);
                 st.b[fetch_t + row(k)][at] = make_float2(x, x);
                 if (FINAL) {
-                    const float y = Elem<T>::get(fetch_c[k]);
+                    const float y = place_share(n, p.states, kPadded) * Elem<T>::get(fetch_c[k]);
                     st.c[fetch_t + row(k)][at] = make_float2(y, y);
                 }
             }
@@ -358,9 +359,11 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
                 const float2 v0 = split_pair(h[n]), v1 = split_pair(h[n + 1]),
                              v2 = split_pair(h[n + 2]), v3 = split_pair(h[n + 3]);
                 if (live0)
-                    *reinterpret_cast<float4 *>(state0 + n) = make_float4(v0.x, v1.x, v2.x, v3.x);
+                    *reinterpret_cast<float4 *>(state0 + n0 + n) =
+                        make_float4(v0.x, v1.x, v2.x, v3.x);
                 if (live1)
-                    *reinterpret_cast<float4 *>(state1 + n) = make_float4(v0.y, v1.y, v2.y, v3.y);
+                    *reinterpret_cast<float4 *>(state1 + n0 + n) =
+                        make_float4(v0.y, v1.y, v2.y, v3.y);
             }
         } else {
 #pragma unroll
@@ -368,9 +371,9 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
                 const float2 v = split_pair(h[n]);
                 if (n0 + n < p.states) {
                     if (live0)
-                        state0[n] = v.x;
+                        state0[n0 + n] = v.x;
                     if (live1)
-                        state1[n] = v.y;
+                        state1[n0 + n] = v.y;
                 }
             }
         }
@@ -396,9 +399,10 @@ __global__ void __launch_bounds__(kScanThreads) carry_kernel(ScanArgs p, Spans w
     const int per_group = p.channels / p.groups, channels = 2 * kScanThreads / G;
     const int blocks = (per_group + channels - 1) / channels;
     const int local = (block % blocks) * channels + threadIdx.x / G * 2;
-    const int d = block / blocks * per_group + local, k0 = threadIdx.x % G * NS + n;
+    const int d = block / blocks * per_group + local;
+    const int k0 = place_state(threadIdx.x % G * NS + n, p.states);
     const auto decay = [&](int c) {
-        return k0 < p.states && local + c < per_group
+        return local + c < per_group
                    ? kLog2e * __ldg(p.a + static_cast<long long>(d + c) * p.states + k0)
                    : 0.0f;
     };

@@ -104,8 +104,13 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs p)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             h[n] = fmaf(ex2(st * a[n]), h[n], su * Elem<T>::get(x.b[n]));
-            v = fmaf(h[n], Elem<T>::get(x.c[n]), v);
+            // (places beyond the states have no part in the output: an infinite
+            // input makes NaN of their zeros)
+            if (WIDE || n0 + n < p.states)
+                v = fmaf(h[n], Elem<T>::get(x.c[n]), v);
         }
+        if (WIDE && n0 >= p.states)
+            v = 0.0f;
         if (slot >= 0) {
             float *to = place(slot);
             if (WIDE) {

@@ -196,6 +196,28 @@ def test_an_infinite_input_stays_an_infinity(dtype, channels, states, step, skip
     _check_infinities(dtype, channels, states, 24, step, skip)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("states", [1, 2, 3, 5, 7, 9, 13, 17, 24, 33, 48, 65, 100])
+@pytest.mark.parametrize("channels", [40, 33])
+@pytest.mark.parametrize("step", [False, True])
+def test_an_infinite_input_beside_unused_places(dtype, channels, states, step):
+    """States that do not fill the lanes' places."""
+    _check_infinities(dtype, channels, states, 24, step, True)
+
+
+@pytest.mark.parametrize("states", [13, 33])
+def test_infinite_step_sizes(states):
+    v = _inputs("f32", 30, 20, states)
+    v["dt"][6, 3] = float("inf")
+    v["b"].abs_()
+    v["c"].abs_()
+    v["u"].abs_()
+    y = binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"])
+    # the states become infinities and, without a step size of that kind, stay so
+    assert torch.isposinf(y[6:, 3]).all() and torch.isfinite(y[:6]).all()
+    assert torch.isfinite(y[:, :3]).all() and torch.isfinite(y[:, 4:]).all()
+
+
 @pytest.mark.parametrize("skip", [False, True])
 def test_an_infinite_input_in_a_large_batch_of_steps(skip):
     _check_infinities("bf16", 128, 16, 300, True, skip, gated=True)
