@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(kScanThreads, 5) scan_kernel(ScanArgs p, Spans
 
 // Between the passes: turns what the first pass left of each span into the
 // state after it, every span carrying the state before it on by
-// e^(a * its step sizes' sum).  A thread follows one state of a channel pair
+// e^(a * its step sizes' sum).  Token by token an infinite state stays infinite
+// however far it decays, so it is not multiplied by a product that has become 0
+// on the way (by one of an infinite step size it is).  A thread follows one state of a channel pair
 // over a sequence's spans, loading kCarry of them together.  grid (sequences *
 // channel blocks * NS).
 constexpr int kCarry = 16;
@@ -426,7 +428,11 @@ __global__ void __launch_bounds__(kScanThreads) carry_kernel(ScanArgs p, Spans w
 #pragma unroll
         for (int j = 0; j < kCarry; ++j)
             if (k + j < left) {
-                h = fma2(ex2_pair(mul2(sums[j], a)), h, ends[j]);
+                const float2 far = split_pair(mul2(sums[j], a)), from = split_pair(h);
+                const float2 by = split_pair(ex2_pair(make_pair(far.x, far.y)));
+                const bool x_stays = isinf(from.x) && far.x > -INFINITY;
+                const bool y_stays = isinf(from.y) && far.y > -INFINITY;
+                h = fma2(make_pair(x_stays ? 1.0f : by.x, y_stays ? 1.0f : by.y), h, ends[j]);
                 state[(k + j) * row * NS] = h;
             }
     }

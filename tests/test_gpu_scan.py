@@ -205,6 +205,25 @@ def test_an_infinite_input_beside_unused_places(dtype, channels, states, step):
     _check_infinities(dtype, channels, states, 24, step, True)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("states", [4, 13, 16, 64])
+def test_an_infinite_input_in_a_long_prompt(dtype, states):
+    """Decays so fast that a span's product of them is 0, while no token's is."""
+    assert binding.lstm_selective_scan_workspace(600, 24, states, 1, 1, True) > 0  # (in spans)
+    _check_infinities(dtype, 24, states, 600, False, True, least=-30.0, at=(40, 300))
+
+
+def test_an_infinite_state_in_a_long_prompt():
+    v = _inputs("f32", 600, 24, 16)
+    v["a"] = -torch.linspace(1, 40, 16, device="cuda").repeat(24, 1)
+    state = torch.zeros(1, 24, 16, device="cuda")
+    state[0, 5, 1], state[0, 6, 15] = float("inf"), float("-inf")
+    binding.lstm_selective_scan(v["u"], v["dt"], v["a"], v["b"], v["c"], state=state,
+                                resume=_i32([1]))
+    assert state[0, 5, 1] == float("inf") and state[0, 6, 15] == float("-inf")
+    assert int(torch.isfinite(state).sum()) == 24 * 16 - 2
+
+
 @pytest.mark.parametrize("states", [13, 33])
 def test_infinite_step_sizes(states):
     v = _inputs("f32", 30, 20, states)
