@@ -442,7 +442,8 @@ template <typename T, int NS, int G, bool WIDE>
 int launch_prompts(const ScanArgs &p, const Plan &plan, void *workspace, cudaStream_t stream)
 {
     constexpr int kChannels = 2 * kScanThreads / G;
-    if (plan.spans * plan.blocks > 0x7fffffffll || plan.blocks * p.seq.count * NS > 0x7fffffffll)
+    if (plan.spans * plan.blocks > 0x7fffffffll ||
+        (plan.whole > 0 && plan.blocks * p.seq.count * NS > 0x7fffffffll))  // carry_kernel's grid
         return fail(LSTM_E_OVERFLOW, "lstm_selective_scan: %d sequences, %d tokens, %d channels",
                     p.seq.count, p.seq.tokens, p.channels);
     Spans w = {plan.chunk, plan.each, nullptr, nullptr, static_cast<int>(plan.blocks),

@@ -93,6 +93,21 @@ def test_only_empty_prompts():
     assert torch.equal(conv[1::2], kept[1::2]) and (conv[::2] == 0).all()
 
 
+def test_very_many_prompts_in_one_piece():
+    """2^21 prompts of 128 blocks of channels: more than 2^31 states a thread of one block, which
+    only prompts in several spans are limited to."""
+    n, channels = 1 << 21, 16384
+    state = torch.full((2, channels, 16), 7.0, device="cuda")
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    slots[0], slots[n - 1] = 1, 0
+    empty = torch.zeros(0, channels, device="cuda")
+    bc = torch.zeros(0, 16, device="cuda")
+    y = binding.lstm_selective_scan(empty, empty, -torch.ones(channels, 16, device="cuda"), bc, bc,
+                                    offsets=torch.zeros(n + 1, dtype=torch.int32, device="cuda"),
+                                    state=state, slots=slots)
+    assert y.shape == (0, channels) and not state.any()
+
+
 @pytest.mark.parametrize("length", [589, 1000, 2500])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_prompts(dtype, length):
