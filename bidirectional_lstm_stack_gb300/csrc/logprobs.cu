@@ -537,7 +537,8 @@ int launch_small(const LogprobArgs &p, cudaStream_t stream)
     if (st != LSTM_OK)
         return st;
     const int per_block = kSmallThreads / LANES;
-    small_kernel<T, LANES><<<(p.rows + per_block - 1) / per_block, kSmallThreads, 0, stream>>>(p);
+    const unsigned blocks = (static_cast<unsigned>(p.rows) + per_block - 1) / per_block;
+    small_kernel<T, LANES><<<blocks, kSmallThreads, 0, stream>>>(p);
     return cuda_status(cudaGetLastError(), "lstm_token_logprobs launch");
 }
 

@@ -58,6 +58,17 @@ def test_many_rows_of_few_classes(rows):
     _check(normal(g, rows, 7, scale=4.0), _tokens(g, rows, 7), 3)
 
 
+def test_as_many_rows_as_there_can_be():
+    rows = (1 << 31) - 1
+    logits = torch.zeros(rows, 1, device="cuda", dtype=torch.bfloat16)
+    entropy = torch.full((rows,), 7.0, device="cuda")
+    st = binding.load().lstm_token_logprobs(logits.data_ptr(), 1, binding.LSTM_BF16, rows, 1, None,
+                                            None, entropy.data_ptr(), 0, None, None,
+                                            torch.cuda.current_stream().cuda_stream)
+    assert st == binding.LSTM_OK, binding.lstm_stack_last_error()
+    assert not entropy.any()
+
+
 @pytest.mark.parametrize("top", [0, 1, 2, 31, 32])
 @pytest.mark.parametrize("vocab", [32, 1000, 30000])
 def test_numbers_of_alternatives(top, vocab):
