@@ -442,7 +442,7 @@ PyObject *token_logprobs(PyObject *, PyObject *const *args, Py_ssize_t count)
         logp = stream.empty({x.rows}, at::kFloat);
     if (truth(v[3], true))
         entropy = stream.empty({x.rows}, at::kFloat);
-    if (top > 0) {
+    if (top > 0 && top <= LSTM_TOP_MAX) {  // (more are refused, and may not fit)
         top_logp = stream.empty({x.rows, top}, at::kFloat);
         top_ids = stream.empty({x.rows, top}, at::kLong);
     }

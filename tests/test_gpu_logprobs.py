@@ -158,6 +158,12 @@ def test_behind_the_heads():
     torch.testing.assert_close(got, logp.amax(-1), rtol=1e-5, atol=1e-6)
 
 
+def test_very_many_alternatives_are_refused_before_memory_is_asked_for():
+    with pytest.raises(binding.LSTMError) as e:
+        binding.lstm_token_logprobs(torch.zeros(64, 100, device="cuda"), top=(1 << 31) - 1)
+    assert e.value.code == binding.LSTM_E_INVALID
+
+
 def test_refusals():
     x = torch.zeros(4, 10, device="cuda")
     run = binding.lstm_token_logprobs
