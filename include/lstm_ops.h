@@ -143,7 +143,8 @@ int lstm_selective_scan_step(const void *u, long long u_stride, const void *dt,
  *            one of 32, 64 and 128, or 0 for one scale a row; else not read.
  *            A scale is the largest |n| of its columns / 448, at least
  *            2^-126, and 1 where all are 0; y = n / scale rounded to nearest
- *            even, so y * scale stands for n.
+ *            even (both quotients as fp32 division rounds them), so y * scale
+ *            stands for n.
  * A row that holds infinities or NaN gives NaN where IEEE arithmetic does.
  * 1 <= cols <= 32768.  Errors: LSTM_E_INVALID, LSTM_E_OVERFLOW,
  * LSTM_E_DEVICE, LSTM_E_CUDA. */

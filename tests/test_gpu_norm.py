@@ -111,6 +111,51 @@ def test_zero_rows_and_zero_values():
     assert (y == 0).all()
 
 
+def _e4m3(v):
+    """fp32 values rounded to the nearest e4m3 value (on the host)."""
+    return torch.from_numpy(v).to(torch.float8_e4m3fn).float().numpy()
+
+
+@pytest.mark.parametrize("cols", [32, 60, 512, 1111, 4096, 16384, 20001])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("size", [1.0, 1e-36, 1e-30, 1e12, 1e30])
+def test_eight_bits_are_the_quotients_own(cols, group, size):
+    """Scales and 8-bit values bit for bit: fp32's quotients of the norm that the same kernel
+    gives for fp32 output.  The residual's sizes make the norm's sizes differ widely in a row."""
+    g = gen(cols)
+    x = normal(g, 40, cols) * torch.exp2(-12 * uniform(g, 40, cols))
+    weight = (0.5 + uniform(g, cols)) * size
+    x[3] = 0.0
+    x[4, ::2] = 0.0
+    x[5] = torch.where(x[5] < 0, -1.0, 1.0)
+    n = binding.lstm_residual_rms_norm(x, weight, 1e-5)[0].cpu().numpy()
+    y, scales, _ = binding.lstm_residual_rms_norm(x, weight, 1e-5, quantize=True, group=group)
+    step = group or cols
+    top = np.stack([np.abs(n[:, k:k + step]).max(1) for k in range(0, cols, step)], 1)
+    expected = np.where(top > 0, np.maximum(top / np.float32(448), np.float32(2.0 ** -126)),
+                        np.float32(1))
+    assert expected.dtype == np.float32
+    np.testing.assert_array_equal(scales.cpu().numpy(), expected)
+    wide = np.repeat(expected, step, 1)[:, :cols]
+    np.testing.assert_array_equal(y.float().cpu().numpy(), _e4m3(n / wide))
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("cols", [256, 255])
+def test_eight_bits_of_an_infinite_norm(cols, group):
+    weight = torch.ones(cols, device="cuda")
+    weight[40] = float("inf")
+    y, scales, _ = binding.lstm_residual_rms_norm(torch.ones(2, cols, device="cuda"), weight, 1e-6,
+                                                  quantize=True, group=group)
+    y, scales = f64(y.float()), f64(scales)
+    # beside it in its group: a quotient by an infinity
+    ours = np.arange(cols) // (group or cols) == 40 // (group or cols)
+    assert np.isinf(scales[:, 40 // (group or cols)]).all() and np.isfinite(scales).sum() == scales.size - 2
+    assert np.isnan(y[:, 40]).all() and int(np.isnan(y).sum()) == 2
+    y[:, 40] = 0.0
+    assert (y[:, ours] == 0.0).all() and (y[:, ~ours] == 448.0).all()
+
+
 def test_tiny_and_huge_values():
     weight = torch.ones(64, device="cuda")
     # the mean of squares underflows to zero: eps alone divides
