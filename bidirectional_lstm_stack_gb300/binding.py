@@ -404,6 +404,7 @@ class LSTMHeads:
 # that every tensor has the type, shape and device that the call's sizes say.
 # Matrices are [rows, columns] with consecutive columns and any row stride.
 # Outputs that are not given are allocated for the stream the call runs on.
+# Forward only: while gradients are recorded, tensors that require one are refused.
 # Small calls last longer on the host than on the GPU, so checks, outputs and
 # the call itself are compiled (csrc/python_ops.cpp): a decode step of one
 # sequence takes 7.6 us from Python, through ctypes it took 25.

@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -71,7 +72,12 @@ const Tensor *optional_tensor(const char *name, PyObject *o)
     if (!o)
         return nullptr;
     TORCH_CHECK_TYPE(THPVariable_Check(o), name, " is no tensor");
-    return &THPVariable_Unpack(o);
+    const Tensor &t = THPVariable_Unpack(o);
+    // forward only: an output without a gradient would pass unnoticed
+    TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                      " requires a gradient, which these operators do not have: detach it, or call "
+                      "them under torch.no_grad()");
+    return &t;
 }
 const Tensor &tensor(const char *name, PyObject *o)
 {

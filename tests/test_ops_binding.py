@@ -54,6 +54,50 @@ def test_a_module_that_is_not_built_is_missing(monkeypatch):
         binding.lstm_token_logprobs(torch.zeros(2, 8))
 
 
+@pytest.mark.parametrize("function", range(6))
+def test_a_matrix_that_requires_a_gradient_is_refused(function):
+    m = torch.zeros(2, 8, requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        _calls(m)[function]()
+    with pytest.raises(ValueError, match="requires a gradient"):  # of a graph's inner tensors too
+        _calls(m * 2)[function]()
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # (nothing else is wrong)
+        _calls(m)[function]()
+
+
+@pytest.mark.gpu
+def test_any_tensor_that_requires_a_gradient_is_refused():
+    ones = lambda *s: torch.ones(*s, device="cuda")
+    x, n = ones(2, 8), 4
+    calls = [
+        (binding.lstm_causal_conv, [x, ones(8, 4)],
+         dict(bias=ones(8), state=ones(2, 3, 8), sequences=2, y=ones(2, 8))),
+        (binding.lstm_causal_conv_step, [x, ones(8, 4), ones(8), ones(2, 3, 8)], dict(y=ones(2, 8))),
+        (binding.lstm_selective_scan, [x, x, -ones(8, n), ones(2, n), ones(2, n)],
+         dict(skip=ones(8), z=x, dt_bias=ones(8), state=ones(2, 8, n), sequences=2, y=ones(2, 8))),
+        (binding.lstm_selective_scan_step, [x, x, -ones(8, n), ones(2, n), ones(2, n), ones(2, 8, n)],
+         dict(skip=ones(8), z=x, dt_bias=ones(8), y=ones(2, 8))),
+        (binding.lstm_residual_rms_norm, [x, ones(8), 1e-5],
+         dict(residual=x, residual_out=ones(2, 8), y=ones(2, 8))),
+        (binding.lstm_residual_rms_norm, [x, ones(8), 1e-5], dict(quantize=True, scales=ones(2, 1))),
+        (binding.lstm_token_logprobs, [x], {})]
+    for call, args, more in calls:
+        expected = call(*[a.clone() if torch.is_tensor(a) else a for a in args],
+                        **{k: v.clone() if torch.is_tensor(v) else v for k, v in more.items()})
+        for k, v in list(enumerate(args)) + list(more.items()):
+            if not torch.is_tensor(v):
+                continue
+            other_args, other = list(args), dict(more)
+            (other_args if isinstance(k, int) else other)[k] = v.clone().requires_grad_()
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(*other_args, **other)
+        with torch.no_grad():
+            got = call(*[a.clone().requires_grad_() if torch.is_tensor(a) else a for a in args],
+                       **{k: v.clone() if torch.is_tensor(v) else v for k, v in more.items()})
+        first = lambda r: r if torch.is_tensor(r) else r[0] if r[0] is not None else r[1]
+        assert torch.equal(first(got).float(), first(expected).float())
+
+
 @pytest.mark.gpu
 def test_arguments_that_are_wrong_beside_a_good_matrix():
     x, w, v = torch.zeros(4, 8).cuda(), torch.zeros(8, 4).cuda(), torch.ones(8).cuda()
