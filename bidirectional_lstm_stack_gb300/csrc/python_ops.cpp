@@ -254,6 +254,17 @@ void call(F function, As... as)
     throw python_error();
 }
 
+// Tells autograd that the tensor of this argument, if it was given, has been
+// overwritten.  (Tensors of inference mode have no count of that.)
+void written(PyObject *o)
+{
+    if (!o)
+        return;
+    const Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_inference())
+        t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject *wrap(const Tensor &t) { return THPVariable_Wrap(t); }
 PyObject *wrap(const std::optional<Tensor> &t)
 {
@@ -290,6 +301,8 @@ PyObject *causal_conv(PyObject *, PyObject *const *args, Py_ssize_t count)
                            truth(v[3], true), as_int("sequences", p.count), p.offsets, state.at,
                            state.count, state.slots, state.resume, y.data_ptr(),
                            matrix("y", y, x.rows, x.cols, x.type, x), stream.at);
+    written(v[6]);
+    written(v[9]);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -311,6 +324,8 @@ PyObject *causal_conv_step(PyObject *, PyObject *const *args, Py_ssize_t count)
                                 as_int("channels", x.cols), as_int("width", width), w, bias,
                                 truth(v[4], true), state.at, state.count, state.slots,
                                 y.data_ptr(), matrix("y", y, x.rows, x.cols, x.type, x), stream.at);
+    written(v[3]);
+    written(v[6]);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -367,6 +382,8 @@ PyObject *selective_scan(PyObject *, PyObject *const *args, Py_ssize_t count)
         static_cast<float *>(state.at), state.count, state.slots, state.resume, y.data_ptr(),
         matrix("y", y, u.rows, u.cols, u.type, u), bytes ? workspace.data_ptr() : nullptr, bytes,
         stream.at);
+    written(v[12]);
+    written(v[15]);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -386,6 +403,8 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *args, Py_ssize_t coun
         type, as_int("sequences", u.rows), as_int("channels", u.cols), as_int("states", s.states),
         as_int("groups", s.groups), static_cast<float *>(state.at), state.count, state.slots,
         y.data_ptr(), matrix("y", y, u.rows, u.cols, u.type, u), stream.at);
+    written(v[5]);
+    written(v[12]);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -427,6 +446,11 @@ PyObject *residual_rms_norm(PyObject *, PyObject *const *args, Py_ssize_t count)
         res_out ? res_out->data_ptr() : nullptr, out_stride, y.data_ptr(),
         matrix("y", y, x.rows, x.cols, y_type, x), quantize ? static_cast<int>(LSTM_E4M3) : type,
         scales_at, group, stream.at);
+    if (residual)
+        written(v[4]);
+    written(v[7]);
+    if (quantize)
+        written(v[8]);
     return wrap_all(std::optional<Tensor>(y), scales, res_out);
     END_HANDLE_TH_ERRORS
 }

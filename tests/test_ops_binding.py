@@ -141,6 +141,49 @@ def test_given_outputs_are_what_is_returned():
     assert torch.equal(r, expected)
 
 
+def _overwriting_calls():
+    ones = lambda *s: torch.ones(*s, device="cuda")
+    x, n = ones(2, 8), 4
+    scan = (x, x, -ones(8, n), ones(2, n), ones(2, n))
+    y, state, scan_state = ones(2, 8), ones(2, 3, 8), ones(2, 8, n)
+    residual, scales, q = ones(2, 8), ones(2, 1), ones(2, 8).to(torch.float8_e4m3fn)
+    return [(lambda: binding.lstm_causal_conv(x, ones(8, 4), state=state, sequences=2, y=y), (state, y)),
+            (lambda: binding.lstm_causal_conv_step(x, ones(8, 4), None, state, y=y), (state, y)),
+            (lambda: binding.lstm_selective_scan(*scan, state=scan_state, sequences=2, y=y),
+             (scan_state, y)),
+            (lambda: binding.lstm_selective_scan_step(*scan, scan_state, y=y), (scan_state, y)),
+            (lambda: binding.lstm_residual_rms_norm(x, ones(8), 1e-5, residual=residual,
+                                                    residual_out=residual, y=y), (residual, y)),
+            (lambda: binding.lstm_residual_rms_norm(x, ones(8), 1e-5, quantize=True, y=q,
+                                                    scales=scales), (q, scales))], x
+
+
+@pytest.mark.gpu
+def test_overwritten_tensors_count_it():
+    """What autograd checks tensors that it has saved by."""
+    calls, x = _overwriting_calls()
+    for call, tensors in calls:
+        before = [t._version for t in tensors]
+        call()
+        assert all(t._version > b for t, b in zip(tensors, before)) and x._version == 0
+    w = torch.ones(2, 8, device="cuda", requires_grad=True)
+    y = torch.ones(2, 8, device="cuda")
+    loss = (w * y).sum()  # saves y
+    binding.lstm_causal_conv(x, torch.ones(8, 4, device="cuda"), y=y)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+@pytest.mark.gpu
+def test_tensors_of_inference_mode():
+    with torch.inference_mode():
+        for call, _ in _overwriting_calls()[0]:
+            call()
+        inside = _overwriting_calls()[0]
+    for call, _ in inside:
+        call()
+
+
 @pytest.mark.gpu
 def test_calls_of_two_threads():
     x, w = torch.randn(256, 64).cuda(), torch.randn(64, 4).cuda()
