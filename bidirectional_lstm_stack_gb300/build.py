@@ -3,8 +3,10 @@ module _native.so from csrc/*.cpp.
 
 Each translation unit compiles in parallel with nvcc into ``_build/`` at the
 repository root; both are linked next to this file.  No cmake, no torch
-extension machinery: the library has a plain C ABI, and the module, which
-takes torch tensors, is linked to the installed torch.
+extension machinery: the library has a plain C ABI and needs CUDA alone.  The
+module takes torch tensors and is linked to the installed torch; without a
+torch for CUDA or without Python's headers the library is built all the same,
+and a warning says what the module lacks.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -33,9 +36,23 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
-def _torch() -> str:
+def _torch() -> str | None:
     """Folder of the installed torch (found, not imported)."""
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _module_lacks() -> str | None:
+    """What the module cannot be built without and is not there."""
+    torch = _torch()
+    if torch is None:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return f"the torch in {torch} is one without CUDA"
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        return f"there is no Python.h in {python}"
+    return None
 
 
 def _torch_flags():
@@ -60,23 +77,6 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     newest_header = max(os.path.getmtime(h) for h in _headers())
-    # (another torch is another set of headers)
-    newest_torch = max(newest_header, os.path.getmtime(os.path.join(_torch(), "version.py")))
-    jobs = []
-
-    def objects(srcs, flags, newest):
-        objs = []
-        for src in srcs:
-            obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
-            objs.append(obj)
-            if (force or not os.path.exists(obj) or os.path.getmtime(obj) < os.path.getmtime(src)
-                    or os.path.getmtime(obj) < newest):
-                jobs.append([nvcc, *ARCH, *FLAGS, *flags, *(extra or []), "-c", src, "-o", obj])
-        return objs
-
-    objs = objects(sources(), [], newest_header)
-    kernels = len(jobs)
-    native = objects(sources(".cpp"), _torch_flags(), newest_torch)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -84,22 +84,48 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
-        for log in ex.map(run, jobs):
+    def objects(srcs, flags, newest):
+        """Their objects, and the commands that make those that are missing or old."""
+        objs, jobs = [], []
+        for src in srcs:
+            obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
+            objs.append(obj)
+            if (force or not os.path.exists(obj) or os.path.getmtime(obj) < os.path.getmtime(src)
+                    or os.path.getmtime(obj) < newest):
+                jobs.append([nvcc, *ARCH, *FLAGS, *flags, *(extra or []), "-c", src, "-o", obj])
+        return objs, jobs
+
+    def link(out, runs, args):
+        for log in [r.result() for r in runs]:
             if verbose and log:
                 print(log)
-    def link(out, args):
-        tmp = out + f".{os.getpid()}.tmp"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *args])
-        os.replace(tmp, out)
+        if force or runs or not os.path.exists(out):
+            tmp = out + f".{os.getpid()}.tmp"
+            run([nvcc, *ARCH, "-shared", "-o", tmp, *args])
+            os.replace(tmp, out)
 
-    if force or kernels or not os.path.exists(LIB):
-        link(LIB, objs)
-    if force or len(jobs) > kernels or not os.path.exists(NATIVE):
-        # (torch's libraries are loaded before the module is)
-        link(NATIVE, [*native, "-L", PKG, "-llstmstack", "-Xlinker", "-rpath,$ORIGIN", "-L",
-                      os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
-                      "-lc10", "-lc10_cuda"])
+    objs, jobs = objects(sources(), [], newest_header)
+    lacks = _module_lacks()
+    native, native_jobs = [], []
+    if not lacks:
+        # (another torch is another set of headers)
+        newest_torch = os.path.getmtime(os.path.join(_torch(), "version.py"))
+        native, native_jobs = objects(sources(".cpp"), _torch_flags(),
+                                      max(newest_header, newest_torch))
+    with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs) + len(native_jobs))) as ex:
+        runs = [ex.submit(run, job) for job in jobs]
+        native_runs = [ex.submit(run, job) for job in native_jobs]
+        # the library first: it does not depend on the module
+        link(LIB, runs, objs)
+        if not lacks:
+            # (torch's libraries are loaded before the module is)
+            link(NATIVE, native_runs,
+                 [*native, "-L", PKG, "-llstmstack", "-Xlinker", "-rpath,$ORIGIN", "-L",
+                  os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                  "-lc10", "-lc10_cuda"])
+    if lacks:
+        warnings.warn(f"{LIB} is built, {os.path.basename(NATIVE)} (calls on torch tensors) is not: "
+                      f"{lacks}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
