@@ -159,13 +159,57 @@ def test_weights_at_any_element(dtype, offset, width, channels):
     y = binding.lstm_causal_conv(x, w, b)
     ref, _, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True, [(0, 45)])
     assert_close(y, ref, bound, dtype, "y")
-    state = normal(g, 45, width - 1, channels, dtype=DTYPES[dtype])
+    state = at_element(normal(g, 45, width - 1, channels, dtype=DTYPES[dtype]), offset)
     before = f64(state)
     y = binding.lstm_causal_conv_step(x, w, b, state)
     ref, new, bound = oracle.causal_conv(f64(x), f64(w), f64(b), True,
                                          [(i, i + 1) for i in range(45)], before, None, [1] * 45)
     assert_close(y, ref, bound, dtype, "y of the step")
     np.testing.assert_array_equal(f64(state), new)
+
+
+# all lengths from nothing to several runs of 32 tokens, on both sides of multiples of 4, 12, 16 and 32
+LENGTHS = [1, 0, 2, 3, 4, 5, 11, 12, 13, 15, 16, 17, 0, 31, 32, 33, 47, 48, 49, 63, 64, 65, 100]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels,tokens,width", [
+    (4096, 2100, 4), (4094, 2100, 4), (4095, 1100, 4), (2048, 4100, 3),   # runs of 32 tokens
+    (4096, 740, 4), (4094, 740, 4), (4095, 740, 4), (2048, 1100, 2)])     # runs of 16
+def test_long_runs(dtype, channels, tokens, width):
+    """From 2^19 vectors of channels on a thread works on 16 tokens, from 2^21 on 32, its rows
+    on their way through a ring; with four, two and one channels a thread."""
+    lengths = LENGTHS + [tokens - sum(LENGTHS)]
+    n = len(lengths)
+    assert lengths[-1] > 0
+    _check(dtype, channels, width, lengths, pool=n + 2, slots=[(5 * k + 3) % (n + 2) for k in range(n)],
+           resume=[k % 3 != 1 for k in range(n)])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_long_runs_of_equal_prompts(dtype):
+    _check(dtype, 4096, 4, [70] * 31, uniform=True, pool=31, resume=[k % 2 for k in range(31)])
+    _check(dtype, 2048, 4, [1031], uniform=True, strided=True, act=False, bias=False)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("channels", [32, 30, 31])
+@pytest.mark.parametrize("act", [False, True])
+def test_infinities_and_nan_stay_where_the_definition_has_them(dtype, channels, act):
+    g = gen(11)
+    x = normal(g, 40, channels, dtype=DTYPES[dtype])
+    x[7, 3], x[20, 4], x[39, 5], x[0, 29] = (float(v) for v in ("inf", "-inf", "nan", "inf"))
+    w, state = normal(g, channels, 4), normal(g, 1, 3, channels, dtype=DTYPES[dtype])
+    before = f64(state)
+    y = binding.lstm_causal_conv(x, w, silu=act, state=state)
+    with np.errstate(invalid="ignore"):
+        ref, new, bound = oracle.causal_conv(f64(x), f64(w), None, act, [(0, 40)], before)
+    np.testing.assert_array_equal(f64(state), new)
+    odd = ~np.isfinite(ref)
+    assert odd.any()
+    np.testing.assert_array_equal(f64(y)[odd], ref[odd])
+    assert_close(torch.where(torch.from_numpy(odd), torch.zeros(()), y.cpu().float()),
+                 np.where(odd, 0.0, ref), np.where(odd, 0.0, bound), dtype)
 
 
 def test_on_another_stream():

@@ -52,6 +52,19 @@ def test_long_rows(rows, vocab):
     assert_close(got[1][take], h, bound[:, 1], "f32")
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,vocab", [(1, 131072), (2, 100003), (70, 40000), (5, 300007), (160, 20000)])
+@pytest.mark.parametrize("top", [0, 32])
+def test_all_outputs_of_long_rows(dtype, rows, vocab, top):
+    """Rows shared by one to eight blocks, tokens in the part of each."""
+    g = gen(vocab)
+    logits = normal(g, rows, vocab, scale=2.0, dtype=DTYPES[dtype])
+    for part in range(8 if rows <= 2 else 1):
+        tokens = (_tokens(g, rows, vocab) + part * vocab // 8) % vocab
+        tokens[0] = [0, vocab - 1, vocab // 2, vocab // 8][part % 4]
+        _check(logits, tokens, top)
+
+
 @pytest.mark.parametrize("rows", [1, 33, 2000])
 def test_many_rows_of_few_classes(rows):
     g = gen(rows)

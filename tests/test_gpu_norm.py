@@ -6,7 +6,7 @@ import torch
 
 from bidirectional_lstm_stack_gb300 import binding
 from oracle import ops as oracle
-from ops_util import DTYPES, ROUND, assert_close, f64, gen, normal, slice_of, uniform
+from ops_util import DTYPES, ROUND, assert_close, at_element, f64, gen, normal, slice_of, uniform
 
 pytestmark = pytest.mark.gpu
 
@@ -85,6 +85,28 @@ def test_rows(rows):
 @pytest.mark.parametrize("quantize", [False, True])
 def test_rows_of_wider_matrices(quantize):
     _check("bf16", 9, 256, strided=True, quantize=quantize)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("offset", [1, 2, 3, 4])
+@pytest.mark.parametrize("quantize", [False, True])
+def test_weights_at_any_element(dtype, offset, quantize):
+    x, res, weight = _inputs(dtype, 5, 264, True)
+    at = at_element(weight, offset)
+    assert at.data_ptr() % 16 == 4 * offset % 16
+    run = lambda w: binding.lstm_residual_rms_norm(x, w, 1e-5, residual=res, quantize=quantize, group=64)
+    y, scales, v = run(at)
+    ref, ref_v = oracle.residual_rms_norm(f64(x), f64(res), f64(weight), 1e-5)
+    size = (np.abs(f64(x)) + np.abs(f64(res))) * np.abs(f64(weight)) / np.sqrt(
+        (ref_v ** 2).mean(1, keepdims=True) + 1e-5)
+    bound = NORM * np.abs(ref) + oracle.U32 * size
+    assert torch.equal(v, run(weight)[2])
+    if not quantize:
+        assert_close(y, ref, bound, dtype, "y")
+        return
+    wide = np.repeat(f64(scales), 64, axis=1)[:, :264]
+    got = f64(y.float()) * wide
+    assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -4 + wide * 2.0 ** -10 + 2 * bound).all()
 
 
 def test_residual_in_place():

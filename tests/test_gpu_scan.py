@@ -7,7 +7,7 @@ import torch
 
 from bidirectional_lstm_stack_gb300 import binding
 from oracle import ops as oracle
-from ops_util import DTYPES, assert_close, f64, gen, normal, slice_of, uniform
+from ops_util import DTYPES, assert_close, at_element, f64, gen, normal, slice_of, uniform
 
 pytestmark = pytest.mark.gpu
 
@@ -126,6 +126,20 @@ def test_large_layers(lengths, channels, states, equal):
     _check("bf16", lengths, channels, states, uniform_=equal, pool=n + 1,
            slots=[(3 * k + 1) % (n + 1) if (n + 1) % 3 else n - k for k in range(n)],
            resume=[k % 3 != 0 for k in range(n)])
+
+
+@pytest.mark.parametrize("dtype,channels,states,copies", [
+    ("bf16", 4096, 16, 2), ("f32", 4100, 16, 2), ("f16", 4095, 13, 2), ("bf16", 2048, 16, 4),
+    ("bf16", 1030, 8, 2), ("f16", 515, 64, 2), ("bf16", 512, 128, 2), ("f32", 512, 32, 4),
+    ("bf16", 4096, 4, 2), ("bf16", 2049, 5, 2)])
+def test_unequal_prompts_in_order_and_whole(dtype, channels, states, copies):
+    """Prompts that are put in order, but not divided: the workspace holds their order alone."""
+    lengths = [0, 1, 2, 7, 8, 9, 15, 16, 17, 33, 64, 120] * copies
+    n = len(lengths)
+    size = binding.lstm_selective_scan_workspace(sum(lengths), channels, states, 1, n, False)
+    assert size == 8 * (n + 1), size
+    _check(dtype, lengths, channels, states, pool=n + 3, slots=[(7 * k + 2) % (n + 3) for k in range(n)],
+           resume=[k % 3 != 2 for k in range(n)])
 
 
 def test_large_layers_in_fp32():
@@ -308,6 +322,32 @@ def test_step_of_a_large_batch(dtype, sequences, channels, states, groups):
     assert binding.lstm_fault_status() == 0
     assert_close(y, ref, bound, dtype, "y")
     assert_close(state, new, new_bound, "f32", "state")
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+@pytest.mark.parametrize("dtype,sequences,channels,states", [
+    ("bf16", 300, 128, 16), ("f32", 4, 64, 16), ("f16", 5, 33, 8), ("bf16", 20, 40, 13)])
+def test_weights_and_states_at_any_element(offset, dtype, sequences, channels, states):
+    """Views into larger buffers: prompts of one token each, and steps."""
+    v = _inputs(dtype, sequences, channels, states)
+    for k, shift in (("a", 0), ("skip", 1), ("dt_bias", 2)):
+        v[k] = at_element(v[k], (offset + shift) % 4)
+    start = normal(gen(8), sequences, channels, states)
+    for what in ("prompts", "step"):
+        state = at_element(start, offset)
+        assert state.data_ptr() % 16 == 4 * offset
+        first = [v[k] for k in ("u", "dt", "a", "b", "c")]
+        more = {k: v[k] for k in ("skip", "z", "dt_bias")}
+        if what == "step":
+            y = binding.lstm_selective_scan_step(*first, state, **more)
+        else:
+            y = binding.lstm_selective_scan(*first, state=state, sequences=sequences,
+                                            resume=torch.ones(sequences, device="cuda").int(), **more)
+        ref, new, bound, new_bound = oracle.selective_scan(
+            *(f64(v[k]) for k in ("u", "dt", "a", "b", "c", "skip", "z", "dt_bias")), True, 1,
+            [(s, s + 1) for s in range(sequences)], f64(start), step=True)
+        assert_close(y, ref, bound, dtype, what)
+        assert_close(state, new, new_bound, "f32", what + "'s state")
 
 
 def test_a_step_whose_states_do_not_arrive_is_reported():
