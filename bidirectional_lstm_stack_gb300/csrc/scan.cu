@@ -166,6 +166,10 @@ int scan(const char *what, ScanArgs &p, int dtype, int rows, bool step, void *wo
                     rows, p.channels, p.states, LSTM_SCAN_MAX_STATES, p.groups);
     const int size = element_size(dtype);
     const long long wide = static_cast<long long>(p.groups) * p.states;
+    // (the kernels count channels a block beyond the last and a row's b in 32 bits)
+    if (p.channels > kMostChannels || wide > kMostChannels)
+        return fail(LSTM_E_OVERFLOW, "%s: %d channels, %d groups of %d states (rows of at most %d)",
+                    what, p.channels, p.groups, p.states, kMostChannels);
     if (rows > 0 &&  // without rows there may be no buffers either
         ((st = check_matrix(what, "u", p.u, p.u_stride, rows, p.channels, size)) ||
          (st = check_matrix(what, "dt", p.dt, p.dt_stride, rows, p.channels, size)) ||
@@ -219,8 +223,8 @@ using namespace lstm;
 extern "C" size_t lstm_selective_scan_workspace(int tokens, int channels, int states, int groups,
                                                 int sequences, int equal_lengths)
 {
-    if (tokens < 0 || channels <= 0 || states <= 0 || states > LSTM_SCAN_MAX_STATES ||
-        groups <= 0 || sequences <= 0 || tokens > kMostTokens || sequences > kMostSequences)
+    if (tokens < 0 || channels <= 0 || channels > kMostChannels || states <= 0 ||
+        states > LSTM_SCAN_MAX_STATES || groups <= 0 || sequences <= 0 || tokens > kMostTokens || sequences > kMostSequences)
         return 0;
     return make_plan(tokens, channels, states, groups, sequences, equal_lengths != 0).bytes;
 }

@@ -60,6 +60,7 @@ struct Spans {
     Pair *sums;    // [numbers][channel blocks][threads]
 };
 
+constexpr int kMostChannels = 1 << 30;  // and numbers of a row of b or c
 constexpr int kScanThreads = 64;  // of a block; with two channels a thread
 
 // How a call's prompts are worked on: the same for its workspace's size and

@@ -99,6 +99,8 @@ int lstm_causal_conv_step(const void *x, long long x_stride, int dtype, int sequ
  *                 1 <= states <= LSTM_SCAN_MAX_STATES
  *   b, c        : device [tokens][groups][states] (a row's groups * states
  *                 values consecutive); groups divides channels
+ *                 (channels and groups * states: at most 2^30, else
+ *                 LSTM_E_OVERFLOW)
  *   skip, dt_bias : device [channels] fp32, or NULL: nothing is added
  *   state       : device [state_slots][channels][states] fp32, the h; NULL:
  *                 no states (state_slots, slots and resume are then not read)

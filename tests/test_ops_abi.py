@@ -151,5 +151,20 @@ def test_workspace_of_sizes_that_are_refused(lib):
     assert binding.lstm_selective_scan_workspace(MOST + 1, 64, 16, 1, MOST + 1, False) == 0
 
 
+@pytest.mark.parametrize("channels,groups,states", [
+    (MOST + 1, 1, 8), (0x7fffffff, 1, 16), (MOST, MOST // 4, 8), (1 << 28, 1 << 28, 16)])
+def test_very_wide_scans(lib, channels, groups, states):
+    """Channels a block beyond the last, and places in a row of b, are counted in 32 bits."""
+    big = 1 << 40
+    prompt = lib.lstm_selective_scan(64, big, 64, big, 64, 64, big, 64, big, None, None, 0, None, 1, 0,
+                                     4, channels, states, groups, 1, None, None, 0, None, None, 64,
+                                     big, None, 0, None)
+    assert prompt == binding.LSTM_E_OVERFLOW
+    step = lib.lstm_selective_scan_step(64, big, 64, big, 64, 64, big, 64, big, None, None, 0, None, 1,
+                                        0, 4, channels, states, groups, 64, 8, None, 64, big, None)
+    assert step == binding.LSTM_E_OVERFLOW
+    assert f"{channels} channels" in binding.lstm_stack_last_error()
+
+
 def test_timeout_hook_refuses_limits_above_two_seconds(lib):
     assert lib.lstm_test_scan_step_timeout(1, 2000001, 0) == INVALID
