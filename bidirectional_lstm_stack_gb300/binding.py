@@ -1,13 +1,15 @@
 """ctypes binding of liblstmstack.so (declared in include/lstm_stack.h and
 include/lstm_ops.h).
 
-Argument marshalling only: every function here checks nothing the library
-does not check again, computes nothing, and forwards to the C entry point of
-the same name.  Device buffers are torch CUDA tensors (their ``data_ptr``),
-streams are torch streams (their ``cuda_stream`` handle; default: the current
-stream of the tensor's device).  The functions of lstm_ops.h go through the
-compiled module ``_native``, which checks tensors and allocates outputs.  If the
-library is missing, every call raises ``LibraryMissing``: there is no fallback.
+Argument marshalling only: the functions compute nothing and forward to the C
+entry point of the same name.  Those of lstm_stack.h check nothing the library
+does not check again.  Those of lstm_ops.h go through the compiled module
+``_native``, which allocates outputs and alone checks shapes, types, devices and
+gradients (the C entry points take sizes and strides on trust).  Device buffers
+are torch CUDA tensors (their ``data_ptr``), streams are torch streams (their
+``cuda_stream`` handle; default: the current stream of the tensor's device).  If
+the library or the module is missing, calls raise ``LibraryMissing``: there is no
+fallback.
 """
 from __future__ import annotations
 
@@ -402,12 +404,13 @@ class LSTMHeads:
 #
 # The C entry points take sizes and strides on trust, so these functions check
 # that every tensor has the type, shape and device that the call's sizes say.
-# Matrices are [rows, columns] with consecutive columns and any row stride.
+# Matrices are [rows, columns] with consecutive columns and any row stride of at
+# least the columns.  Outputs must not overlap inputs (residual_out may be residual).
 # Outputs that are not given are allocated for the stream the call runs on.
 # Forward only: while gradients are recorded, tensors that require one are refused.
 # Small calls last longer on the host than on the GPU, so checks, outputs and
 # the call itself are compiled (csrc/python_ops.cpp): a decode step of one
-# sequence takes 7.6 us from Python, through ctypes it took 25.
+# sequence takes 5 us from Python, through ctypes it took 25.
 
 _ops = None
 

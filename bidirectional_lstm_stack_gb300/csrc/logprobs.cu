@@ -13,9 +13,13 @@
 // counting, for each, the keys above it.  Long rows are shared by the blocks of
 // a cluster, which join their sums and keys through distributed shared memory.
 //
-// Bound by instructions: eight an element against two or four bytes.  64 rows
-// of 100003 bf16: 6.3 us without alternatives, 13 us with 20; 2048 rows of
-// 32000: 35 us (3.8 TB/s) and 51 us.
+// 64 rows of 100003 bf16: 6.4 us without alternatives, 13 us with 20 (their bytes
+// take 1.9 us at the card's copy rate); 2048 rows of 32000: 35 us (3.8 TB/s) and
+// 51 us (19 us).  Neither the bytes nor the instructions bound it: some eight an
+// element would take 14 us for the latter rows.  It waits: a turn's loads are
+// issued only after the last turn's sums, and nothing is loaded between the
+// barriers of the joins and of the selection (with 20 alternatives issue slots are
+// 48 % busy, barriers and loads the longest stalls).
 #include <cmath>
 
 #include "ops.cuh"

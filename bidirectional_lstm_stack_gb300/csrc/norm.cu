@@ -6,7 +6,7 @@
 // Memory-bound: a handful of operations per element.  One pass: a block holds
 // its row in registers between the sum of squares and the outputs, so every
 // input is read once and every output written once.  12288 rows of 4096 bf16:
-// with a residual to e4m3 and a scale per 128 columns 60 us (5.9 TB/s, 87 % of
+// with a residual to e4m3 and a scale per 128 columns 60 us (5.9 TB/s, 86 % of
 // the card's copy rate); 8192 rows to bf16 41 us (6.5 TB/s, 96 %).
 #include <cfloat>
 
@@ -248,8 +248,9 @@ int launch_sized(const NormArgs &p, int rows, bool quant, cudaStream_t stream)
 {
     const int vectors = (p.cols + V - 1) / V;
     if constexpr (V == 1) {
-        // single elements: several a thread (2047 columns of bf16, 8192 rows:
-        // 256 threads of eight 42 us, 512 of four 50, 1024 of two 80)
+        // single elements: several a thread (2047 columns of bf16, 8192 rows, to
+        // e4m3 by groups: 256 threads of eight 40 us; with the groups' divisors
+        // computed for every element 42, 512 of four 50, 1024 of two 80)
         if (vectors <= 512)
             return launch<T, 1, 2, 256>(p, rows, quant, stream);
         if (vectors <= 2048)

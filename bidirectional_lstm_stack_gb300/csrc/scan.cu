@@ -77,7 +77,11 @@ constexpr int kLeastChunk = 32;
 
 Plan make_plan(int tokens, int channels, int states, int groups, int sequences, bool equal)
 {
-    // the longest sequence: known, or guessed at three times the mean
+    // The longest sequence: known, or guessed at three times the mean, as the host
+    // does not see the lengths (prompts whose lengths spread evenly over a factor of
+    // thirty reach 3.5 times).  Where one is much longer the guess keeps it whole:
+    // 4096 tokens beside 63 prompts of one, 2048 channels x 16 states, take 479 us,
+    // the 4096 alone, in spans, 80.
     const double mean = sequences > 0 ? static_cast<double>(tokens) / sequences : 0;
     const double longest = equal || sequences <= 1 ? mean : fmin(3 * mean, tokens);
     Plan best = {};
@@ -102,7 +106,9 @@ Plan make_plan(int tokens, int channels, int states, int groups, int sequences, 
         const double work = static_cast<double>(tokens) * r.blocks;
         const double uneven = equal || sequences <= 1 ? 1.0 : rate.uneven;
         for (int split = 0; split < 2; ++split) {
-            // spans that fill the machine six blocks deep
+            // spans that fill the machine six blocks deep (or a little less: their
+            // length is rounded up to 16 tokens, so 4096 tokens of 2048 channels make
+            // 52 spans of 80 in 16 channel blocks, 5.5 blocks an SM)
             long long chunk = static_cast<long long>(work / (152 * 6));
             chunk = (chunk + 15) / 16 * 16;
             if (chunk < kLeastChunk)

@@ -1,8 +1,9 @@
 // The selective scan's next token of every sequence.
 //
 // Memory-bound: the states are read and written once, 8 bytes a state against
-// some eight operations.  256 sequences of 4096 channels x 16 states: 26 us,
-// 5.5 TB/s, 80 % of the card's copy rate (tiles' kernel; the other one 38 us).
+// some eight operations.  256 sequences of 4096 channels x 16 states in a pool of
+// 300: 26 us, 5.5 TB/s, 80 % of the card's copy rate (tiles' kernel; the other one
+// 38 us).
 #include "scan.cuh"
 
 namespace lstm {
@@ -333,10 +334,13 @@ int launch_tiles(const ScanArgs &p, cudaStream_t stream)
     return cuda_status(cudaGetLastError(), "lstm_selective_scan_step launch");
 }
 
-// Whether the tiles' kernel takes the call: states of a channel block are one
-// run of whole 16-byte units, no block spans two groups, and there are enough
-// states for the ring to pay (8 sequences x 2048 channels x 16 states: 3.0 us
-// with it, 2.8 without; 32 sequences: 3.7 and 4.4).
+// Whether the tiles' kernel takes the call (for 4, 8, .. 128 states; it is not
+// instantiated for other counts, which take the general kernel: 256 sequences x
+// 4096 channels x 24 states 77 us, x 48 156 us, where their bytes take 30 and
+// 59): states of a channel block are one run of whole 16-byte units, no block
+// spans two groups, and there are enough states for the ring to pay (8 sequences
+// x 2048 channels x 16 states: 3.0 us with it, 2.8 without; 32 sequences: 3.7 and
+// 4.4).
 bool takes_tiles(const ScanArgs &p, int lanes)
 {
     const int across = kThreads / lanes;

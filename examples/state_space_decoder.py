@@ -112,7 +112,8 @@ class Decoder:
                 slots=slots))
 
     def generate(self, tokens, offsets, slots, steps: int, top: int = 5):
-        """The likeliest next tokens of packed prompts, one at a time.  Returns
+        """The likeliest next tokens of packed prompts (of one token at least),
+        one at a time.  Returns
         (tokens, log probabilities, entropies, alternatives), [steps, sequences]
         each ([steps, sequences, top] the last)."""
         logits = self.prompts(tokens, offsets, slots)[offsets[1:].long() - 1]
