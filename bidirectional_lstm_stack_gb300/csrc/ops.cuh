@@ -247,7 +247,6 @@ __device__ __forceinline__ void load_weights(const float *p, float (&w)[V])
 
 // ---- functions ---------------------------------------------------------------------
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x)
 {

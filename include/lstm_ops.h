@@ -148,6 +148,9 @@ int lstm_selective_scan_step(const void *u, long long u_stride, const void *dt,
  *            even (both quotients as fp32 division rounds them), so y * scale
  *            stands for n.
  * A row that holds infinities or NaN gives NaN where IEEE arithmetic does.
+ * Squares are summed in fp32: a row whose sum of squares is above 3.4e38 (values
+ * of 1e19 and more) has a norm of 0, as one with an infinity has, and squares
+ * below 1e-45 add nothing to eps.
  * 1 <= cols <= 32768.  Errors: LSTM_E_INVALID, LSTM_E_OVERFLOW,
  * LSTM_E_DEVICE, LSTM_E_CUDA. */
 int lstm_residual_rms_norm(const void *x, long long x_stride, const void *residual,

@@ -190,6 +190,15 @@ def test_tiny_and_huge_values():
     np.testing.assert_allclose(f64(y), 1.0, rtol=NORM)
 
 
+def test_rows_of_infinities_and_zeros_beside_them():
+    x = torch.ones(4, 300, device="cuda")
+    x[1, 7], x[2] = float("inf"), 0.0
+    y = f64(binding.lstm_residual_rms_norm(x, torch.ones(300, device="cuda"), 0.0)[0])
+    assert np.isnan(y[1, 7]) and (np.delete(y[1], 7) == 0).all()  # v / infinity
+    assert np.isnan(y[2]).all()  # 0 / 0
+    np.testing.assert_allclose(y[[0, 3]], 1.0, rtol=NORM)
+
+
 def test_not_a_number_stays_in_its_row():
     x = torch.ones(3, 128, device="cuda")
     x[1, 5] = float("nan")
