@@ -19,6 +19,8 @@
  *    in elements, at least cols (so it may be a slice of wider rows).  Any
  *    element-aligned address and any stride are taken; rows that start on
  *    16-byte boundaries move faster.
+ *  - Weights, biases and states are densely packed, at any element-aligned
+ *    address.
  *  - The calls allocate nothing, keep nothing between calls, wait for nothing
  *    and can be captured into a CUDA graph (after one call on the device
  *    outside a capture).  Outputs must not overlap inputs unless stated.
