@@ -1,9 +1,9 @@
-"""ctypes binding of liblstmstack.so (declared in include/lstm_stack.h and
-include/lstm_ops.h).
+"""ctypes binding of liblstmstack.so (declared in include/lstm_stack.h,
+include/lstm_ops.h and include/lstm_layers.h).
 
 Argument marshalling only: the functions compute nothing and forward to the C
 entry point of the same name.  Those of lstm_stack.h check nothing the library
-does not check again.  Those of lstm_ops.h go through the compiled module
+does not check again.  Those of lstm_ops.h and lstm_layers.h go through the compiled module
 ``_native``, which allocates outputs and alone checks shapes, types, devices and
 gradients (the C entry points take sizes and strides on trust).  Device buffers
 are torch CUDA tensors (their ``data_ptr``), streams are torch streams (their
@@ -43,6 +43,11 @@ LSTM_F32 = 0
 LSTM_BF16 = 1
 LSTM_F16 = 2
 LSTM_E4M3 = 3
+LSTM_ACT_NONE = 0
+LSTM_ACT_RELU = 1
+LSTM_ACT_GELU = 2
+LSTM_ACT_GELU_TANH = 3
+LSTM_ACT_SILU = 4
 
 _c_float_p = ctypes.POINTER(ctypes.c_float)
 _vp = ctypes.c_void_p
@@ -127,6 +132,15 @@ def load():
             "lstm_residual_rms_norm": (i, [_vp, ll, _vp, ll, i, _vp, f, i, i, _vp, ll, _vp, ll, i,
                                            _vp, i, _vp]),
             "lstm_token_logprobs": (i, [_vp, ll, i, i, i, _vp, _vp, _vp, i, _vp, _vp, _vp]),
+            "lstm_linear_attention": (i, 3 * [_vp, ll, ll, i] +
+                                      [_vp, ll, f, i, i, i, i, i, i, _vp, _vp, i, _vp, _vp, _vp, ll,
+                                       _vp, sz, _vp]),
+            "lstm_linear_attention_workspace": (sz, [i, i, i, i, i, i]),
+            "lstm_linear_attention_step": (i, 3 * [_vp, ll, ll, i] +
+                                           [_vp, ll, f, i, i, i, i, i, _vp, i, _vp, _vp, ll, _vp]),
+            "lstm_dense": (i, [_vp, ll, _vp, ll, _vp, i, _vp, ll, i, i, i, i, _vp, ll, _vp, sz,
+                               _vp]),
+            "lstm_dense_workspace": (sz, [_vp, ll, _vp, ll, i, i, i, i]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -500,3 +514,61 @@ def lstm_token_logprobs(logits, tokens=None, *, top: int = 0, entropy: bool = Tr
     returns (logp, entropy, top_logp, top_ids): fp32 [rows], fp32 [rows], fp32
     and int64 [rows, top]; None for what is not asked for."""
     return (_ops or _load_ops()).token_logprobs(logits, tokens, top, entropy, stream)
+
+
+# ---- linear attention and dense products (include/lstm_layers.h) -------------------
+#
+# Checked, allocated and called as the functions above.
+
+def lstm_linear_attention(q, k, v, log_decay, *, scale: float = 1.0, sequences=None, offsets=None,
+                          state=None, slots=None, resume=None, y=None, stream=None):
+    """Linear attention with a decay for each head over packed prompts,
+    S = e^log_decay S + k v^T, y = scale S^T q; returns y [tokens, heads,
+    values] (new unless given) and moves the state, if given, on.
+
+    q [tokens, q_heads, keys], k [tokens, k_heads, keys], v [tokens, v_heads,
+    values], each with any strides between tokens and heads, their heads shared
+    by groups of the call's; log_decay fp32 [heads], or [tokens, heads] for
+    each token its own; offsets int32 [sequences + 1] (None: `sequences`
+    prompts of equal length, default one); state [slots, heads, keys, values]
+    fp32, slots and resume int32 [sequences]."""
+    return (_ops or _load_ops()).linear_attention(q, k, v, log_decay, scale, sequences, offsets,
+                                                  state, slots, resume, y, stream)
+
+
+def lstm_linear_attention_workspace(tokens: int, heads: int, keys: int, values: int,
+                                    sequences: int, equal_lengths: bool) -> int:
+    """Bytes of workspace of lstm_linear_attention."""
+    return load().lstm_linear_attention_workspace(tokens, heads, keys, values, sequences,
+                                                  int(equal_lengths))
+
+
+def lstm_linear_attention_step(q, k, v, log_decay, state, *, scale: float = 1.0, slots=None,
+                               y=None, stream=None):
+    """The next token of every sequence, q [sequences, q_heads, keys] and so on;
+    returns y (new unless given) and moves the state on.  Arguments as
+    lstm_linear_attention."""
+    return (_ops or _load_ops()).linear_attention_step(q, k, v, log_decay, state, scale, slots, y,
+                                                       stream)
+
+
+_ACTIVATIONS = {None: LSTM_ACT_NONE, "relu": LSTM_ACT_RELU, "gelu": LSTM_ACT_GELU,
+                "gelu_tanh": LSTM_ACT_GELU_TANH, "silu": LSTM_ACT_SILU}
+
+
+def lstm_dense(x, w, bias=None, *, activation=None, residual=None, y=None, stream=None):
+    """act(x w^T + bias) + residual of x [rows, in] and w [out, in] of one type;
+    returns y [rows, out] (new unless given; may be residual).
+
+    bias [out] fp32; activation None, "relu", "gelu", "gelu_tanh" or "silu";
+    residual [rows, out] of x's type."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation {activation!r}, expected one of {list(_ACTIVATIONS)}")
+    return (_ops or _load_ops()).dense(x, w, bias, _ACTIVATIONS[activation], residual, y, stream)
+
+
+def lstm_dense_workspace(x, x_stride: int, w, w_stride: int, dtype: int, rows: int, inputs: int,
+                         outputs: int) -> int:
+    """Bytes of workspace of lstm_dense (x and w tensors)."""
+    return load().lstm_dense_workspace(_ptr(x), x_stride, _ptr(w), w_stride, dtype, rows, inputs,
+                                       outputs)

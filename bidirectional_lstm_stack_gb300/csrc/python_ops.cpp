@@ -1,4 +1,4 @@
-// The calls of binding.py's functions of lstm_ops.h on torch tensors: what a call's
+// The calls of binding.py's functions of lstm_ops.h and lstm_layers.h on torch tensors: what a call's
 // sizes promise is checked here (the C entry points take sizes and strides on
 // trust), outputs that are not given are allocated for the stream that the call
 // runs on, and everything else is the library's.  Small calls last longer on the
@@ -16,9 +16,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <optional>
 
-#include "lstm_ops.h"
+#include "lstm_layers.h"
 
 namespace {
 
@@ -108,10 +109,11 @@ struct Rows {
     at::ScalarType type;
     at::Device device;
 
-    Rows(const char *name, const Tensor &m)
+    Rows(const char *name, const Tensor &m, int dims = 2)
         : t(m), rows(0), cols(0), type(m.scalar_type()), device(m.device())
     {
-        TORCH_CHECK_VALUE(m.dim() == 2, name, " has shape ", m.sizes(), ", expected two dimensions");
+        TORCH_CHECK_VALUE(m.dim() == dims, name, " has shape ", m.sizes(), ", expected ",
+                          dims == 2 ? "two" : "three", " dimensions");
         TORCH_CHECK_VALUE(device.is_cuda(), name, " is on ", device, ", expected a CUDA device");
         rows = m.size(0);
         cols = m.size(1);
@@ -177,8 +179,9 @@ struct State {
         const int64_t n = t->dim() > 0 ? t->size(0) : 0;
         TORCH_CHECK_VALUE(slots_o || n >= sequences, sequences, " sequences without slots, a state of ",
                           n);
-        const int64_t shape[3] = {n, inner[0], inner[1]};
-        at = dense("state", t, shape, type, r);
+        int64_t shape[4] = {n};
+        std::copy(inner.begin(), inner.end(), shape + 1);
+        at = dense("state", t, {shape, inner.size() + 1}, type, r);
         count = as_int("state's slots", n);
         slots = indices("slots", slots_o, sequences, r);
         resume = indices("resume", resume_o, sequences, r);
@@ -488,6 +491,152 @@ PyObject *token_logprobs(PyObject *, PyObject *const *args, Py_ssize_t count)
     END_HANDLE_TH_ERRORS
 }
 
+// Rows of heads [rows, heads, width]: consecutive widths, any strides between heads and rows.
+struct Heads {
+    const void *at;
+    long long stride, head_stride;
+    int count;
+
+    Heads(const char *name, const Tensor &m, int64_t width, const Rows &r)
+    {
+        TORCH_CHECK_VALUE(m.dim() == 3 && m.size(0) == r.rows && m.size(2) == width &&
+                              m.scalar_type() == r.type && m.device() == r.device,
+                          name, " is ", m.scalar_type(), " ", m.sizes(), " on ", m.device(),
+                          ", expected ", r.type, " [", r.rows, ", heads, ", width, "] on ", r.device);
+        TORCH_CHECK_VALUE(width <= 1 || m.stride(2) == 1, name,
+                          " needs consecutive numbers in a head, has stride ", m.stride(2),
+                          " between them");
+        at = m.data_ptr();
+        stride = m.stride(0);
+        head_stride = m.stride(1);
+        count = as_int(name, m.size(1));
+    }
+};
+
+// What both functions of linear attention begin with.
+struct Attention {
+    int64_t keys, values, heads;
+    Heads q, k, v;
+    const float *decay;
+    long long decay_stride = 0;
+    float scale;
+
+    Attention(const Rows &r, PyObject *k_o, PyObject *v_o, PyObject *decay_o, PyObject *scale_o)
+        : keys(r.t.size(2)), values(last_size("v", tensor("v", v_o))),
+          heads(last_size("log_decay", tensor("log_decay", decay_o))), q("q", r.t, keys, r),
+          k("k", tensor("k", k_o), keys, r), v("v", tensor("v", v_o), values, r)
+    {
+        const Tensor &d = tensor("log_decay", decay_o);
+        if (d.dim() == 2) {
+            decay_stride = matrix("log_decay", d, r.rows, heads, at::kFloat, r);
+            decay = static_cast<const float *>(d.data_ptr());
+        } else {
+            decay = weights("log_decay", decay_o, {heads}, r);
+        }
+        TORCH_CHECK_TYPE(scale_o, "scale is None");
+        const double s = PyFloat_AsDouble(scale_o);
+        if (s == -1.0 && PyErr_Occurred())
+            throw python_error();
+        scale = static_cast<float>(s);
+    }
+    // Row stride of the outputs [rows, heads, values], a row's heads consecutive.
+    long long y_stride(const Tensor &y, const Rows &r) const
+    {
+        const Heads h("y", y, values, r);
+        TORCH_CHECK_VALUE(h.count == heads && (heads <= 1 || h.head_stride == values), "y is ",
+                          y.sizes(), " with heads ", h.head_stride, " apart, expected ", heads,
+                          " consecutive heads of ", values);
+        return h.stride;
+    }
+};
+
+PyObject *linear_attention(PyObject *, PyObject *const *args, Py_ssize_t count)
+{
+    HANDLE_TH_ERRORS
+    const Arguments<12> v(args, count);
+    const Rows q("q", tensor("q", v[0]), 3);
+    const int type = element_type(q.t);
+    const Attention a(q, v[1], v[2], v[3], v[4]);
+    const Prompts p(v[5], v[6], q);
+    const State state(v[7], v[8], v[9], {a.heads, a.keys, a.values}, at::kFloat, p.count, q);
+    const Stream stream(v[11], q);
+    const Tensor y = stream.output("y", v[10], {q.rows, a.heads, a.values}, q.type);
+    const long long y_stride = a.y_stride(y, q);
+    const int tokens = as_int("tokens", q.rows), heads = as_int("heads", a.heads),
+              keys = as_int("keys", a.keys), values = as_int("values", a.values),
+              sequences = as_int("sequences", p.count);
+    const size_t bytes =
+        lstm_linear_attention_workspace(tokens, heads, keys, values, sequences, !p.offsets);
+    Tensor workspace;
+    if (bytes)
+        workspace = stream.empty({static_cast<int64_t>(bytes)}, at::kByte);
+    call(lstm_linear_attention, a.q.at, a.q.stride, a.q.head_stride, a.q.count, a.k.at, a.k.stride,
+         a.k.head_stride, a.k.count, a.v.at, a.v.stride, a.v.head_stride, a.v.count, a.decay,
+         a.decay_stride, a.scale, type, tokens, heads, keys, values, sequences, p.offsets,
+         static_cast<float *>(state.at), state.count, state.slots, state.resume, y.data_ptr(),
+         y_stride, bytes ? workspace.data_ptr() : nullptr, bytes, stream.at);
+    written(v[7]);
+    written(v[10]);
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *linear_attention_step(PyObject *, PyObject *const *args, Py_ssize_t count)
+{
+    HANDLE_TH_ERRORS
+    const Arguments<9> v(args, count);
+    const Rows q("q", tensor("q", v[0]), 3);
+    const int type = element_type(q.t);
+    const Attention a(q, v[1], v[2], v[3], v[5]);
+    const State state(v[4], v[6], nullptr, {a.heads, a.keys, a.values}, at::kFloat, q.rows, q);
+    const Stream stream(v[8], q);
+    const Tensor y = stream.output("y", v[7], {q.rows, a.heads, a.values}, q.type);
+    const long long y_stride = a.y_stride(y, q);
+    call(lstm_linear_attention_step, a.q.at, a.q.stride, a.q.head_stride, a.q.count, a.k.at,
+         a.k.stride, a.k.head_stride, a.k.count, a.v.at, a.v.stride, a.v.head_stride, a.v.count,
+         a.decay, a.decay_stride, a.scale, type, as_int("sequences", q.rows),
+         as_int("heads", a.heads), as_int("keys", a.keys), as_int("values", a.values),
+         static_cast<float *>(state.at), state.count, state.slots, y.data_ptr(), y_stride,
+         stream.at);
+    written(v[4]);
+    written(v[7]);
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *dense_product(PyObject *, PyObject *const *args, Py_ssize_t count)
+{
+    HANDLE_TH_ERRORS
+    const Arguments<7> v(args, count);
+    const Rows x("x", tensor("x", v[0]));
+    const int type = element_type(x.t);
+    const long long x_stride = matrix("x", x.t, x.rows, x.cols, x.type, x);
+    const Tensor &w = tensor("w", v[1]);
+    const int64_t out = w.dim() > 0 ? w.size(0) : 0;
+    const long long w_stride = matrix("w", w, out, x.cols, x.type, x);
+    const float *bias = weights("bias", v[2], {out}, x);
+    const Tensor *residual = optional_tensor("residual", v[4]);
+    const long long residual_stride =
+        residual ? matrix("residual", *residual, x.rows, out, x.type, x) : 0;
+    const Stream stream(v[6], x);
+    const Tensor y = stream.output("y", v[5], {x.rows, out}, x.type);
+    const long long y_stride = matrix("y", y, x.rows, out, x.type, x);
+    const int rows = as_int("rows", x.rows), in = as_int("columns of x", x.cols),
+              columns = as_int("rows of w", out);
+    const size_t bytes = lstm_dense_workspace(x.t.data_ptr(), x_stride, w.data_ptr(), w_stride,
+                                              type, rows, in, columns);
+    Tensor workspace;
+    if (bytes)
+        workspace = stream.empty({static_cast<int64_t>(bytes)}, at::kByte);
+    call(lstm_dense, x.t.data_ptr(), x_stride, w.data_ptr(), w_stride, bias,
+         as_int("activation", number(v[3], LSTM_ACT_NONE)), residual ? residual->data_ptr() : nullptr,
+         residual_stride, type, rows, in, columns, y.data_ptr(), y_stride,
+         bytes ? workspace.data_ptr() : nullptr, bytes, stream.at);
+    written(v[5]);
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_XSETREF(g_error, Py_NewRef(cls));
@@ -508,6 +657,9 @@ PyMethodDef methods[] = {
     method<selective_scan_step>("selective_scan_step"),
     method<residual_rms_norm>("residual_rms_norm"),
     method<token_logprobs>("token_logprobs"),
+    method<linear_attention>("linear_attention"),
+    method<linear_attention_step>("linear_attention_step"),
+    method<dense_product>("dense"),
     {"set_error", set_error, METH_O, "The class of the library's errors."},
     {nullptr, nullptr, 0, nullptr},
 };

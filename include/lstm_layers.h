@@ -1,0 +1,118 @@
+/*
+ * lstm_layers.h -- the part of liblstmstack.so's C ABI for layers whose state
+ * is a matrix per head, and for the dense products around them:
+ *  - lstm_linear_attention, lstm_linear_attention_step: linear attention with a
+ *    decay for each head over prompts, and over the next token of each sequence;
+ *  - lstm_dense: a matrix product with bias, activation and residual.
+ *
+ * The conventions of lstm_ops.h hold: its element types, matrices with row
+ * strides, packed sequences, pools of states, and its return codes.
+ */
+#ifndef LSTM_LAYERS_H
+#define LSTM_LAYERS_H
+
+#include "lstm_ops.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define LSTM_ATTENTION_MAX_KEYS 128
+#define LSTM_ATTENTION_MAX_VALUES 256
+#define LSTM_ATTENTION_MAX_HEADS 32768
+
+/* Linear attention, each sequence for itself and each head h with a state S of
+ * `keys` x `values` numbers:
+ *   S          = e^(log_decay[t][h]) * S + k[t] v[t]^T
+ *   y[t][h][c] = scale * sum_n q[t][n] * S[n][c]
+ * with q, k and v of head h's group.
+ *   q, k : device [tokens][q_heads or k_heads][keys]; consecutive keys, the
+ *          heads of a token *_head_stride elements apart (not read for one
+ *          head) and the tokens *_stride, each at least keys (so a token's
+ *          heads may lie side by side, or all tokens of a head)
+ *   v    : device [tokens][v_heads][values], as q and k
+ *          q_heads, k_heads and v_heads divide heads; head h has the head
+ *          h / (heads / q_heads) of q, and so on
+ *   log_decay : device fp32, decay_stride 0: [heads], the same for every
+ *          token; else [tokens][heads] with that row stride (at least heads).
+ *          A value of -infinity forgets the state; values are below 88
+ *   y    : device [tokens][heads][values], the heads of a token consecutive
+ *          and the tokens y_stride apart (at least heads * values)
+ *   state : device [state_slots][heads][keys][values] fp32, or NULL: no
+ *          states (state_slots, slots and resume are then not read)
+ *   workspace : device, 16-byte aligned, workspace_bytes long and at least
+ *          lstm_linear_attention_workspace(...) bytes of the same sizes (0:
+ *          may be NULL); its contents need not be kept between calls, but two
+ *          calls that may run at the same time need one each
+ * 1 <= keys <= LSTM_ATTENTION_MAX_KEYS, 1 <= values <=
+ * LSTM_ATTENTION_MAX_VALUES, 1 <= heads <= LSTM_ATTENTION_MAX_HEADS.
+ * States are fp32, and what a token adds to them is off by 2^-15 of itself at
+ * most.  With 16-bit types the products that make y take the state and the
+ * products of queries and keys rounded to parts of bf16 (LSTM_BF16: 8 bits,
+ * LSTM_F16: 16); with LSTM_F32 everything keeps 24 bits.
+ * An infinity or a NaN makes what depends on it, itself or through a state,
+ * infinite or NaN; tokens before it, other heads and sequences are as without.
+ * A wait inside the kernel that does not end within two seconds sets the
+ * library's fault word (lstm_fault_status); outputs and states are then
+ * unspecified.
+ * Errors: LSTM_E_INVALID (null, sizes, type, stride, device), LSTM_E_LENGTH
+ * (offsets NULL and tokens no multiple of sequences; a workspace that is too
+ * short), LSTM_E_OVERFLOW, LSTM_E_DEVICE, LSTM_E_CUDA. */
+size_t lstm_linear_attention_workspace(int tokens, int heads, int keys, int values, int sequences,
+                                       int equal_lengths);
+int lstm_linear_attention(const void *q, long long q_stride, long long q_head_stride, int q_heads,
+                          const void *k, long long k_stride, long long k_head_stride, int k_heads,
+                          const void *v, long long v_stride, long long v_head_stride, int v_heads,
+                          const float *log_decay, long long decay_stride, float scale, int dtype,
+                          int tokens, int heads, int keys, int values, int sequences,
+                          const int *offsets, float *state, int state_slots, const int *slots,
+                          const int *resume, void *y, long long y_stride, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* The next token of every sequence: row s of q, k, v, log_decay and y is
+ * sequence s's, and its state moves on by one token, all in fp32.  Arguments
+ * and errors as lstm_linear_attention; state is required. */
+int lstm_linear_attention_step(const void *q, long long q_stride, long long q_head_stride,
+                               int q_heads, const void *k, long long k_stride,
+                               long long k_head_stride, int k_heads, const void *v,
+                               long long v_stride, long long v_head_stride, int v_heads,
+                               const float *log_decay, long long decay_stride, float scale,
+                               int dtype, int sequences, int heads, int keys, int values,
+                               float *state, int state_slots, const int *slots, void *y,
+                               long long y_stride, void *stream);
+
+/* Activations of lstm_dense. */
+enum {
+    LSTM_ACT_NONE = 0,
+    LSTM_ACT_RELU = 1,      /* max(v, 0) */
+    LSTM_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2 */
+    LSTM_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    LSTM_ACT_SILU = 4       /* v / (1 + e^-v) */
+};
+
+/* y[r][n] = act(sum_k x[r][k] * w[n][k] + bias[n]) + residual[r][n]
+ *   x        : device [rows][in]
+ *   w        : device [out][in] of x's type, row stride w_stride
+ *   bias     : device [out] fp32, or NULL
+ *   residual : device [rows][out] of x's type, or NULL; may be y
+ *   y        : device [rows][out]
+ *   workspace: as lstm_linear_attention's; lstm_dense_workspace(...) bytes
+ * Products and sums are fp32, with LSTM_F32 too (each product keeps 24 bits of
+ * its factors).  16-bit x and w whose rows all start on 16-byte boundaries are
+ * read in place; others, and fp32, go through the workspace first.
+ * An infinity or a NaN in x or w makes its row's or column's results infinite
+ * or NaN.  Waits inside the kernel are bounded as lstm_linear_attention's.
+ * Errors: LSTM_E_INVALID, LSTM_E_LENGTH (workspace), LSTM_E_OVERFLOW,
+ * LSTM_E_DEVICE, LSTM_E_CUDA. */
+size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w, long long w_stride,
+                            int dtype, int rows, int in, int out);
+int lstm_dense(const void *x, long long x_stride, const void *w, long long w_stride,
+               const float *bias, int activation, const void *residual, long long residual_stride,
+               int dtype, int rows, int in, int out, void *y, long long y_stride, void *workspace,
+               size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LSTM_LAYERS_H */

@@ -1,0 +1,177 @@
+"""The dense product against its float64 definition: types, sizes that no tile
+divides, activations, residuals, strides and alignment, values that are not
+finite, streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+from bidirectional_lstm_stack_gb300 import binding
+from oracle import layers as oracle
+from ops_util import DTYPES, assert_close, at_element, f64, gen, normal, slice_of
+
+pytestmark = pytest.mark.gpu
+
+
+def _check(dtype, rows, n_in, n_out, *, bias=True, activation=None, residual=True, layout="dense",
+           seed=1, in_place=False):
+    g, t = gen(seed), DTYPES[dtype]
+    x = normal(g, rows, n_in, dtype=t)
+    w = normal(g, n_out, n_in, scale=n_in ** -0.5, dtype=t)
+    b = normal(g, n_out) if bias else None
+    r = normal(g, rows, n_out, dtype=t) if residual else None
+    if layout != "dense":
+        pad = {"slices": 8, "odd": 3}[layout]
+        x, w = slice_of(x, pad, pad), slice_of(w, pad, pad)
+        r = None if r is None else slice_of(r, pad, pad)
+    y = None
+    if layout != "dense":
+        y = slice_of(torch.zeros(rows, n_out, dtype=t, device="cuda"), pad, pad)
+    ref, bound = oracle.dense(f64(x), f64(w), f64(b), activation, f64(r))
+    if in_place:
+        y = r
+    got = binding.lstm_dense(x, w, b, activation=activation, residual=r, y=y)
+    assert y is None or got is y
+    assert_close(got, ref, bound, dtype, f"{dtype} {rows}x{n_in}x{n_out}")
+    return got
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [0, 1, 2, 3, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 200,
+                                  257, 600])
+def test_rows(dtype, rows):
+    _check(dtype, rows, 96, 136)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 5, 40, 130])
+@pytest.mark.parametrize("n_in,n_out", [(1, 1), (1, 300), (7, 5), (64, 64), (63, 65), (65, 127), (129, 257),
+                                        (777, 1003), (256, 1024), (1000, 8), (2048, 24)])
+def test_sizes(dtype, rows, n_in, n_out):
+    _check(dtype, rows, n_in, n_out, bias=n_in != 64, residual=n_out != 65)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("activation", [None, "relu", "gelu", "gelu_tanh", "silu"])
+def test_activations(dtype, rows, activation):
+    for bias, residual in ((False, False), (True, False), (False, True), (True, True)):
+        _check(dtype, rows, 80, 72, activation=activation, bias=bias, residual=residual)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("layout", ["slices", "odd"])
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 64, 64), (40, 100, 90), (150, 128, 256), (300, 33, 31)])
+def test_columns_of_wider_rows(dtype, layout, rows, n_in, n_out):
+    _check(dtype, rows, n_in, n_out, layout=layout)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_the_residual_in_place(dtype):
+    for rows, layout in ((1, "dense"), (17, "odd"), (300, "dense"), (300, "slices")):
+        _check(dtype, rows, 200, 264, in_place=True, layout=layout, activation="silu")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_weights_and_biases_at_any_element(dtype):
+    g = gen(3)
+    x, w, b = (normal(g, 70, 64, dtype=DTYPES[dtype]), normal(g, 96, 64, dtype=DTYPES[dtype]),
+               normal(g, 96))
+    ref = binding.lstm_dense(x, w, b)
+    for offset in (1, 2, 3, 4, 5):
+        for m in (dict(x=at_element(x, offset)), dict(w=at_element(w, offset)),
+                  dict(b=at_element(b, offset))):
+            m = {"x": x, "w": w, "b": b, **m}
+            assert torch.equal(binding.lstm_dense(m["x"], m["w"], m["b"]), ref)
+
+
+def test_larger_products():
+    _check("bf16", 1100, 1024, 1536)
+    _check("f16", 1030, 520, 2050, activation="gelu")
+    _check("f32", 700, 600, 900, activation="gelu_tanh")
+    _check("bf16", 1, 4096, 2048)
+    _check("bf16", 33, 4100, 1000)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [5, 200])
+def test_values_that_are_not_finite_stay_in_their_rows_and_columns(dtype, rows):
+    g, t = gen(1), DTYPES[dtype]
+    x, w = normal(g, rows, 100, dtype=t), normal(g, 150, 100, dtype=t)
+    y = binding.lstm_dense(x, w)
+    x[3, 40], w[70, 99], w[90, 0] = float("inf"), float("nan"), float("-inf")
+    got = binding.lstm_dense(x, w)
+    assert not got[3].isfinite().any() and not got[:, [70, 90]].isfinite().any()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[3] = False
+    keep[:, [70, 90]] = False
+    assert torch.equal(got[keep], y[keep])
+    # of the residual and the bias too, and nothing is hidden by an activation
+    r, b = torch.zeros(rows, 150, dtype=t, device="cuda"), torch.zeros(150, device="cuda")
+    r[0, 5], b[6] = float("nan"), float("nan")
+    for activation in (None, "relu", "gelu", "gelu_tanh", "silu"):
+        got = binding.lstm_dense(x, w, b, activation=activation, residual=r)
+        assert got[0, 5].isnan() and got[:, 6].isnan().all() and got[:, 70].isnan().all()
+
+
+@pytest.mark.parametrize("activation", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_activations_far_out(activation):
+    v = torch.tensor([-1e30, -200.0, -90.0, -20.0, -0.0, 0.0, 20.0, 90.0, 1e30], device="cuda")
+    got = binding.lstm_dense(v[:, None], torch.ones(1, 1, device="cuda"), activation=activation)[:, 0]
+    ref = oracle.activate(activation, f64(v))
+    # below -12 the functions' factor is the difference of numbers next to 1
+    assert np.allclose(f64(got), ref, rtol=2.0 ** -20, atol=1e-5)
+
+
+def test_large_and_small_fp32_numbers():
+    x = torch.tensor([[3.4e38, 0.0], [0.0, 1e-30], [1.0, 2.0 ** -23]], device="cuda")
+    w = torch.tensor([[1.0, 1.0], [0.5, 1.0]], device="cuda")
+    got = binding.lstm_dense(x, w)
+    assert torch.equal(got, x @ w.t())
+
+
+def test_the_same_call_gives_the_same_bits():
+    for rows in (1, 20, 700):
+        g = gen(1)
+        x, w = normal(g, rows, 2048, dtype=torch.bfloat16), normal(g, 512, 2048, dtype=torch.bfloat16)
+        y = binding.lstm_dense(x, w)
+        for _ in range(3):
+            assert torch.equal(binding.lstm_dense(x, w), y)
+
+
+def test_other_streams_and_calls_at_once():
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for dtype, offset in ((torch.bfloat16, 0), (torch.float32, 0), (torch.float16, 1)):
+        m = [(at_element(normal(gen(s), 300, 640, dtype=dtype), offset), normal(gen(s), 500, 640, dtype=dtype))
+             for s in (1, 2)]
+        alone = [binding.lstm_dense(x, w) for x, w in m]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            got = [binding.lstm_dense(x, w, stream=s) for (x, w), s in zip(m, streams)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(alone, got))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 30, 300])
+def test_a_captured_call_reads_what_is_there_when_it_is_replayed(dtype, rows):
+    g, t = gen(1), DTYPES[dtype]
+    x, w = normal(g, rows, 512, dtype=t), normal(g, 384, 512, dtype=t)
+    y = torch.empty(rows, 384, dtype=t, device="cuda")
+    binding.lstm_dense(x, w, y=y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.lstm_dense(x, w, y=y)
+    for _ in range(2):
+        x.copy_(normal(g, rows, 512))
+        w.copy_(normal(g, 384, 512))
+        graph.replay()
+        assert torch.equal(y, binding.lstm_dense(x, w))
+
+
+def test_launch_failures_are_errors():
+    lib = binding.load()
+    x, w = torch.zeros(5, 8, device="cuda"), torch.zeros(8, 8, device="cuda")
+    assert lib.lstm_test_fail_launches(0, 1) == 0
+    with pytest.raises(binding.LSTMError):
+        binding.lstm_dense(x, w)
+    binding.lstm_dense(x, w)
