@@ -24,7 +24,7 @@
 #include <string>
 
 #include "common.cuh"
-#include "lstm_ops.h"
+#include "lstm_layers.h"
 
 namespace lstm {
 
@@ -1094,6 +1094,16 @@ extern "C" int lstm_test_recurrence_timeout(int withhold, unsigned int wait_limi
 extern "C" int lstm_test_projection_timeout(int withhold, unsigned int wait_limit_us, int device)
 {
     return set_timeout_test(kTestProjection, "projection", withhold, wait_limit_us, device);
+}
+
+extern "C" int lstm_test_attention_timeout(int withhold, unsigned int wait_limit_us, int device)
+{
+    return set_timeout_test(kTestAttention, "attention", withhold, wait_limit_us, device);
+}
+
+extern "C" int lstm_test_dense_timeout(int withhold, unsigned int wait_limit_us, int device)
+{
+    return set_timeout_test(kTestDense, "dense", withhold, wait_limit_us, device);
 }
 
 extern "C" int lstm_test_scan_step_timeout(int withhold, unsigned int wait_limit_us, int device)

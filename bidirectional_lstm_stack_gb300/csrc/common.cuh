@@ -66,7 +66,9 @@ enum TestKernel {
     kTestProjection = 1,
     kTestHeads = 2,
     kTestScanStep = 3,
-    kTestKernels = 4
+    kTestAttention = 4,
+    kTestDense = 5,
+    kTestKernels = 6
 };
 // The settings of `kernel` on the current device.
 KernelTest kernel_test(int kernel);
@@ -124,6 +126,11 @@ int projection_prepare(int device);
 // Store map of a row-major fp32 matrix [rows][cols] written in 32 x 32
 // slices with the 128-byte swizzle (the projection's G).
 int encode_store_map(CUtensorMap *map, float *base, long rows, int cols);
+// Map of a matrix [rows][cols] of `type` (base and row pitch multiples of 16
+// bytes) in boxes of 128 bytes x box_rows rows with the 128-byte swizzle;
+// what a box has beyond the matrix reads as zeros and is not written.
+int encode_box_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, long long rows,
+                   long long cols, long long pitch_bytes, int box_rows);
 
 // ---- dense heads of the segmentation model (heads.cu) ----------------------
 // W rows of one k-block of the heads' weights (all 128 output columns).
@@ -355,6 +362,27 @@ __device__ __forceinline__ void mma_tf32_tmem_a(uint32_t d_tmem, uint32_t a_tmem
                  "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16 (both fp16 or both
+// bf16), one CTA.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// The same with A in tensor memory: two consecutive K elements a 32-bit column.
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
 // Arrives once on `bar` when every tcgen05 operation this thread issued
 // before has completed.
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
@@ -542,6 +570,29 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t addr)
            (static_cast<uint64_t>(512 >> 4) << 32) |    // stride offset: 8 rows x 64 B
            (static_cast<uint64_t>(1) << 46) |           // descriptor version (tcgen05)
            (static_cast<uint64_t>(4) << 61);            // 64-byte swizzle
+}
+
+// Operands with the 128-byte swizzle, rows of 128 bytes, 8-row groups 1024 bytes
+// apart.  K-major: a row holds 64 consecutive K elements of one M or N index.
+// MN-major: a row holds 64 consecutive M or N elements of one K index, and the
+// next 64 of them lie `next` bytes on.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t next = 16)
+{
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+           (static_cast<uint64_t>(next >> 4) << 16) |   // leading offset (unused when K-major)
+           (static_cast<uint64_t>(1024 >> 4) << 32) |   // stride offset: 8 rows x 128 B
+           (static_cast<uint64_t>(1) << 46) |           // descriptor version (tcgen05)
+           (static_cast<uint64_t>(2) << 61);            // 128-byte swizzle
+}
+
+// Instruction descriptor of kind::f16, M = m, N = n: D fp32, A and B bf16 (or
+// fp16), each K-major or MN-major.
+__host__ __device__ constexpr uint32_t f16_idesc(int m, int n, bool bf16, bool a_mn = false,
+                                                 bool b_mn = false)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+           (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // Instruction descriptor of kind::tf32, M = m, N = n: D fp32, A and B TF32,

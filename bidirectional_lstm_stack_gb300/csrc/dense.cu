@@ -1,22 +1,60 @@
 // Dense product with bias, activation and residual in its epilogue:
 //     y[r][n] = act(sum_k x[r][k] w[n][k] + bias[n]) + residual[r][n].
+//
+// One kernel (sm_103a) of warps with one task each:
+//  * warp 0 (one thread) streams K blocks of 64 (128 bytes, 128-byte swizzle) of the
+//    tile's two operands through a ring of stages with TMA;
+//  * warp 1 (one thread) issues tcgen05.mma kind::f16, M = 128, into a tensor-memory
+//    accumulator;
+//  * warps 2-5 read a finished accumulator (a lane per row of the tile), add the bias,
+//    apply the activation, add the residual and store.
+// Many rows: M are 128 rows of x and N up to 256 rows of w; one CTA an SM walks over
+// the tiles, and a second accumulator lets a tile's epilogue run under the next tile's
+// products.  Few rows (at most kFewRows): the operands change places, M are 128 rows
+// of w and N the 16 to 64 rows of x, so that a tile's 128 lanes all work and w streams
+// once.  Where a call has fewer tiles than SMs, the CTAs of a cluster take a part of K
+// each and join their sums through distributed shared memory, in the order of the parts.
+//
+// fp32 goes as bf16: x = x1 + x2 + x3 exactly, each the 8 leading bits of what the ones
+// before it leave, and of the nine products of two numbers' parts the six that reach
+// 2^-24 of the product are summed, the small ones first.  The split, and a copy to
+// 16-byte pitches of 16-bit operands that TMA cannot read in place, is a kernel before.
+#include <mutex>
+
 #include "lstm_layers.h"
 #include "ops.cuh"
 
 namespace lstm {
 namespace {
 
+constexpr int BM = 128;
+constexpr int BK = 64;
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int kFewRows = 64;
+constexpr int kMaxStages = 8;
+constexpr int kParts = 3;      // of an fp32 number
+constexpr int kProducts = 6;   // of two of them
+constexpr int THREADS = 192;
+constexpr int PRODUCER_WARP = 0, MMA_WARP = 1;
+constexpr int SLICE_BYTES = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out
+
 struct DenseArgs {
-    const void *x, *w;
-    long long x_stride, w_stride;
     const float *bias;
-    int activation;
     const void *residual;
-    long long residual_stride;
-    int rows, in, out;
     void *y;
-    long long y_stride;
+    long long residual_stride, y_stride;
+    int rows, in, out;
+    int activation;
+    int products;         // 1, or kProducts
+    int split;            // CTAs of a cluster, each a part of K
+    bool store_boxes;     // y takes TMA stores
+    bool vectors;         // the residual's rows start on 16-byte boundaries
+    int group;            // tiles down M that run side by side
 };
+
+// Which parts of x and w the p-th product takes.
+__host__ __device__ constexpr int part_of_x(int p) { return p == 0 ? 2 : p == 1 || p == 3 ? 1 : 0; }
+__host__ __device__ constexpr int part_of_w(int p) { return p == 2 ? 2 : p == 1 || p == 4 ? 1 : 0; }
 
 __device__ __forceinline__ float activate(int kind, float v)
 {
@@ -34,45 +72,532 @@ __device__ __forceinline__ float activate(int kind, float v)
     }
 }
 
-constexpr int kTile = 32;
+template <int BN_, bool SWAP_>
+struct Shape {
+    static constexpr int BN = BN_;
+    static constexpr bool SWAP = SWAP_;
+    static constexpr int B_BYTES = BN * BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    // few rows: two CTAs an SM
+    static constexpr int DATA_BYTES = SWAP ? 104 * 1024 : 224 * 1024;
+    static constexpr int OUT_BYTES = SWAP ? 0 : 4 * 2 * SLICE_BYTES;
+    static constexpr int FIT = (DATA_BYTES - OUT_BYTES) / STAGE_BYTES;
+    static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int ACCS = SWAP ? 1 : 2;
+    static constexpr int TMEM_COLS = ACCS * BN < 32 ? 32 : ACCS * BN;
+    static constexpr int CW = BN < 32 ? BN : 32;  // columns read at a time
+    static constexpr size_t SMEM_BYTES = RING_BYTES + OUT_BYTES + 256 + 1024;
+    static_assert(STAGES >= 4 && BN * BM * 4 <= RING_BYTES, "ring");
+    static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+};
+
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t taddr, float (&f)[N])
+{
+    uint32_t r[N];
+    if constexpr (N == 32)
+        ptx::tmem_ld_32x32b_x32(taddr, r);
+    else
+        ptx::tmem_ld_32x32b_x16(taddr, r);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        f[i] = __uint_as_float(r[i]);
+}
+
+template <class S, typename T>
+__global__ void __launch_bounds__(THREADS, S::SWAP ? 2 : 1)
+dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+             const __grid_constant__ CUtensorMap y_map, const DenseArgs p, uint32_t idesc,
+             long long tiles, int tiles_m, unsigned *fault, KernelTest test)
+{
+    constexpr int BN = S::BN, STAGES = S::STAGES, CW = S::CW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *out_slices = smem + S::RING_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(out_slices + S::OUT_BYTES);
+    uint64_t *empty = full + kMaxStages;
+    uint64_t *acc_full = empty + kMaxStages;  // [2]
+    uint64_t *acc_empty = acc_full + 2;       // [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(&acc_full[a], 1);
+            ptx::mbar_init(&acc_empty[a], 128);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&a_map);
+        ptx::prefetch_tensormap(&b_map);
+    }
+    if (warp == MMA_WARP) {
+        ptx::tmem_alloc(tmem_slot, S::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // this CTA's tiles, and its part of their K blocks
+    const int part = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const long long first = blockIdx.x / p.split, step = gridDim.x / p.split;
+    const int kblocks = (p.in + BK - 1) / BK, all = kblocks * p.products;
+    const int kb_begin = static_cast<int>(static_cast<long long>(all) * part / p.split);
+    const int kb_end = static_cast<int>(static_cast<long long>(all) * (part + 1) / p.split);
+    const auto place = [&](long long t, int *m, int *n) {
+        // groups of tiles down M, inside them down M first
+        const long long tiles_n = tiles / tiles_m;
+        const long long g = t / (p.group * tiles_n), in_group = t - g * p.group * tiles_n;
+        const int tall = min(p.group, tiles_m - static_cast<int>(g) * p.group);
+        *m = (static_cast<int>(g) * p.group + static_cast<int>(in_group % tall)) * BM;
+        *n = static_cast<int>(in_group / tall) * BN;
+    };
+    long long issued = 0;
+    int committed = 0;
+
+    if (warp == PRODUCER_WARP) {
+        // failure test (`withhold`): nothing is loaded, so the waits for it run out
+        if (lane == 0 && !test.withhold) {
+            const int a_rows = S::SWAP ? p.out : p.rows, b_rows = S::SWAP ? p.rows : p.out;
+            for (long long t = first; t < tiles && !*abort_flag; t += step) {
+                int m0, n0;
+                place(t, &m0, &n0);
+                bool ok = true;
+                for (int kb = kb_begin; kb < kb_end; ++kb, ++issued) {
+                    const int s = static_cast<int>(issued % STAGES);
+                    const uint32_t n = static_cast<uint32_t>(issued / STAGES);
+                    if (n > 0 && !ptx::mbar_wait_bounded(&empty[s], (n - 1) & 1, abort_flag, fault,
+                                                         kFaultProducer, test.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const int product = kb / kblocks, k0 = (kb - product * kblocks) * BK;
+                    int ax = 0, bx = 0;  // rows of the parts before these
+                    if (p.products > 1) {
+                        ax = (S::SWAP ? part_of_w(product) : part_of_x(product)) * a_rows;
+                        bx = (S::SWAP ? part_of_x(product) : part_of_w(product)) * b_rows;
+                    }
+                    uint8_t *st = smem + s * S::STAGE_BYTES;
+                    ptx::mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
+                    ptx::tma_load_2d(st, &a_map, &full[s], k0, ax + m0);
+                    ptx::tma_load_2d(st + A_BYTES, &b_map, &full[s], k0, bx + n0);
+                }
+                if (!ok)
+                    break;
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        if (lane == 0) {
+            long long kbi = 0;
+            for (long long t = first; t < tiles && !*abort_flag; t += step) {
+                const int a = committed % S::ACCS;
+                const uint32_t use = static_cast<uint32_t>(committed / S::ACCS);
+                if (use > 0 && !ptx::mbar_wait_bounded(&acc_empty[a], (use - 1) & 1, abort_flag,
+                                                       fault, kFaultMma, test.wait_limit_ns))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + a * BN;
+                bool ok = true;
+                for (int kb = kb_begin; kb < kb_end; ++kb, ++kbi) {
+                    const int s = static_cast<int>(kbi % STAGES);
+                    if (!ptx::mbar_wait_bounded(&full[s], (kbi / STAGES) & 1, abort_flag, fault,
+                                                kFaultMma, test.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t at = ptx::smem_u32(smem + s * S::STAGE_BYTES);
+#pragma unroll
+                    for (int j = 0; j < BK / 16; ++j)
+                        ptx::mma_f16(d, ptx::sw128_desc(at + 32 * j),
+                                     ptx::sw128_desc(at + A_BYTES + 32 * j), idesc,
+                                     kb != kb_begin || j != 0);
+                    ptx::mma_commit(&empty[s]);
+                }
+                ptx::mma_commit(&acc_full[a]);  // also when stopping: frees the epilogue
+                ++committed;
+                if (!ok)
+                    break;
+            }
+        }
+    } else {
+        // epilogue: this warp reads the tensor-memory lanes (rows of the tile) 32q..32q+31
+        const int q = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+        uint8_t *slices = out_slices + q * 2 * SLICE_BYTES;
+        T *const y = static_cast<T *>(p.y);
+        const T *const residual = static_cast<const T *>(p.residual);
+        int count = 0, sent = 0;
+        for (long long t = first; t < tiles; t += step, ++count) {
+            int m0, n0;
+            place(t, &m0, &n0);
+            const int a = count % S::ACCS;
+            const bool got = ptx::mbar_wait_bounded(&acc_full[a], (count / S::ACCS) & 1, abort_flag,
+                                                    fault, kFaultEpilogue, test.wait_limit_ns);
+            // tcgen05.ld is warp-collective: continue only if every lane may
+            const bool ok = __all_sync(0xffffffffu, got) && !*abort_flag;
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + lane_base + a * BN;
+            float *const sums = reinterpret_cast<float *>(smem);  // [BN][BM], over the ring
+            if (p.split > 1) {
+                // (every load of the ring has landed and been multiplied)
+                if (ok) {
+#pragma unroll 1
+                    for (int c = 0; c < BN; c += CW) {
+                        float f[CW];
+                        read_columns<CW>(acc + c, f);
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            sums[(c + j) * BM + q * 32 + lane] = f[j];
+                    }
+                }
+                ptx::cluster_arrive_release();
+                ptx::cluster_wait_acquire();
+            }
+            if (!ok)
+                break;
+            // columns c0 .. c0 + CW - 1 of the accumulator, over all parts of K
+            const auto fetch = [&](int c0, float (&f)[CW]) {
+                if (p.split == 1) {
+                    read_columns<CW>(acc + c0, f);
+                    return;
+                }
+#pragma unroll
+                for (int j = 0; j < CW; ++j)
+                    f[j] = 0.0f;
+                for (int k = 0; k < p.split; ++k) {
+                    const uint32_t from =
+                        ptx::map_to_rank(ptx::smem_u32(sums + c0 * BM + q * 32 + lane), k);
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + j * BM * 4));
+                        f[j] += v;
+                    }
+                }
+            };
+            if constexpr (S::SWAP) {
+                // a lane's row of the tile is one column of y, its columns are rows of y
+                const int n = m0 + q * 32 + lane;
+                const float bias = p.bias && n < p.out ? __ldg(p.bias + n) : 0.0f;
+                for (int c0 = part * CW; c0 < BN && n0 + c0 < p.rows; c0 += p.split * CW) {
+                    float f[CW];
+                    fetch(c0, f);
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) {
+                        const long long r = n0 + c0 + j;
+                        if (r < p.rows && n < p.out) {
+                            float v = activate(p.activation, f[j] + bias);
+                            if (residual)
+                                v += Elem<T>::get(residual[r * p.residual_stride + n]);
+                            y[r * p.y_stride + n] = Elem<T>::put(v);
+                        }
+                    }
+                }
+            } else {
+                constexpr int V = Elem<T>::kVector;
+                const long long r = m0 + q * 32 + lane;
+                // slices of 128 bytes of a row
+                constexpr int WIDE = 128 / static_cast<int>(sizeof(T));
+                for (int c0 = part * WIDE; c0 < BN && n0 + c0 < p.out; c0 += p.split * WIDE, ++sent) {
+                    uint8_t *buf = slices + (sent & 1) * SLICE_BYTES;
+#pragma unroll
+                    for (int h = 0; h < WIDE; h += CW) {
+                        float f[CW];
+                        fetch(c0 + h, f);
+                        const int n = n0 + c0 + h;
+                        const T *res = residual ? residual + r * p.residual_stride + n : nullptr;
+                        const bool whole = n + CW <= p.out;
+                        if (p.bias) {
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                f[j] += n + j < p.out ? __ldg(p.bias + n + j) : 0.0f;
+                        }
+                        if (p.activation != LSTM_ACT_NONE) {
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                f[j] = activate(p.activation, f[j]);
+                        }
+                        if (res && r < p.rows) {
+                            if (whole && p.vectors) {
+#pragma unroll
+                                for (int j = 0; j < CW; j += V) {
+                                    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V> *>(res + j);
+#pragma unroll
+                                    for (int i = 0; i < V; ++i)
+                                        f[j + i] += Elem<T>::get(v.v[i]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < CW; ++j)
+                                    if (n + j < p.out)
+                                        f[j] += Elem<T>::get(res[j]);
+                            }
+                        }
+                        if (p.store_boxes) {
+                            if (h == 0) {
+                                // the store that last used this buffer has read it
+                                if (lane == 0)
+                                    ptx::bulk_wait_group_read<1>();
+                                __syncwarp();
+                            }
+                            // 16-byte unit u of the row goes to unit u ^ (row % 8)
+#pragma unroll
+                            for (int j = 0; j < CW; j += V) {
+                                float some[V];
+#pragma unroll
+                                for (int i = 0; i < V; ++i)
+                                    some[i] = f[j + i];
+                                const int unit = (h + j) / V;
+                                *reinterpret_cast<Pack<T, V> *>(
+                                    buf + lane * 128 + ((unit ^ (lane & 7)) << 4)) = pack<T, V>(some);
+                            }
+                        } else if (r < p.rows) {
+#pragma unroll
+                            for (int j = 0; j < CW; ++j)
+                                if (n + j < p.out)
+                                    y[r * p.y_stride + n + j] = Elem<T>::put(f[j]);
+                        }
+                    }
+                    if (p.store_boxes) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (m0 + q * 32 < p.rows)
+                                ptx::tma_store_2d(&y_map, buf, n0 + c0, m0 + q * 32);
+                            ptx::bulk_commit_group();
+                        }
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&acc_empty[a]);
+        }
+        if (lane == 0)
+            ptx::bulk_wait_group<0>();
+        __syncwarp();
+    }
+    if (p.split > 1) {
+        __syncwarp();
+        // the other warps' share of the epilogue's barrier, then: nobody reads this CTA's
+        // sums any more
+        if (warp < 2) {
+            ptx::cluster_arrive_release();
+            ptx::cluster_wait_acquire();
+        }
+        ptx::cluster_arrive_release();
+        ptx::cluster_wait_acquire();
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == PRODUCER_WARP && lane == 0) {
+        // every load has landed before the CTA's shared memory goes away
+        for (long long k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
+            ptx::mbar_wait_drain(&full[k % STAGES], (k / STAGES) & 1, fault, kDefaultWaitLimitNs);
+    }
+    if (warp == MMA_WARP) {
+        if (lane == 0) {
+            // every product has completed before tensor memory is freed
+            for (int k = committed > S::ACCS ? committed - S::ACCS : 0; k < committed; ++k)
+                ptx::mbar_wait_drain(&acc_full[k % S::ACCS], (k / S::ACCS) & 1, fault,
+                                     kDefaultWaitLimitNs);
+        }
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, S::TMEM_COLS);
+    }
+}
+
+// ---- what TMA cannot read in place ---------------------------------------------------
+// Rows of a 16-bit matrix with a pitch of whole 16 bytes, or the three parts of an fp32
+// one, [part][rows][pitch].  The bits between a row's end and its pitch are not read.
+constexpr int kCopyThreads = 256;
+
+__device__ __forceinline__ float leading(float v, unsigned short *bits)
+{
+    const unsigned u = __float_as_uint(v);
+    *bits = static_cast<unsigned short>(u >> 16);
+    return __uint_as_float(u & 0xffff0000u);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kTile * 8) dense_kernel(const DenseArgs p)
+__global__ void __launch_bounds__(kCopyThreads)
+operand_kernel(const T *__restrict__ from, long long stride, long long rows, int cols, int pitch,
+               unsigned short *__restrict__ to)
 {
-    __shared__ float a[kTile][kTile + 1], b[kTile][kTile + 1];
-    const int x = threadIdx.x % kTile, y = threadIdx.x / kTile;
-    const long long n0 = static_cast<long long>(blockIdx.x) * kTile;
-    for (long long r0 = static_cast<long long>(blockIdx.y) * kTile; r0 < p.rows;
-         r0 += static_cast<long long>(gridDim.y) * kTile) {
-        float sum[4] = {};
-        for (int k0 = 0; k0 < p.in; k0 += kTile) {
-            __syncthreads();
-            for (int i = y; i < kTile; i += 8) {
-                const bool in = x < p.in - k0;
-                a[i][x] = in && r0 + i < p.rows
-                              ? Elem<T>::get(static_cast<const T *>(p.x)[(r0 + i) * p.x_stride + k0 + x])
-                              : 0.0f;
-                b[i][x] = in && n0 + i < p.out
-                              ? Elem<T>::get(static_cast<const T *>(p.w)[(n0 + i) * p.w_stride + k0 + x])
-                              : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kTile; ++k)
+    const long long quads = (cols + 3) / 4, cells = rows * quads;
+    const long long part = rows * pitch;
+    for (long long i = blockIdx.x * static_cast<long long>(kCopyThreads) + threadIdx.x; i < cells;
+         i += static_cast<long long>(gridDim.x) * kCopyThreads) {
+        const long long r = i / quads;
+        const int c = static_cast<int>(i - r * quads) * 4;
+        const T *src = from + r * stride + c;
+        unsigned short *dst = to + r * pitch + c;
+        ushort4 o[kParts];
+        unsigned short *bits[kParts] = {&o[0].x, &o[1].x, &o[2].x};
+        T v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sum[j] = fmaf(a[y + 8 * j][k], b[x][k], sum[j]);
-        }
+        for (int j = 0; j < 4; ++j)
+            v[j] = c + j < cols ? src[j] : T();
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long long r = r0 + y + 8 * j, n = n0 + x;
-            if (r < p.rows && n < p.out) {
-                float v = activate(p.activation, sum[j] + (p.bias ? p.bias[n] : 0.0f));
-                if (p.residual)
-                    v += Elem<T>::get(static_cast<const T *>(p.residual)[r * p.residual_stride + n]);
-                static_cast<T *>(p.y)[r * p.y_stride + n] = Elem<T>::put(v);
+            for (int j = 0; j < 4; ++j) {
+                float f = v[j];
+                const float lead = leading(f, bits[0] + j);
+                // (an infinity or a NaN has no rest; a NaN's leading bits may be an infinity's)
+                const bool finite = fabsf(f) <= 3.402823466e38f;
+                if (f != f)
+                    bits[0][j] = 0x7fc0;
+                f = finite ? f - lead : 0.0f;
+                f -= leading(f, bits[1] + j);
+                leading(f, bits[2] + j);
             }
+#pragma unroll
+            for (int k = 0; k < kParts; ++k)
+                *reinterpret_cast<ushort4 *>(dst + k * part) = o[k];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bits[0][j] = *reinterpret_cast<unsigned short *>(&v[j]);
+            *reinterpret_cast<ushort4 *>(dst) = o[0];
         }
     }
+}
+
+template <typename T>
+int copy_operand(const void *from, long long stride, long long rows, int cols, int pitch, void *to,
+                 cudaStream_t stream)
+{
+    const int st = check_launch_injection("lstm_dense");
+    if (st != LSTM_OK)
+        return st;
+    const long long blocks = (rows * ((cols + 3) / 4) + kCopyThreads - 1) / kCopyThreads;
+    operand_kernel<T><<<static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16), kCopyThreads, 0,
+                        stream>>>(static_cast<const T *>(from), stride, rows, cols, pitch,
+                                  static_cast<unsigned short *>(to));
+    return cuda_status(cudaGetLastError(), "lstm_dense launch");
+}
+
+// One operand as TMA reads it: in place, or in the workspace.
+struct Operand {
+    bool copied;
+    int pitch;         // elements, of the copy
+    size_t bytes;      // of the workspace
+
+    Operand(const void *at, long long stride, int dtype, long long rows, int cols)
+        : copied(dtype == LSTM_F32 || !rows_aligned(at, rows > 1 ? stride : 0, 2)),
+          pitch((cols + 7) / 8 * 8),
+          bytes(copied ? static_cast<size_t>(rows) * pitch * 2 * (dtype == LSTM_F32 ? kParts : 1) : 0)
+    {
+        bytes = (bytes + 255) / 256 * 256;
+    }
+};
+
+// ---- launches ---------------------------------------------------------------------------
+template <class S, typename T>
+int launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &y, DenseArgs &p, bool bf16,
+           int split, cudaStream_t stream)
+{
+    static SharedMemory memory;
+    int st = memory.allow(dense_kernel<S, T>, S::SMEM_BYTES);
+    if (st != LSTM_OK)
+        return st;
+    unsigned *fault = fault_word();
+    if (!fault)
+        return fail(LSTM_E_CUDA, "cannot resolve the device fault word");
+    if ((st = check_launch_injection("lstm_dense")))
+        return st;
+    const int down = S::SWAP ? p.out : p.rows, along = S::SWAP ? p.rows : p.out;
+    const int tiles_m = static_cast<int>((down + BM - 1LL) / BM);
+    const long long tiles = tiles_m * ((along + S::BN - 1LL) / S::BN);
+    p.split = split;
+    p.group = S::SWAP ? 1 : 12;
+    cudaLaunchConfig_t cfg = {};
+    // few rows: a cluster for each tile; else no more CTAs than run at once
+    const long long ctas = S::SWAP || split > 1 ? tiles * split : tiles < 152 ? tiles : 152;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attribute;
+    attribute.id = cudaLaunchAttributeClusterDimension;
+    attribute.val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+    cfg.attrs = &attribute;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, dense_kernel<S, T>, a, b, y, p,
+                                          ptx::f16_idesc(BM, S::BN, bf16), tiles, tiles_m, fault,
+                                          kernel_test(kTestDense)),
+                       "lstm_dense launch");
+}
+
+// Tiles' width and the parts of K.
+struct Plan {
+    bool swap;
+    int width;
+    int split;
+};
+
+Plan make_plan(int rows, int in, int out, int products)
+{
+    Plan r = {rows <= kFewRows, 0, 1};
+    const long long kblocks = (in + BK - 1LL) / BK * products;
+    long long tiles;
+    if (r.swap) {
+        r.width = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+        tiles = (out + BM - 1LL) / BM;
+    } else {
+        const long long tall = (rows + BM - 1LL) / BM;
+        r.width = 256;
+        while (r.width > 64 && tall * ((out + r.width - 1LL) / r.width) < 152)
+            r.width /= 2;
+        tiles = tall * ((out + r.width - 1LL) / r.width);
+    }
+    while (r.split < 8 && tiles * r.split < 152 && kblocks >= 8 * r.split)
+        r.split *= 2;
+    return r;
+}
+
+template <typename T>
+int product(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &y, DenseArgs &p,
+            const Plan &plan, bool bf16, cudaStream_t stream)
+{
+    if (plan.swap) {
+        switch (plan.width) {
+        case 16:
+            return launch<Shape<16, true>, T>(w, x, y, p, bf16, plan.split, stream);
+        case 32:
+            return launch<Shape<32, true>, T>(w, x, y, p, bf16, plan.split, stream);
+        default:
+            return launch<Shape<64, true>, T>(w, x, y, p, bf16, plan.split, stream);
+        }
+    }
+    switch (plan.width) {
+    case 64:
+        return launch<Shape<64, false>, T>(x, w, y, p, bf16, plan.split, stream);
+    case 128:
+        return launch<Shape<128, false>, T>(x, w, y, p, bf16, plan.split, stream);
+    default:
+        return launch<Shape<256, false>, T>(x, w, y, p, bf16, plan.split, stream);
+    }
+}
+
+CUtensorMapDataType map_type(int dtype)
+{
+    return dtype == LSTM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+           : dtype == LSTM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
 }  // namespace
@@ -80,10 +605,12 @@ __global__ void __launch_bounds__(kTile * 8) dense_kernel(const DenseArgs p)
 
 using namespace lstm;
 
-extern "C" size_t lstm_dense_workspace(const void *, long long, const void *, long long, int, int,
-                                       int, int)
+extern "C" size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w,
+                                       long long w_stride, int dtype, int rows, int in, int out)
 {
-    return 0;
+    if (rows <= 0 || in <= 0 || out <= 0)
+        return 0;
+    return Operand(x, x_stride, dtype, rows, in).bytes + Operand(w, w_stride, dtype, out, in).bytes;
 }
 
 extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long long w_stride,
@@ -98,9 +625,10 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
     if (rows < 0 || in <= 0 || out <= 0 || activation < LSTM_ACT_NONE || activation > LSTM_ACT_SILU)
         return fail(LSTM_E_INVALID, "%s: %d rows, %d to %d columns, activation %d", what, rows, in,
                     out, activation);
-    if (rows > kMostTokens || in > kMostTokens || out > kMostTokens)
+    // (the kernels count the rows of all parts, and K blocks of all products, in 32 bits)
+    if (rows > LSTM_DENSE_MAX || in > LSTM_DENSE_MAX || out > LSTM_DENSE_MAX)
         return fail(LSTM_E_OVERFLOW, "%s: %d rows, %d to %d columns (at most %d)", what, rows, in,
-                    out, kMostTokens);
+                    out, LSTM_DENSE_MAX);
     const int size = element_size(dtype);
     if ((st = check_matrix(what, "w", w, w_stride, out, in, size)) ||
         (bias && (st = check_matrix(what, "bias", bias, out, 1, out, 4))))
@@ -115,25 +643,50 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
         return st;
     if (rows == 0)
         return LSTM_OK;
-    const size_t needed = lstm_dense_workspace(x, x_stride, w, w_stride, dtype, rows, in, out);
-    if (needed > 0 && !workspace)
+    const Operand ox(x, x_stride, dtype, rows, in), ow(w, w_stride, dtype, out, in);
+    if (ox.bytes + ow.bytes > 0 && !workspace)
         return fail(LSTM_E_INVALID, "%s: workspace is null", what);
-    if (workspace_bytes < needed)
+    if (workspace_bytes < ox.bytes + ow.bytes)
         return fail(LSTM_E_LENGTH, "%s: workspace has %zu bytes, needs %zu", what, workspace_bytes,
-                    needed);
+                    ox.bytes + ow.bytes);
     if ((st = check_aligned(workspace, "workspace")))
         return st;
     DeviceGuard guard(device);
     if (!guard.ok)
         return fail(LSTM_E_CUDA, "cannot make device %d current", device);
-    if ((st = check_launch_injection(what)))
+    cudaStream_t on = static_cast<cudaStream_t>(stream);
+
+    const Plan plan = make_plan(rows, in, out, dtype == LSTM_F32 ? kProducts : 1);
+    const CUtensorMapDataType type =
+        dtype == LSTM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int parts = dtype == LSTM_F32 ? kParts : 1;
+    const auto map = [&](CUtensorMap *m, const Operand &o, const void *at, long long stride,
+                         long long n, void *copy, int box_rows) {
+        int status = LSTM_OK;
+        long long pitch = (n > 1 ? stride : (in + 7) / 8 * 8) * 2;
+        if (o.copied) {
+            if (dtype == LSTM_F32)
+                status = copy_operand<float>(at, stride, n, in, o.pitch, copy, on);
+            else
+                status = copy_operand<unsigned short>(at, stride, n, in, o.pitch, copy, on);
+            at = copy;
+            pitch = o.pitch * 2LL;
+        }
+        return status != LSTM_OK ? status
+                                 : encode_box_map(m, type, at, n * parts, in, pitch, box_rows);
+    };
+    CUtensorMap x_map, w_map, y_map = {};
+    if ((st = map(&x_map, ox, x, x_stride, rows, workspace, plan.swap ? plan.width : BM)) ||
+        (st = map(&w_map, ow, w, w_stride, out, static_cast<char *>(workspace) + ox.bytes,
+                  plan.swap ? BM : plan.width)))
         return st;
-    const DenseArgs p = {x, w, x_stride, w_stride, bias, activation, residual, residual_stride,
-                         rows, in, out, y, y_stride};
-    const long long tall = (rows + kTile - 1LL) / kTile;
-    const dim3 grid(static_cast<unsigned>((out + kTile - 1LL) / kTile),
-                    static_cast<unsigned>(tall < 65535 ? tall : 65535));
-    LSTM_WITH_TYPE(dtype, T, (dense_kernel<T><<<grid, kTile * 8, 0,
-                                                static_cast<cudaStream_t>(stream)>>>(p)));
-    return cuda_status(cudaGetLastError(), "lstm_dense launch");
+    DenseArgs p = {bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
+                   dtype == LSTM_F32 ? kProducts : 1, 1, false, false, 1};
+    p.vectors = !residual || rows_aligned(residual, rows > 1 ? residual_stride : 0, size);
+    p.store_boxes = !plan.swap && rows_aligned(y, y_stride, size);
+    if (p.store_boxes &&
+        (st = encode_box_map(&y_map, map_type(dtype), y, rows, out, y_stride * size, 32)))
+        return st;
+    LSTM_WITH_TYPE(dtype, T,
+                   return product<T>(x_map, w_map, y_map, p, plan, dtype != LSTM_F16, on));
 }

@@ -477,6 +477,26 @@ int encode_store_map(CUtensorMap *map, float *base, long rows, int cols)
     return encode_map(map, base, rows, cols, OUT_COLS, 32, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+int encode_box_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, long long rows,
+                   long long cols, long long pitch_bytes, int box_rows)
+{
+    auto encode = encode_fn();
+    if (!encode)
+        return fail(LSTM_E_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+    const cuuint32_t box[2] = {type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 32u : 64u,
+                               static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = encode(map, type, 2, const_cast<void *>(base), dims, strides, box, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(LSTM_E_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld x %lld, pitch %lld",
+                    (int)r, rows, cols, pitch_bytes);
+    return LSTM_OK;
+}
+
 namespace {
 // Every instantiation, for the per-device attributes.
 const void *const kKernels[] = {

@@ -90,6 +90,8 @@ enum {
     LSTM_ACT_SILU = 4       /* v / (1 + e^-v) */
 };
 
+#define LSTM_DENSE_MAX (1 << 29)
+
 /* y[r][n] = act(sum_k x[r][k] * w[n][k] + bias[n]) + residual[r][n]
  *   x        : device [rows][in]
  *   w        : device [out][in] of x's type, row stride w_stride
@@ -97,6 +99,7 @@ enum {
  *   residual : device [rows][out] of x's type, or NULL; may be y
  *   y        : device [rows][out]
  *   workspace: as lstm_linear_attention's; lstm_dense_workspace(...) bytes
+ * rows, in and out are at most LSTM_DENSE_MAX.
  * Products and sums are fp32, with LSTM_F32 too (each product keeps 24 bits of
  * its factors).  16-bit x and w whose rows all start on 16-byte boundaries are
  * read in place; others, and fp32, go through the workspace first.
@@ -110,6 +113,11 @@ int lstm_dense(const void *x, long long x_stride, const void *w, long long w_str
                const float *bias, int activation, const void *residual, long long residual_stride,
                int dtype, int rows, int in, int out, void *y, long long y_stride, void *workspace,
                size_t workspace_bytes, void *stream);
+
+/* Failure-injection hooks, as lstm_test_recurrence_timeout: with withhold != 0
+ * lstm_linear_attention and lstm_dense load nothing, so that their waits run out. */
+int lstm_test_attention_timeout(int withhold, unsigned int wait_limit_us, int device);
+int lstm_test_dense_timeout(int withhold, unsigned int wait_limit_us, int device);
 
 #ifdef __cplusplus
 }

@@ -175,3 +175,21 @@ def test_launch_failures_are_errors():
     with pytest.raises(binding.LSTMError):
         binding.lstm_dense(x, w)
     binding.lstm_dense(x, w)
+
+
+@pytest.mark.parametrize("rows", [4, 70, 400])
+def test_a_wait_that_runs_out_sets_the_fault_word_and_the_next_call_works(rows):
+    lib = binding.load()
+    x, w = normal(gen(1), rows, 1024, dtype=torch.bfloat16), normal(gen(2), 256, 1024, dtype=torch.bfloat16)
+    ref = binding.lstm_dense(x, w)
+    assert binding.lstm_fault_status() == 0
+    try:
+        assert lib.lstm_test_dense_timeout(1, 1000, 0) == 0
+        binding.lstm_dense(x, w)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.lstm_test_dense_timeout(0, 0, 0) == 0
+    assert binding.lstm_fault_status() != 0
+    assert torch.equal(binding.lstm_dense(x, w), ref)
+    torch.cuda.synchronize()
+    assert binding.lstm_fault_status() == 0

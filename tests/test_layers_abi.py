@@ -85,7 +85,8 @@ def test_dense_refuses(lib, bad):
 
 
 def test_dense_overflow(lib):
-    assert _dense(lib, rows=0x7fffffff) == OVERFLOW
+    for size in ("rows", "n_in", "n_out"):
+        assert _dense(lib, **{size: (1 << 29) + 1}) == OVERFLOW
 
 
 # ---- the binding ---------------------------------------------------------------------------------
