@@ -1,79 +1,11 @@
-// Linear attention with a decay for each head: per sequence and head
-//     S_t = e^(g_t) S_(t-1) + k_t v_t^T,   y_t = scale S_t^T q_t.
+// Linear attention with a decay for each head, per sequence and head
+//     S_t = e^(g_t) S_(t-1) + k_t v_t^T,   y_t = scale S_t^T q_t:
+// the entry points.  attention_prompts.cuh has the prompts' kernels (one file for each
+// element type instantiates them), attention_step.cu the single tokens'.
 #include "attention.cuh"
 
 namespace lstm {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kCols = 32;
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs p)
-{
-    constexpr int kGroups = kThreads / kCols, kEach = LSTM_ATTENTION_MAX_KEYS / kGroups;
-    __shared__ float q[LSTM_ATTENTION_MAX_KEYS], k[LSTM_ATTENTION_MAX_KEYS], part[kThreads];
-    const int s = blockIdx.x, head = blockIdx.y;
-    const int x = threadIdx.x % kCols, group = threadIdx.x / kCols;
-    const int col = blockIdx.z * kCols + x;
-    const bool inside = col < p.values;
-    const int slot = sequence_slot(p.slots, s);
-    float *state = slot >= 0 ? p.state_of(slot, head) + col : nullptr;
-    const bool resumes = state && sequence_resumes(p.slots, s);
-    float h[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int row = group + j * kGroups;
-        h[j] = resumes && inside && row < p.keys ? state[static_cast<long long>(row) * p.values] : 0.0f;
-    }
-    const int end = sequence_end(p.seq, s);
-    for (int t = sequence_begin(p.seq, s); t < end; ++t) {
-        __syncthreads();
-        for (int n = threadIdx.x; n < p.keys; n += kThreads) {
-            q[n] = Elem<T>::get(p.q.row<T>(t, head)[n]);
-            k[n] = Elem<T>::get(p.k.row<T>(t, head)[n]);
-        }
-        const float v = inside ? Elem<T>::get(p.v.row<T>(t, head)[col]) : 0.0f;
-        const float left = expf(p.decay[t * p.decay_stride + head]);
-        __syncthreads();
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int row = group + j * kGroups;
-            if (row < p.keys) {
-                h[j] = fmaf(k[row], v, left * h[j]);
-                sum = fmaf(q[row], h[j], sum);
-            }
-        }
-        part[threadIdx.x] = sum;
-        __syncthreads();
-        if (group == 0 && inside) {
-            float y = 0.0f;
-            for (int g = 0; g < kGroups; ++g)
-                y += part[g * kCols + x];
-            p.out<T>(t, head)[col] = Elem<T>::put(p.scale * y);
-        }
-    }
-    if (state && inside) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int row = group + j * kGroups;
-            if (row < p.keys)
-                state[static_cast<long long>(row) * p.values] = h[j];
-        }
-    }
-}
-
-int launch_attention(const AttentionArgs &p, int dtype, cudaStream_t stream)
-{
-    const int st = check_launch_injection("lstm_linear_attention");
-    if (st != LSTM_OK)
-        return st;
-    const dim3 grid(static_cast<unsigned>(p.seq.count), static_cast<unsigned>(p.heads),
-                    static_cast<unsigned>((p.values + kCols - 1) / kCols));
-    LSTM_WITH_TYPE(dtype, T, (attention_kernel<T><<<grid, kThreads, 0, stream>>>(p)));
-    return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
-}
 
 int check_heads(const char *what, const char *name, HeadRows &m, int own, int heads, int width,
                 int rows, int size)
@@ -136,7 +68,11 @@ int attention(const char *what, AttentionArgs &p, int q_heads, int k_heads, int 
     if (!guard.ok)
         return fail(LSTM_E_CUDA, "cannot make device %d current", device);
     cudaStream_t on = static_cast<cudaStream_t>(stream);
-    return step ? launch_attention_step(p, dtype, on) : launch_attention(p, dtype, on);
+    if (step)
+        return launch_attention_step(p, dtype, on);
+    return dtype == LSTM_F32    ? launch_attention_f32(p, on)
+           : dtype == LSTM_BF16 ? launch_attention_bf16(p, on)
+                                : launch_attention_f16(p, on);
 }
 
 }  // namespace

@@ -48,6 +48,9 @@ struct AttentionArgs {
     }
 };
 
+int launch_attention_f32(const AttentionArgs &p, cudaStream_t stream);
+int launch_attention_bf16(const AttentionArgs &p, cudaStream_t stream);
+int launch_attention_f16(const AttentionArgs &p, cudaStream_t stream);
 int launch_attention_step(const AttentionArgs &p, int dtype, cudaStream_t stream);
 
 }  // namespace lstm

@@ -1,0 +1,11 @@
+// Linear attention over prompts in fp16.
+#include "attention_prompts.cuh"
+
+namespace lstm {
+
+int launch_attention_f16(const AttentionArgs &p, cudaStream_t stream)
+{
+    return prompts::launch_keys<__half>(p, stream);
+}
+
+}  // namespace lstm

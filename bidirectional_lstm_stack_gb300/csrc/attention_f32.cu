@@ -1,0 +1,11 @@
+// Linear attention over prompts in fp32.
+#include "attention_prompts.cuh"
+
+namespace lstm {
+
+int launch_attention_f32(const AttentionArgs &p, cudaStream_t stream)
+{
+    return prompts::launch_keys<float>(p, stream);
+}
+
+}  // namespace lstm
