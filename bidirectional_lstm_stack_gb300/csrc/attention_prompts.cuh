@@ -14,7 +14,7 @@
 //    swizzle, so the same tile serves as K-major and as MN-major operand); a warp beside
 //    them sums the log decays, in fp64, since c_i - c_j of far sums would lose what
 //    separates near tokens;
-//  * 4 output warps turn scores into P, and inter and intra into y;
+//  * 8 output warps turn scores into P, and inter and intra into y;
 //  * 4 or 8 state warps hold S in registers (fp32, a lane per value), write w v, add the
 //    update and hand S on as bf16;
 //  * two threads issue the products, those of the outputs and those of the states, so that
@@ -176,51 +176,63 @@ __device__ __forceinline__ void load_parts(const uint8_t *at, int apart, float (
 }
 
 // ---- loading ------------------------------------------------------------------------------
-// Rows t0 .. t0 + 63 of a head into a tile of `units` 16-byte units a row; rows from
-// `len` and numbers from `width` on are zeros.
-template <typename T>
+// Rows t0 .. t0 + 63 of a head into a tile of UNITS 16-byte units a row; rows from
+// `len` and numbers from `width` on are zeros.  A thread keeps its unit and goes down the
+// rows, so that swizzle and width are worked out once.
+template <typename T, int UNITS>
 __device__ __forceinline__ void load_tile(uint8_t *tile, int apart, const HeadRows &m, bool aligned,
-                                          long long t0, int head, int len, int width, int units,
-                                          int first, int tid)
+                                          long long t0, int head, int len, int width, int first,
+                                          int tid)
 {
-    const T *base = m.row<T>(t0, head) + first;
-    const int total = C * units;
-    if constexpr (sizeof(T) == 2 && Parts<T>::kIn == 1) {
+    constexpr int kDown = kLoaders / UNITS;  // rows of a turn, a multiple of 8
+    static_assert(kDown % 8 == 0, "the swizzle of a thread's rows");
+    const int u = tid % UNITS, r0 = tid / UNITS;
+    const T *src = m.row<T>(t0 + r0, head) + first + u * 8;
+    const long long down = kDown * m.stride;
+    uint8_t *dst = tile + (u >> 3) * kSlab + r0 * kRowBytes + (((u & 7) ^ (r0 & 7)) << 4);
+    const int there = min(max(width - u * 8, 0), 8);
+    if constexpr (Parts<T>::kIn == 1) {
         if (aligned) {
-#pragma unroll 4
-            for (int i = tid; i < total; i += kLoaders) {
-                const int r = i / units, u = i - r * units;
-                const int there = r < len ? min(max(width - u * 8, 0), 8) : 0;
-                const T *src = there ? base + r * m.stride + u * 8 : base;
-                const uint32_t dst = ptx::smem_u32(tile + (u >> 3) * kSlab + r * kRowBytes +
-                                                   (((u & 7) ^ (r & 7)) << 4));
-                ptx::cp_async_16(dst, src, there * 2);
+            const uint32_t to = ptx::smem_u32(dst);
+            const T *const some = m.row<T>(t0, head);  // an address where there is nothing to read
+#pragma unroll
+            for (int k = 0; k < C / kDown; ++k) {
+                const bool in = r0 + k * kDown < len && there > 0;
+                ptx::cp_async_16(to + k * kDown * kRowBytes, in ? src : some, in ? there * 2 : 0);
+                src += down;
             }
             return;
         }
     }
-#pragma unroll 2
-    for (int i = tid; i < total; i += kLoaders) {
-        const int r = i / units, u = i - r * units;
-        const int there = r < len ? min(max(width - u * 8, 0), 8) : 0;
-        const T *src = base + r * m.stride + u * 8;
-        float f[8];
-        if (aligned && there == 8) {
-            constexpr int V = Elem<T>::kVector;
+    constexpr int kTogether = 4;  // rows in flight
+#pragma unroll 1
+    for (int k0 = 0; k0 < C / kDown; k0 += kTogether) {
+        float f[kTogether][8];
 #pragma unroll
-            for (int j = 0; j < 8; j += V) {
-                const Pack<T, V> v = load_pack<T, V>(src + j);
+        for (int k = 0; k < kTogether; ++k) {
+            const bool in = k0 + k < C / kDown && r0 + (k0 + k) * kDown < len;
+            if (aligned && there == 8) {
+                constexpr int V = Elem<T>::kVector;
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    f[j + e] = Elem<T>::get(v.v[e]);
+                for (int j = 0; j < 8; j += V) {
+                    Pack<T, V> v = {};
+                    if (in)
+                        v = load_pack<T, V>(src + k * down + j);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        f[k][j + e] = Elem<T>::get(v.v[e]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[k][j] = in && j < there ? Elem<T>::get(src[k * down + j]) : 0.0f;
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                f[j] = j < there ? Elem<T>::get(src[j]) : 0.0f;
         }
-        store_parts<Parts<T>::kIn>(
-            tile + (u >> 3) * kSlab + r * kRowBytes + (((u & 7) ^ (r & 7)) << 4), apart, f);
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+            if (k0 + k < C / kDown)
+                store_parts<Parts<T>::kIn>(dst + (k0 + k) * kDown * kRowBytes, apart, f[k]);
+        src += kTogether * down;
     }
 }
 
@@ -255,13 +267,14 @@ __device__ __forceinline__ void sum_decays(Decays &d, float g0, float g1, int la
 
 // Value v's sum over the keys up to query t, from the tiles.
 template <typename T>
-__device__ __noinline__ float seen_by(int t, int v, const uint8_t *p_tile, const uint8_t *v_tile,
+__device__ __forceinline__ float seen_by(int t, int v, const uint8_t *p_tile, const uint8_t *v_tile,
                                       int tile_v)
 {
     const auto number = [](const uint8_t *at) {
         return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(at));
     };
     float sum = 0.0f;
+#pragma unroll 1
     for (int j = 0; j <= t; ++j) {
         float pv = 0.0f, vv = 0.0f;
 #pragma unroll
@@ -280,11 +293,22 @@ __device__ __noinline__ float seen_by(int t, int v, const uint8_t *p_tile, const
 // Thread layout: output warps, state warps, two issuing warps, the decays' warp, loaders.
 template <int KP>
 struct Warps {
+    static constexpr int kOut = 8;
     static constexpr int kState = 4 * (KP / 64);
-    static constexpr int kIssue = 4 + kState;
+    static constexpr int kIssue = kOut + kState;
     static constexpr int kDecay = kIssue + 2;
     static constexpr int kLoad = kDecay + 1;
-    static constexpr int kThreads = (kLoad + 4) * 32;
+    static constexpr int kThreads = (kLoad + 4 + 1) * 32;  // (whole warpgroups)
+    // Registers: as the block is launched (65536 over its threads), and, with 128 keys, as
+    // its warpgroups then share those of the launch, 768 x 80 = 256 x (72 + 104 + 64)
+    static constexpr int kRegisters = KP > 64 ? 80 : 96;
+    static constexpr bool kShare = KP > 64;
+    static constexpr int kOutRegisters = 72, kStateRegisters = 104, kRestRegisters = 64;
+    static_assert(kThreads % 128 == 0 && kIssue % 4 == 0, "warpgroups");
+    static_assert(!kShare || kThreads * kRegisters == kOut * 32 * kOutRegisters +
+                                                          kState * 32 * kStateRegisters +
+                                                          (kThreads - kIssue * 32) * kRestRegisters,
+                  "registers");
 };
 // Tensor memory: two buffers of scores (intra goes where its scores were), inter, the
 // update, and S^T in up to three parts.
@@ -296,12 +320,13 @@ struct Columns {
     static_assert(kUsed <= 512, "tensor memory");
 };
 
-// D (+)= the products of parts that matter, over `steps` blocks of 16 along the sum.
-template <int NA, int NB, typename A, typename B, typename M>
+// D = the products of parts that matter, over `steps` of the MOST blocks of 16 along the
+// sum; a, b: an operand's descriptor for a part and a block, known but for a constant.
+template <int MOST, int NA, int NB, typename A, typename B, typename M>
 __device__ __forceinline__ void multiply(int steps, const A &a, const B &b, const M &mma)
 {
     constexpr int most = NA > NB ? NA : NB;
-    uint32_t accumulate = 0;
+    bool started = false;
     // the small products first
 #pragma unroll
     for (int order = most - 1; order >= 0; --order)
@@ -310,10 +335,12 @@ __device__ __forceinline__ void multiply(int steps, const A &a, const B &b, cons
             const int j = order - i;
             if (j < 0 || j >= NB)
                 continue;
-            for (int k = 0; k < steps; ++k) {
-                mma(a(i, k), b(j, k), accumulate);
-                accumulate = 1;
-            }
+#pragma unroll
+            for (int k = 0; k < MOST; ++k)
+                if (k < steps) {
+                    mma(a(i, k), b(j, k), started || k > 0);
+                }
+            started = true;
         }
 }
 
@@ -349,17 +376,17 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
             ptx::mbar_init(&bar.full[s], kLoaders + 32);
-            ptx::mbar_init(&bar.empty[s], 2 + 4);
+            ptx::mbar_init(&bar.empty[s], 2 + W::kOut);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&bar.scores_full[b], 1);
-            ptx::mbar_init(&bar.scores_free[b], 128);
+            ptx::mbar_init(&bar.scores_free[b], W::kOut * 32);
             ptx::mbar_init(&bar.done[b], 1);
         }
-        ptx::mbar_init(&bar.p_full, 128);
-        ptx::mbar_init(&bar.p_free, 4);
+        ptx::mbar_init(&bar.p_full, W::kOut * 32);
+        ptx::mbar_init(&bar.p_free, W::kOut);
         ptx::mbar_init(&bar.inter_full, 1);
-        ptx::mbar_init(&bar.inter_free, 128);
+        ptx::mbar_init(&bar.inter_free, W::kOut * 32);
         ptx::mbar_init(&bar.intra_full, 1);
         ptx::mbar_init(&bar.state_full, W::kState * 32);
         ptx::mbar_init(&bar.weighted_full, W::kState * 32);
@@ -381,48 +408,59 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
         return ptx::mbar_wait_bounded(b, parity, abort, fault, code, test.wait_limit_ns);
     };
 
-    if (warp < 4) {
+    if constexpr (W::kShare) {
+        if (warp < W::kOut)
+            ptx::fewer_registers<W::kOutRegisters>();
+        else if (warp < W::kIssue)
+            ptx::more_registers<W::kStateRegisters>();
+        else
+            ptx::fewer_registers<W::kRestRegisters>();
+    }
+    if (warp < W::kOut) {
         // ---- outputs: scores to P, inter and intra to y ----
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const int v = warp * 32 + lane, i = v;  // lanes are values, and queries of the scores
-        T *const y = p.out<T>(run.begin, head) + v0 + v;
+        // lanes are values, and queries of the scores; a warp takes half of the columns
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const int v = quarter * 32 + lane, i = v;
+        T *y = p.out<T>(run.begin + half * 32, head) + v0 + v;
         for (int c = 0; c < chunks; ++c) {
             const int s = stage_of(c), b = c & 1;
-            const uint32_t scores = tmem + lanes + Col::kScores + 64 * b;
+            const uint32_t columns = tmem + lanes + Col::kScores + 64 * b + 32 * half;
             const Decays &d = decays[s];
-            const int len = min(run.end - run.begin - c * C, C);
             // (p_free: the warps that read P of the chunk before are done with it)
             bool ok = (c == 0 || wait(&bar.p_free, (c - 1) & 1, kFaultConverter)) &&
                       wait(&bar.full[s], turn_of(c), kFaultConverter) &&
                       wait(&bar.scores_full[b], (c >> 1) & 1, kFaultConverter);
             ok = __all_sync(0xffffffffu, ok) && !*abort;
-            if (ok && warp < 2) {
+            if (ok && quarter < 2) {
                 ptx::tc_fence_after();
-                const float2 mine = d.sum[i];
                 uint8_t *const row = p_tile + i * kRowBytes;
+                const int swizzle = (i & 7) << 4;
+                if (half > quarter) {  // all keys of these columns come after all queries
+                    const float none[8] = {};
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half > warp) {  // all keys of these columns come after all queries
-                        const float none[8] = {};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            store_parts<P::kMid>(row + (((half * 4 + u) ^ (i & 7)) << 4), kSlab, none);
-                        continue;
-                    }
-                    uint32_t r[32];
-                    ptx::tmem_ld_32x32b_x32(scores + 32 * half, r);
-                    ptx::tmem_ld_wait();
+                    for (int u = 0; u < 4; ++u)
+                        store_parts<P::kMid>(row + (((half * 4 + u) << 4) ^ swizzle), kSlab, none);
+                } else {
+                    const float2 mine = d.sum[i];
+                    uint32_t r[16];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
+                        if (u % 2 == 0) {
+                            ptx::tmem_ld_32x32b_x16(columns + u * 8, r);
+                            ptx::tmem_ld_wait();
+                        }
                         float f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 8; e += 2) {
                             const int j = half * 32 + u * 8 + e;
-                            const float2 other = d.sum[j];
-                            const float gap = (mine.x - other.x) + (mine.y - other.y);
-                            f[e] = j <= i ? __uint_as_float(r[u * 8 + e]) * ex2(gap) : 0.0f;
+                            const float4 other = *reinterpret_cast<const float4 *>(&d.sum[j]);
+                            const float one = (mine.x - other.x) + (mine.y - other.y);
+                            const float two = (mine.x - other.z) + (mine.y - other.w);
+                            f[e] = j <= i ? __uint_as_float(r[u % 2 * 8 + e]) * ex2(one) : 0.0f;
+                            f[e + 1] = j + 1 <= i ? __uint_as_float(r[u % 2 * 8 + e + 1]) * ex2(two) : 0.0f;
                         }
-                        store_parts<P::kMid>(row + (((half * 4 + u) ^ (i & 7)) << 4), kSlab, f);
+                        store_parts<P::kMid>(row + (((half * 4 + u) << 4) ^ swizzle), kSlab, f);
                     }
                 }
                 ptx::fence_proxy_async_smem();
@@ -434,56 +472,68 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
             if (!__all_sync(0xffffffffu, ok) || *abort)
                 break;
             ptx::tc_fence_after();
-            T *const at = y + static_cast<long long>(c) * C * p.y_stride;
+            const int len = run.end - run.begin - c * C - half * 32;
+            const uint32_t inter = tmem + lanes + Col::kInter + 32 * half;
+            uint32_t r[16];
+            bool finite = true;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t r[32];
-                float out[32];
-                ptx::tmem_ld_32x32b_x32(scores + 32 * half, r);
+            for (int e0 = 0; e0 < 32; e0 += 16) {
+                ptx::tmem_ld_32x32b_x16(columns + e0, r);
                 ptx::tmem_ld_wait();
-                bool finite = true;
 #pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    finite = finite && fabsf(__uint_as_float(r[e])) <= 3.402823466e38f;
+            }
+            if (!__all_sync(0xffffffffu, finite || v >= values)) {
+                // a value that is not finite met the zeros of P at the tokens before it: what
+                // such a token may see is summed again
+                const uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
+#pragma unroll 1
                 for (int e = 0; e < 32; ++e) {
-                    out[e] = __uint_as_float(r[e]);
-                    finite = finite && fabsf(out[e]) <= 3.402823466e38f;
-                }
-                if (!finite && v < values) {
-                    // a value that is not finite met the zeros of P at the tokens before it: what
-                    // such a token may see is summed again
-                    const uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(fabsf(out[e]) <= 3.402823466e38f))
-                            out[e] = seen_by<T>(half * 32 + e, v, p_tile, tile, l.tile_v);
-                }
-                ptx::tmem_ld_32x32b_x32(tmem + lanes + Col::kInter + 32 * half, r);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    out[e] = p.scale * fmaf(__uint_as_float(r[e]), d.since[half * 32 + e], out[e]);
-                if (half == 1) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(&bar.scores_free[b]);
-                    ptx::mbar_arrive(&bar.inter_free);
+                    float sum = __uint_as_float(ptx::tmem_ld_32x32b_x1(columns + e));
+                    const float past = __uint_as_float(ptx::tmem_ld_32x32b_x1(inter + e));
+                    ptx::tmem_ld_wait();
+                    if (v < values && e < len) {
+                        if (!(fabsf(sum) <= 3.402823466e38f))
+                            sum = seen_by<T>(half * 32 + e, v, p_tile, tile, l.tile_v);
+                        y[e * p.y_stride] =
+                            Elem<T>::put(p.scale * fmaf(past, d.since[half * 32 + e], sum));
+                    }
                     __syncwarp();
-                    if (lane == 0) {
-                        ptx::mbar_arrive(&bar.p_free);
-                        ptx::mbar_arrive(&bar.empty[s]);
+                }
+            } else {
+                T *at = y;
+#pragma unroll
+                for (int e0 = 0; e0 < 32; e0 += 16) {
+                    uint32_t past[16];
+                    ptx::tmem_ld_32x32b_x16(columns + e0, r);
+                    ptx::tmem_ld_32x32b_x16(inter + e0, past);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        if (v < values && e0 + e < len)
+                            *at = Elem<T>::put(p.scale * fmaf(__uint_as_float(past[e]),
+                                                              d.since[half * 32 + e0 + e],
+                                                              __uint_as_float(r[e])));
+                        at += p.y_stride;
                     }
                 }
-                if (v < values) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (half * 32 + e < len)
-                            at[(half * 32 + e) * p.y_stride] = Elem<T>::put(out[e]);
-                }
             }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&bar.scores_free[b]);
+            ptx::mbar_arrive(&bar.inter_free);
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(&bar.p_free);
+                ptx::mbar_arrive(&bar.empty[s]);
+            }
+            y += C * p.y_stride;
         }
     } else if (warp < W::kIssue) {
         // ---- states: w v, S, and S as an operand ----
-        const int quarter = warp & 3, k0 = ((warp - 4) >> 2) * 64;
+        const int quarter = warp & 3, k0 = ((warp - W::kOut) >> 2) * 64;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const int v = quarter * 32 + lane, tid = threadIdx.x - 128;
+        const int v = quarter * 32 + lane, tid = threadIdx.x - W::kOut * 32;
         const bool inside = v < values;
         float h[64];
 #pragma unroll
@@ -493,10 +543,10 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
                        : 0.0f;
         const auto hand_on = [&] {
 #pragma unroll
-            for (int n0 = 0; n0 < 32; n0 += 16) {
-                uint32_t r[P::kMid][16];
+            for (int n0 = 0; n0 < 32; n0 += 8) {
+                uint32_t r[P::kMid][8];
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
+                for (int n = 0; n < 8; ++n) {
                     uint32_t parts[P::kMid];
                     split_pair_parts<P::kMid>(h[2 * (n0 + n)], h[2 * (n0 + n) + 1], parts);
 #pragma unroll
@@ -505,7 +555,7 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
                 }
 #pragma unroll
                 for (int part = 0; part < P::kMid; ++part)
-                    ptx::tmem_st_32x32b_x16(
+                    ptx::tmem_st_32x32b_x8(
                         tmem + lanes + Col::kState + part * (KP / 2) + k0 / 2 + n0, r[part]);
             }
             ptx::tmem_st_wait();
@@ -568,24 +618,26 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
             constexpr uint32_t idesc = ptx::f16_idesc(128, C, true);
             constexpr uint32_t idesc_v = ptx::f16_idesc(128, C, true, true, false);
             const int steps = (p.keys + 15) / 16;
-            const uint32_t p_at = ptx::smem_u32(p_tile);
+            // descriptors count 16 bytes: a part or a block further is a number added
+            const uint64_t p_desc = ptx::sw128_desc(ptx::smem_u32(p_tile));
+            const int part_k = l.tile_k >> 4, part_v = l.tile_v >> 4;
+            const auto along_keys = [&](uint64_t desc, int part, int k) {
+                return desc + part * part_k + (k >> 2) * (kSlab >> 4) + (k & 3) * 2;
+            };
             const auto make_scores = [&](int c) {
                 const int s = stage_of(c), b = c & 1;
                 if (!wait(&bar.full[s], turn_of(c), kFaultMma) ||
                     (c >= 2 && !wait(&bar.scores_free[b], ((c >> 1) - 1) & 1, kFaultMma)))
                     return false;
                 ptx::tc_fence_after();
-                const uint32_t q_at = ptx::smem_u32(smem + s * l.stage);
-                const uint32_t k_at = q_at + P::kIn * l.tile_k;
+                const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(smem + s * l.stage));
+                const uint64_t k_desc = q_desc + P::kIn * part_k;
                 const uint32_t to = tmem + Col::kScores + 64 * b;
-                const auto desc = [&](uint32_t at, int part, int k) {
-                    return ptx::sw128_desc(at + part * l.tile_k + (k >> 2) * kSlab + (k & 3) * 32);
-                };
-                multiply<P::kIn, P::kIn>(
-                    steps, [&](int i, int k) { return desc(q_at, i, k); },
-                    [&](int j, int k) { return desc(k_at, j, k); },
-                    [&](uint64_t a, uint64_t b_desc, uint32_t acc) {
-                        ptx::mma_f16(to, a, b_desc, idesc, acc);
+                multiply<KP / 16, P::kIn, P::kIn>(
+                    steps, [&](int i, int k) { return along_keys(q_desc, i, k); },
+                    [&](int j, int k) { return along_keys(k_desc, j, k); },
+                    [&](uint64_t a, uint64_t b_desc, bool more) {
+                        ptx::mma_f16(to, a, b_desc, idesc, more);
                     });
                 ptx::mma_commit(&bar.scores_full[b]);
                 return true;
@@ -596,19 +648,18 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
             for (int c = 0; c < chunks && ok; ++c) {
                 const int s = stage_of(c);
                 const uint32_t q_at = ptx::smem_u32(smem + s * l.stage);
-                const uint32_t v_at = q_at + P::kIn * 2 * l.tile_k;
+                const uint64_t q_desc = ptx::sw128_desc(q_at);
+                const uint64_t v_desc = ptx::sw128_desc(q_at + P::kIn * 2 * l.tile_k, kSlab);
                 if (!wait(&bar.state_full, c & 1, kFaultMma) ||
                     (c > 0 && !wait(&bar.inter_free, (c - 1) & 1, kFaultMma)))
                     break;
                 ptx::tc_fence_after();
-                multiply<P::kMid, P::kIn>(
+                multiply<KP / 16, P::kMid, P::kIn>(
                     steps,
                     [&](int i, int k) { return tmem + Col::kState + i * (KP / 2) + k * 8; },
-                    [&](int j, int k) {
-                        return ptx::sw128_desc(q_at + j * l.tile_k + (k >> 2) * kSlab + (k & 3) * 32);
-                    },
-                    [&](uint32_t a, uint64_t b_desc, uint32_t acc) {
-                        ptx::mma_f16_tmem_a(tmem + Col::kInter, a, b_desc, idesc, acc);
+                    [&](int j, int k) { return along_keys(q_desc, j, k); },
+                    [&](uint32_t a, uint64_t b_desc, bool more) {
+                        ptx::mma_f16_tmem_a(tmem + Col::kInter, a, b_desc, idesc, more);
                     });
                 ptx::mma_commit(&bar.inter_full);
                 if (ahead && c + 1 < chunks && !(ok = make_scores(c + 1)))
@@ -616,12 +667,11 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
                 if (!wait(&bar.p_full, c & 1, kFaultMma))
                     break;
                 ptx::tc_fence_after();
-                multiply<P::kIn, P::kMid>(
-                    C / 16,
-                    [&](int i, int k) { return ptx::sw128_desc(v_at + i * l.tile_v + k * 2048, kSlab); },
-                    [&](int j, int k) { return ptx::sw128_desc(p_at + j * kSlab + k * 32); },
-                    [&](uint64_t a, uint64_t b_desc, uint32_t acc) {
-                        ptx::mma_f16(tmem + Col::kScores + 64 * (c & 1), a, b_desc, idesc_v, acc);
+                multiply<C / 16, P::kIn, P::kMid>(
+                    C / 16, [&](int i, int k) { return v_desc + i * part_v + k * (2048 >> 4); },
+                    [&](int j, int k) { return p_desc + j * (kSlab >> 4) + k * 2; },
+                    [&](uint64_t a, uint64_t b_desc, bool more) {
+                        ptx::mma_f16(tmem + Col::kScores + 64 * (c & 1), a, b_desc, idesc_v, more);
                     });
                 ptx::mma_commit(&bar.intra_full);
                 ptx::mma_commit(&bar.empty[s]);
@@ -636,20 +686,20 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
         // ---- the states' products ----
         if (lane == 0) {
             constexpr uint32_t idesc = ptx::f16_idesc(128, KP, true, true, true);
-            const uint32_t w_at = ptx::smem_u32(weighted);
+            const uint64_t w_desc = ptx::sw128_desc(ptx::smem_u32(weighted), kSlab);
             for (int c = 0; c < chunks; ++c) {
                 const int s = stage_of(c);
                 if (!wait(&bar.full[s], turn_of(c), kFaultMma) ||
                     !wait(&bar.weighted_full, c & 1, kFaultMma))
                     break;
                 ptx::tc_fence_after();
-                const uint32_t k_at = ptx::smem_u32(smem + s * l.stage) + P::kIn * l.tile_k;
-                multiply<P::kWeighted, P::kIn>(
-                    C / 16,
-                    [&](int i, int k) { return ptx::sw128_desc(w_at + i * l.tile_v + k * 2048, kSlab); },
-                    [&](int j, int k) { return ptx::sw128_desc(k_at + j * l.tile_k + k * 2048, kSlab); },
-                    [&](uint64_t a, uint64_t b_desc, uint32_t acc) {
-                        ptx::mma_f16(tmem + Col::kUpdate, a, b_desc, idesc, acc);
+                const uint64_t k_desc = ptx::sw128_desc(
+                    ptx::smem_u32(smem + s * l.stage) + P::kIn * l.tile_k, kSlab);
+                multiply<C / 16, P::kWeighted, P::kIn>(
+                    C / 16, [&](int i, int k) { return w_desc + i * (l.tile_v >> 4) + k * (2048 >> 4); },
+                    [&](int j, int k) { return k_desc + j * (l.tile_k >> 4) + k * (2048 >> 4); },
+                    [&](uint64_t a, uint64_t b_desc, bool more) {
+                        ptx::mma_f16(tmem + Col::kUpdate, a, b_desc, idesc, more);
                     });
                 ptx::mma_commit(&bar.update_full);
                 ptx::mma_commit(&bar.empty[s]);
@@ -674,7 +724,7 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
             g0 = n0;
             g1 = n1;
         }
-    } else if (!test.withhold) {  // (failure test: nothing is loaded, so the waits for it run out)
+    } else if (warp < W::kLoad + 4 && !test.withhold) {  // (failure test: nothing is loaded, so the waits for it run out)
         // ---- loaders ----
         const int tid = threadIdx.x - W::kLoad * 32;
         const auto arrive = [&](int c) {
@@ -697,11 +747,14 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
             uint8_t *const at = smem + s * l.stage;
             const long long t0 = run.begin + static_cast<long long>(c) * C;
             const int len = min(run.end - run.begin - c * C, C);
-            load_tile<T>(at, l.tile_k, p.q, aligned & 1, t0, head, len, p.keys, KP / 8, 0, tid);
-            load_tile<T>(at + P::kIn * l.tile_k, l.tile_k, p.k, aligned & 2, t0, head, len, p.keys,
-                         KP / 8, 0, tid);
-            load_tile<T>(at + P::kIn * 2 * l.tile_k, l.tile_v, p.v, aligned & 4, t0, head, len, values,
-                         l.slabs * 8, v0, tid);
+            load_tile<T, KP / 8>(at, l.tile_k, p.q, aligned & 1, t0, head, len, p.keys, 0, tid);
+            load_tile<T, KP / 8>(at + P::kIn * l.tile_k, l.tile_k, p.k, aligned & 2, t0, head, len,
+                                 p.keys, 0, tid);
+            uint8_t *const v_at = at + P::kIn * 2 * l.tile_k;
+            if (l.slabs == 1)
+                load_tile<T, 8>(v_at, l.tile_v, p.v, aligned & 4, t0, head, len, values, v0, tid);
+            else
+                load_tile<T, 16>(v_at, l.tile_v, p.v, aligned & 4, t0, head, len, values, v0, tid);
             ptx::cp_async_commit();
             if (waiting >= 0) {
                 ptx::cp_async_wait<1>();
@@ -725,11 +778,22 @@ attention_kernel(const AttentionArgs p, const Layout l, const int aligned, unsig
 template <typename T, int KP>
 int launch(const AttentionArgs &p, cudaStream_t stream)
 {
+    using W = Warps<KP>;
     static SharedMemory memory;
     const Layout l = layout<T, KP>(p.values < 128 ? p.values : 128);
     int st = memory.allow(attention_kernel<T, KP>, 227 * 1024);
     if (st != LSTM_OK)
         return st;
+    if (W::kShare) {
+        // warpgroups that ask for more registers than the block has would wait for ever
+        static const int registers = [] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, attention_kernel<T, KP>) == cudaSuccess ? a.numRegs : 0;
+        }();
+        if (registers != W::kRegisters)
+            return fail(LSTM_E_CUDA, "lstm_linear_attention: %d registers a thread, built for %d",
+                        registers, W::kRegisters);
+    }
     unsigned *fault = fault_word();
     if (!fault)
         return fail(LSTM_E_CUDA, "cannot resolve the device fault word");
@@ -741,7 +805,7 @@ int launch(const AttentionArgs &p, cudaStream_t stream)
     const int aligned = in_place(p.q) | in_place(p.k) << 1 | in_place(p.v) << 2;
     const dim3 grid(static_cast<unsigned>(p.seq.count), static_cast<unsigned>(p.heads),
                     static_cast<unsigned>((p.values + 127) / 128));
-    attention_kernel<T, KP><<<grid, Warps<KP>::kThreads, l.total, stream>>>(
+    attention_kernel<T, KP><<<grid, W::kThreads, l.total, stream>>>(
         p, l, aligned, fault, kernel_test(kTestAttention));
     return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
 }
