@@ -7,6 +7,102 @@
 namespace lstm {
 namespace {
 
+// ---- spans ------------------------------------------------------------------------------
+constexpr int kChunk = 64;   // tokens that the prompts' kernel takes at a time
+constexpr int kSms = 152;    // one block of it on each
+constexpr int kLeastSpan = 4;  // chunks
+// In times of a chunk: what a span's chunk costs beside one of a whole sequence, since its
+// update is made twice, and what the two further launches and the joining cost.
+constexpr double kSpanCost = 1.6, kJoinCost = 8.0;
+
+// Chunks of a span, or 0: sequences are whole.  With few sequences and heads most SMs
+// would idle, and with sequences of unequal length (the longest taken to be twice the mean)
+// the longest would be waited for.
+int span_chunks(int tokens, int heads, int values, int sequences, bool equal_lengths)
+{
+    if (tokens <= 0 || sequences <= 0)
+        return 0;
+    const double blocks = static_cast<double>(heads) * ((values + 127) / 128);
+    const double all = blocks * sequences;
+    if (all > 4 * kSms)
+        return 0;
+    const long long mean = ((tokens - 1LL) / sequences + 1 + kChunk - 1) / kChunk;
+    const auto turns = [](double units) { return static_cast<double>((static_cast<long long>(units) + kSms - 1) / kSms); };
+    const double longest = static_cast<double>(equal_lengths ? mean : 2 * mean);
+    double best = longest > turns(all) * mean ? longest : turns(all) * mean;
+    int chunks = 0;
+    for (long long spans = 2; spans <= 64 && mean / spans >= kLeastSpan; ++spans) {
+        const long long each = (mean + spans - 1) / spans;
+        const double cost = turns(all * spans) * each * kSpanCost + kJoinCost;
+        if (cost < best) {
+            best = cost;
+            chunks = static_cast<int>(each);
+        }
+    }
+    return chunks;
+}
+
+// The spans of a call, without their buffers; their bytes.
+Spans plan_spans(int tokens, int heads, int keys, int values, int sequences, bool equal_lengths,
+                 size_t *bytes)
+{
+    Spans r;
+    r.tokens = span_chunks(tokens, heads, values, sequences, equal_lengths) * kChunk;
+    *bytes = 0;
+    if (r.tokens) {
+        r.units = static_cast<int>(tiles_bound(tokens, sequences, r.tokens));
+        *bytes = static_cast<size_t>(r.units) * heads * (static_cast<size_t>(keys) * values + 1) * 4;
+    }
+    return r;
+}
+
+// From what each span adds to a state of zeros to the states that the spans start from: a
+// thread takes V numbers of a head's state along a sequence's spans.  All it reads are
+// states once, and it writes them once.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinAhead = 4;  // spans in flight
+
+template <int V>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttentionArgs p,
+                                                                      const Spans spans)
+{
+    const int sequence = blockIdx.z, head = blockIdx.y;
+    const long long at = (blockIdx.x * static_cast<long long>(kJoinThreads) + threadIdx.x) * V;
+    const int begin = sequence_begin(p.seq, sequence);
+    const int count = spans.count(sequence_end(p.seq, sequence) - begin);
+    if (count == 1 || at >= p.cells())
+        return;
+    const int unit = begin / spans.tokens + sequence;
+    const int slot = sequence_slot(p.slots, sequence);
+    Pack<float, V> s = {};
+    if (slot >= 0 && sequence_resumes(p.slots, sequence)) {
+        const float *from = p.state_of(slot, head) + at;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s.v[i] = from[i];
+        *reinterpret_cast<Pack<float, V> *>(spans.state_of(p, unit, head) + at) = s;
+    }
+    for (int n = 1; n < count; n += kJoinAhead) {
+        Pack<float, V> add[kJoinAhead];
+        float left[kJoinAhead];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (n + k < count) {
+                add[k] = *reinterpret_cast<const Pack<float, V> *>(
+                    spans.state_of(p, unit + n + k, head) + at);
+                left[k] = *spans.left_of(p, unit + n + k - 1, head);
+            }
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (n + k < count) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    s.v[i] = fmaf(left[k], s.v[i], add[k].v[i]);
+                *reinterpret_cast<Pack<float, V> *>(spans.state_of(p, unit + n + k, head) + at) = s;
+            }
+    }
+}
+
 int check_heads(const char *what, const char *name, HeadRows &m, int own, int heads, int width,
                 int rows, int size)
 {
@@ -59,6 +155,18 @@ int attention(const char *what, AttentionArgs &p, int q_heads, int k_heads, int 
     } else {
         p.slots = Slots{nullptr, nullptr, 0};
     }
+    size_t bytes = 0;
+    Spans spans;
+    if (!step) {
+        spans = plan_spans(rows, p.heads, p.keys, p.values, p.seq.count, !p.seq.offsets, &bytes);
+        if (bytes > 0 && !workspace)
+            return fail(LSTM_E_INVALID, "%s: workspace is null", what);
+        if (workspace_bytes < bytes)
+            return fail(LSTM_E_LENGTH, "%s: workspace has %zu bytes, needs %zu", what,
+                        workspace_bytes, bytes);
+        if ((st = check_aligned(workspace, "workspace")))
+            return st;
+    }
     int device = 0;
     if (p.seq.count == 0 || (no_decay && !p.state))
         return LSTM_OK;
@@ -70,19 +178,45 @@ int attention(const char *what, AttentionArgs &p, int q_heads, int k_heads, int 
     cudaStream_t on = static_cast<cudaStream_t>(stream);
     if (step)
         return launch_attention_step(p, dtype, on);
-    return dtype == LSTM_F32    ? launch_attention_f32(p, on)
-           : dtype == LSTM_BF16 ? launch_attention_bf16(p, on)
-                                : launch_attention_f16(p, on);
+    spans.states = static_cast<float *>(workspace);
+    spans.left = spans.states + static_cast<size_t>(spans.units) * p.heads * p.keys * p.values;
+    return dtype == LSTM_F32    ? launch_attention_f32(p, spans, on)
+           : dtype == LSTM_BF16 ? launch_attention_bf16(p, spans, on)
+                                : launch_attention_f16(p, spans, on);
 }
 
 }  // namespace
+
+int launch_attention_join(const AttentionArgs &p, const Spans &spans, cudaStream_t stream)
+{
+    const int st = check_launch_injection("lstm_linear_attention");
+    if (st != LSTM_OK)
+        return st;
+    const long long cells = static_cast<long long>(p.keys) * p.values;
+    const int vector = cells % 4 == 0 ? 4 : 1;
+    // (sequences that are cut are few)
+    const dim3 grid(static_cast<unsigned>((cells + kJoinThreads * vector - 1) / (kJoinThreads * vector)),
+                    static_cast<unsigned>(p.heads), static_cast<unsigned>(p.seq.count));
+    if (vector == 4)
+        attention_join_kernel<4><<<grid, kJoinThreads, 0, stream>>>(p, spans);
+    else
+        attention_join_kernel<1><<<grid, kJoinThreads, 0, stream>>>(p, spans);
+    return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
+}
+
 }  // namespace lstm
 
 using namespace lstm;
 
-extern "C" size_t lstm_linear_attention_workspace(int, int, int, int, int, int)
+extern "C" size_t lstm_linear_attention_workspace(int tokens, int heads, int keys, int values,
+                                                  int sequences, int equal_lengths)
 {
-    return 0;
+    if (heads <= 0 || heads > LSTM_ATTENTION_MAX_HEADS || keys <= 0 || keys > LSTM_ATTENTION_MAX_KEYS ||
+        values <= 0 || values > LSTM_ATTENTION_MAX_VALUES)
+        return 0;
+    size_t bytes;
+    plan_spans(tokens, heads, keys, values, sequences, equal_lengths != 0, &bytes);
+    return bytes;
 }
 
 extern "C" int lstm_linear_attention(const void *q, long long q_stride, long long q_head_stride,

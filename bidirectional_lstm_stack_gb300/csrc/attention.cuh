@@ -48,9 +48,33 @@ struct AttentionArgs {
     }
 };
 
-int launch_attention_f32(const AttentionArgs &p, cudaStream_t stream);
-int launch_attention_bf16(const AttentionArgs &p, cudaStream_t stream);
-int launch_attention_f16(const AttentionArgs &p, cudaStream_t stream);
+// How prompts are cut into spans.  Spans are numbered as tile_owner() numbers tiles, so a
+// sequence's follow each other.
+struct Spans {
+    int tokens = 0;  // of a span; 0: sequences are whole
+    int units = 0;   // numbers
+    float *states = nullptr;  // [units][heads][keys][values]: what each span starts from
+    float *left = nullptr;    // [units][heads]: the product of its decays
+
+    // of a sequence; one of no rows has one span too, for its state
+    __device__ __forceinline__ int count(int rows) const
+    {
+        return rows > tokens ? (rows - 1) / tokens + 1 : 1;
+    }
+    __device__ __forceinline__ float *state_of(const AttentionArgs &p, int unit, int head) const
+    {
+        return states + (static_cast<long long>(unit) * p.heads + head) * p.cells();
+    }
+    __device__ __forceinline__ float *left_of(const AttentionArgs &p, int unit, int head) const
+    {
+        return left + static_cast<long long>(unit) * p.heads + head;
+    }
+};
+
+int launch_attention_f32(const AttentionArgs &p, const Spans &spans, cudaStream_t stream);
+int launch_attention_bf16(const AttentionArgs &p, const Spans &spans, cudaStream_t stream);
+int launch_attention_f16(const AttentionArgs &p, const Spans &spans, cudaStream_t stream);
+int launch_attention_join(const AttentionArgs &p, const Spans &spans, cudaStream_t stream);
 int launch_attention_step(const AttentionArgs &p, int dtype, cudaStream_t stream);
 
 }  // namespace lstm

@@ -3,9 +3,9 @@
 
 namespace lstm {
 
-int launch_attention_bf16(const AttentionArgs &p, cudaStream_t stream)
+int launch_attention_bf16(const AttentionArgs &p, const Spans &spans, cudaStream_t stream)
 {
-    return prompts::launch_keys<__nv_bfloat16>(p, stream);
+    return prompts::launch_keys<__nv_bfloat16>(p, spans, stream);
 }
 
 }  // namespace lstm

@@ -3,9 +3,9 @@
 
 namespace lstm {
 
-int launch_attention_f16(const AttentionArgs &p, cudaStream_t stream)
+int launch_attention_f16(const AttentionArgs &p, const Spans &spans, cudaStream_t stream)
 {
-    return prompts::launch_keys<__half>(p, stream);
+    return prompts::launch_keys<__half>(p, spans, stream);
 }
 
 }  // namespace lstm
