@@ -40,7 +40,7 @@ constexpr int kRowBytes = 128;  // of a tile's row: 64 bf16
 constexpr int kSlab = C * kRowBytes;
 constexpr int kMaxStages = 3;
 constexpr int kLoaders = 128;
-constexpr float kLeast = -300.0f;  // log2 of a decay that leaves nothing of any fp32 number
+constexpr float kMostDecay = 300.0f;  // log2 of a decay that leaves nothing of any fp32 number
 
 // Parts of bf16 that the numbers of a type are split into.
 template <typename T>
@@ -66,24 +66,30 @@ struct Run {
     float *to;          // null: not kept
 };
 
+// Of q, k and v, for TMA.
+struct Maps {
+    CUtensorMap of[3];
+};
+
 // What one stage holds beside its tiles.
 struct Decays {
     float2 sum[C];   // c_i in log2, as the fp32 next to it and the rest
     float until[C];  // e^(c_64 - c_i)
-    float all;       // e^(c_64)
-    float pad[3];
 };
 
-// What the output warps want to know of a chunk, whose stage may be another chunk's by then.
+// What the output and state warps want to know of a chunk, whose stage may be another
+// chunk's by then.
 // Chunk c + 5 is loaded when y of chunk c is done at the earliest: three stages, and two
 // buffers of scores before y.
 struct Info {
     float since[C];      // e^(c_i)
     int first_bad[128];  // of a value's column: the first token that is not finite, or C
+    float all;           // e^(c_64)
+    float pad[3];
 };
 constexpr int kInfos = 8;
-// w v of a chunk is there: the states are two chunks ahead of the outputs at most
-constexpr int kWeights = 4;
+// V's tile is clean: its weighing is two chunks ahead of the outputs at most
+constexpr int kCleans = 4;
 
 struct Layout {
     int slabs;         // of v: 64 values each
@@ -96,7 +102,8 @@ struct Layout {
 struct Barriers {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t scores_full[2], p_full[2], inter_full[2], intra_full[2], y_free[2];
-    uint64_t weighted_full[kWeights], state_full, update_full;
+    uint64_t weighted_full[2], weighted_free[2];  // of half of the tokens each
+    uint64_t clean[kCleans], state_full, update_full, update_free;
     uint64_t done[2];
     uint32_t tmem;
     int abort;
@@ -195,15 +202,15 @@ __device__ __forceinline__ void load_parts(const uint8_t *at, int apart, float (
 }
 
 // ---- loading ------------------------------------------------------------------------------
-// Rows t0 .. t0 + 63 of a head into a tile of `units` 16-byte units a row (8 or 16); rows
-// from `len` and numbers from `width` on are zeros.  A thread keeps its unit and goes down
-// the rows, so that swizzle and width are worked out once.
+// Rows of a head into a tile, `units` units of 16 bytes a row (a power of two up to 16); rows
+// from `len` and numbers from `width` on are zeros, and what lies behind the units stays.  A
+// thread keeps its unit and goes down the rows, so that swizzle and width are worked out once.
 template <typename T>
 __device__ __forceinline__ void load_tile(uint8_t *tile, int apart, const T *from, long long stride,
                                           bool aligned, int len, int width, int units, int tid)
 {
-    constexpr int kTogether = 4;              // rows in flight
-    const int down = kLoaders / units;        // rows of a turn, a multiple of 8
+    constexpr int kTogether = 4;        // rows in flight
+    const int down = kLoaders / units;  // rows of a turn, a multiple of 8
     const int u = tid & (units - 1), r0 = tid / units;
     const T *src = from + r0 * stride + u * 8;
     const long long step = down * stride;
@@ -211,74 +218,78 @@ __device__ __forceinline__ void load_tile(uint8_t *tile, int apart, const T *fro
     const int there = min(max(width - u * 8, 0), 8);
 #pragma unroll 1
     for (int r = r0; r < C; r += kTogether * down) {
-        if (Parts<T>::kIn == 1 && aligned) {
-#pragma unroll
-            for (int k = 0; k < kTogether; ++k) {
-                const bool in = r + k * down < len && there > 0;
-                // (`from` is an address that may be read, for where there is nothing to read)
-                ptx::cp_async_16(ptx::smem_u32(dst + k * down * kRowBytes),
-                                 in ? src + k * step : from, in ? there * 2 : 0);
-            }
-        } else {
-            float f[kTogether][8];
-            if (aligned && there == 8) {
-                constexpr int V = Elem<T>::kVector;
-#pragma unroll
-                for (int k = 0; k < kTogether; ++k)
-#pragma unroll
-                    for (int j = 0; j < 8; j += V) {
-                        Pack<T, V> v = {};
-                        if (r + k * down < len)
-                            v = load_pack<T, V>(src + k * step + j);
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            f[k][j + e] = Elem<T>::get(v.v[e]);
-                    }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kTogether; ++k)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        f[k][j] = r + k * down < len && j < there ? Elem<T>::get(src[k * step + j])
-                                                                  : 0.0f;
-            }
+        float f[kTogether][8];
+        if (aligned && there == 8) {
+            constexpr int V = Elem<T>::kVector;
 #pragma unroll
             for (int k = 0; k < kTogether; ++k)
-                store_parts<Parts<T>::kIn>(dst + k * down * kRowBytes, apart, f[k]);
+#pragma unroll
+                for (int j = 0; j < 8; j += V) {
+                    Pack<T, V> v = {};
+                    if (r + k * down < len)
+                        v = load_pack<T, V>(src + k * step + j);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        f[k][j + e] = Elem<T>::get(v.v[e]);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[k][j] = r + k * down < len && j < there ? Elem<T>::get(src[k * step + j])
+                                                              : 0.0f;
         }
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+            if (r + k * down < C)
+                store_parts<Parts<T>::kIn>(dst + k * down * kRowBytes, apart, f[k]);
         src += kTogether * step;
         dst += kTogether * down * kRowBytes;
     }
 }
 
-// The sums of a chunk's log decays, two tokens a lane; returns the whole sum, in log2.
-__device__ __forceinline__ double sum_decays(Decays &d, Info &info, float g0, float g1, int lane)
+// A log decay in log2, as a whole number of 2^-40 (of a chunk's sum the 64 tokens need 15 bits
+// above the point): sums are exact, and take no fp64, which this GPU has little of.
+constexpr float kOne = 1099511627776.0f;
+__device__ __forceinline__ long long fixed_decay(float g)
 {
-    const auto log2_of = [](float g) {
-        const double v = static_cast<double>(g) * 1.4426950408889634;
-        return v < kLeast ? static_cast<double>(kLeast) : v;  // (a NaN stays)
-    };
-    const double a = log2_of(g0), b = log2_of(g1);
-    double sum = a + b;
+    const float hi = g * 1.44269502f, most = fminf(fmaxf(hi, -kMostDecay), kMostDecay);
+    // (log2 e = 1.44269502 + 1.92596303e-8)
+    const float lo = hi == most ? fmaf(g, 1.92596303e-8f, fmaf(g, 1.44269502f, -hi)) : 0.0f;
+    return __float2ll_rn(most * kOne) + __float2ll_rn(lo * kOne);
+}
+
+// The sums of a chunk's log decays, two tokens a lane; returns the whole sum.
+__device__ __forceinline__ long long sum_decays(Decays &d, Info &info, float g0, float g1, int lane)
+{
+    const long long b = fixed_decay(g1);
+    long long sum = fixed_decay(g0) + b;
 #pragma unroll 1
     for (int m = 1; m < 32; m *= 2) {
-        const double other = __shfl_up_sync(0xffffffffu, sum, m);
+        const long long other = __shfl_up_sync(0xffffffffu, sum, m);
         if (lane >= m)
             sum += other;
     }
-    const double end = __shfl_sync(0xffffffffu, sum, 31);
+    const long long end = __shfl_sync(0xffffffffu, sum, 31);
+    // a NaN is one to all tokens behind it
+    const unsigned before = (1u << lane) - 1, nan0 = __ballot_sync(0xffffffffu, g0 != g0),
+                   nan1 = __ballot_sync(0xffffffffu, g1 != g1);
+    const auto poison = [](unsigned any) { return any ? __uint_as_float(0x7fffffffu) : 0.0f; };
+    const float all_of = poison(nan0 | nan1);
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
-        const double c = k ? sum : sum - b;
+        const long long c = k ? sum : sum - b;
+        const float of = poison(((nan0 | nan1) & before) | (nan0 >> lane & 1) | (k & nan1 >> lane));
         const int i = 2 * lane + k;
-        const float hi = static_cast<float>(c);
-        d.sum[i] = make_float2(hi, static_cast<float>(c - hi));
-        d.until[i] = ex2(static_cast<float>(end - c));
-        info.since[i] = ex2(hi) * (1.0f + 0.6931472f * static_cast<float>(c - hi));
+        const float hi = __ll2float_rn(c), lo = __ll2float_rn(c - __float2ll_rn(hi)) / kOne;
+        d.sum[i] = make_float2(hi / kOne + of, lo);
+        d.until[i] = ex2(__ll2float_rn(end - c) / kOne) + all_of;
+        info.since[i] = ex2(hi / kOne) * fmaf(0.6931472f, lo, 1.0f) + of;
     }
     *reinterpret_cast<int4 *>(&info.first_bad[4 * lane]) = make_int4(C, C, C, C);
     if (lane == 0)
-        d.all = ex2(static_cast<float>(end));
+        info.all = ex2(__ll2float_rn(end) / kOne) + all_of;
     return end;
 }
 
@@ -299,6 +310,29 @@ __device__ __forceinline__ void not_finite(uint8_t *at, int apart, int *first_ba
                 *reinterpret_cast<unsigned short *>(at + k * apart) = 0;
         }
     }
+}
+
+// A number from or to memory, or not; in the order they are written in, since the compiler
+// would have all addresses of a state in registers at a time.
+__device__ __forceinline__ float load_if(bool there, const float *from)
+{
+    float r;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %2, 0;\n\t"
+                 "mov.b32 %0, 0;\n\t"
+                 "@p ld.global.b32 %0, [%1];\n\t}"
+                 : "=f"(r)
+                 : "l"(from), "r"(static_cast<int>(there))
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ void store_if(bool there, float *to, float v)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %2, 0;\n\t"
+                 "@p st.global.b32 [%0], %1;\n\t}" ::"l"(to),
+                 "f"(v), "r"(static_cast<int>(there))
+                 : "memory");
 }
 
 // ptx::mbar_wait_bounded in as few instructions as it takes: the kernel's warps all run
@@ -324,25 +358,18 @@ __device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, vol
 
 // ---- the kernel ------------------------------------------------------------------------------
 // Thread layout, in warpgroups: two of scores' warps (whose spare places take the two issuing
-// warps and the decays' warp), the output warps, the state warps, the loaders.
-template <int KP>
+// warps and the decays' warp), the output warps, the state warps, the loaders.  With TMA the
+// loaders have nothing to load and write w v in the state warps' stead; where those are eight,
+// they do it themselves, and the block's threads have 96 registers, not 80 (a state of 64
+// numbers a thread wants 90).
+template <int KP, bool TMA>
 struct Warps {
     static constexpr int kOutIssue = 2, kStateIssue = 3, kDecay = 6;
     static constexpr int kOut = 8;
     static constexpr int kState = 12, kStates = 4 * (KP / 64);
-    static constexpr int kLoad = kState + kStates;
-    static constexpr int kThreads = (kLoad + 4) * 32;
-    // Registers: as the block is launched (65536 over its threads), and, with 128 keys, as
-    // its warpgroups then share those of the launch
-    static constexpr int kRegisters = KP > 64 ? 80 : 96;
-    static constexpr bool kShare = KP > 64;
-    static constexpr int kScoresRegisters = 72, kOutRegisters = 64, kStateRegisters = 104,
-                         kLoadRegisters = 64;
-    static_assert(kLoad * 32 + kLoaders == kThreads && kState % 4 == 0, "warpgroups");
-    static_assert(!kShare || kThreads * kRegisters == 256 * kScoresRegisters + 128 * kOutRegisters +
-                                                          kStates * 32 * kStateRegisters +
-                                                          kLoaders * kLoadRegisters,
-                  "registers");
+    static constexpr int kLoad = kState + kStates, kLoads = TMA && KP > 64 ? 0 : kLoaders / 32;
+    static constexpr int kThreads = (kLoad + kLoads) * 32;
+    static constexpr int kWeighers = (TMA && kLoads ? kLoads : kStates) * 32;  // who write w v
 };
 // Tensor memory: two buffers of scores (intra goes where its scores were), one or two of
 // inter, the update, and S^T in up to three parts.
@@ -359,11 +386,11 @@ struct Columns {
 // and a block.  One thread of the warp issues; it does so in a branch that the compiler knows
 // to be one thread's, else every descriptor costs ten instructions.
 template <int NA, int NB, typename A, typename B, typename M>
-__device__ __forceinline__ void multiply(bool leader, int steps, const A &a, const B &b, const M &mma)
+__device__ __forceinline__ void multiply(bool leader, int steps, const A &a, const B &b, const M &mma,
+                                         bool more = false)
 {
     constexpr int most = NA > NB ? NA : NB;
     if (leader) {
-        bool more = false;
         // the small products first
 #pragma unroll 1
         for (int order = most - 1; order >= 0; --order)
@@ -379,14 +406,15 @@ __device__ __forceinline__ void multiply(bool leader, int steps, const A &a, con
     }
 }
 
-template <typename T, int KP>
-__global__ void __launch_bounds__(Warps<KP>::kThreads, 1)
-attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, const Layout l,
-                 const int aligned, unsigned *fault, const KernelTest test)
+template <typename T, int KP, bool TMA>
+__global__ void __launch_bounds__(Warps<KP, TMA>::kThreads, 1)
+attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const Spans spans,
+                 const bool outputs, const Layout l, const int aligned, unsigned *fault, const KernelTest test)
 {
-    using W = Warps<KP>;
+    using W = Warps<KP, TMA>;
     using Col = Columns<T, KP>;
     using P = Parts<T>;
+    constexpr int kWeighers = W::kWeighers;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -430,26 +458,34 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
     }
     const int chunks = (run.end - run.begin + C - 1) / C;
 
-    // (what lies above P's diagonal stays zero)
-    for (int n = threadIdx.x; n < l.p_buffers * l.p / 16; n += W::kThreads)
-        reinterpret_cast<uint4 *>(p_tiles)[n] = make_uint4(0, 0, 0, 0);
+    // (what lies above P's diagonal stays zero, and so do columns behind keys and values)
+    const auto clear = [&](uint8_t *at, int bytes) {
+        for (int n = threadIdx.x; n < bytes / 16; n += W::kThreads)
+            reinterpret_cast<uint4 *>(at)[n] = make_uint4(0, 0, 0, 0);
+    };
+    clear(p_tiles, l.p_buffers * l.p);
+    if (!TMA)
+        clear(smem, min(l.stages, chunks) * l.stage);
     ptx::fence_proxy_async_smem();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            ptx::mbar_init(&bar.full[s], kLoaders + 32);
+            ptx::mbar_init(&bar.full[s], TMA ? 2 : kLoaders / 32 + 1);
             ptx::mbar_init(&bar.empty[s], outputs ? 2 : 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&bar.scores_full[b], 1);
-            ptx::mbar_init(&bar.p_full[b], 3 * 32);
+            ptx::mbar_init(&bar.p_full[b], 3);
             ptx::mbar_init(&bar.inter_full[b], 1);
             ptx::mbar_init(&bar.intra_full[b], 1);
-            ptx::mbar_init(&bar.y_free[b], 4 * 32);
+            ptx::mbar_init(&bar.y_free[b], 4);
+            ptx::mbar_init(&bar.weighted_full[b], kWeighers / 32);
+            ptx::mbar_init(&bar.weighted_free[b], 1);
             ptx::mbar_init(&bar.done[b], 1);
         }
-        for (int b = 0; b < kWeights; ++b)
-            ptx::mbar_init(&bar.weighted_full[b], W::kStates * 32);
-        ptx::mbar_init(&bar.state_full, W::kStates * 32);
+        for (int b = 0; b < kCleans; ++b)
+            ptx::mbar_init(&bar.clean[b], kWeighers / 32);
+        ptx::mbar_init(&bar.state_full, W::kStates);
+        ptx::mbar_init(&bar.update_free, W::kStates);
         ptx::mbar_init(&bar.update_full, 1);
         bar.abort = 0;
         ptx::fence_mbar_init();
@@ -462,31 +498,96 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
-    const auto stage_of = [&](int c) { return c % l.stages; };
-    const auto turn_of = [&](int c) { return static_cast<uint32_t>(c / l.stages) & 1; };
+    // the stage of the next chunk, and the parity of its turn
+    const auto advance = [&](int &s, uint32_t &turn) {
+        if (++s == l.stages) {
+            s = 0;
+            turn ^= 1;
+        }
+    };
     // where a chunk stands in buffers used in turn
     const auto parity_of = [](int c, int buffers) { return static_cast<uint32_t>(c / buffers) & 1; };
     // (by all lanes of a warp)
     const auto wait = [&](uint64_t *b, uint32_t parity, unsigned code) {
         return __all_sync(0xffffffffu, wait_bounded(b, parity, abort, fault, code, test.wait_limit_ns)) != 0;
     };
+    // what all lanes did before is there
+    const auto arrive = [&](uint64_t *b) {
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(b);
+    };
+    // w v of chunk c in two halves, and V's tile without what the products must not meet
+    const auto weigh = [&](int c, int s, uint32_t turn, int tid) {
+        if (!wait(&bar.full[s], turn, kFaultConverter))
+            return false;
+        uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
+        const Decays &d = decays[s];
+        int *const first_bad = infos[c % kInfos].first_bad;
+        const int len = TMA ? min(run.end - run.begin - c * C, C) : C;
+        if (TMA && len < C) {
+            // rows of other tokens came along: none of their keys joins the state
+            for (int n = tid; n < l.tile_k / 16; n += kWeighers)
+                if ((n >> 3 & (C - 1)) >= len)
+                    reinterpret_cast<uint4 *>(tile - l.tile_k)[n] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            // w v of the chunk before has been multiplied
+            if (c > 0 && !wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter))
+                return false;
+            uint8_t *const to = weighted + half * (l.weighted / 2);
+#pragma unroll 1
+            for (int n0 = tid; n0 < l.slabs * 256; n0 += 2 * kWeighers) {
+                float none = 0.0f;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int n = n0 + m * kWeighers;
+                    if (m > 0 && n >= l.slabs * 256)
+                        break;
+                    const int j = half * 32 + (n >> 3 & 31);
+                    uint8_t *const at = tile + (n >> 8) * kSlab + half * (kSlab / 2) + (n & 255) * 16;
+                    float f[8];
+                    load_parts<P::kIn>(at, l.tile_v, f);
+                    if (TMA && j >= len) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = 0.0f;
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
+                    }
+                    const float w = d.until[j];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        none = fmaf(f[e], 0.0f, none);
+                        f[e] *= w;
+                    }
+                    store_parts<kWeighted>(to + n * 16, l.slabs * (kSlab / 2), f);
+                }
+                if (none != 0.0f) {
+#pragma unroll 1
+                    for (int n = n0; n <= n0 + kWeighers && n < l.slabs * 256; n += kWeighers) {
+                        const int j = half * 32 + (n >> 3 & 31);
+                        not_finite<P::kIn>(tile + (n >> 8) * kSlab + half * (kSlab / 2) + (n & 255) * 16,
+                                           l.tile_v, first_bad + (n >> 8) * 64 + ((n ^ j) & 7) * 8, j);
+                    }
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            arrive(&bar.weighted_full[half]);
+        }
+        if (lane == 0)
+            ptx::mbar_arrive(&bar.clean[c % kCleans]);
+        return true;
+    };
 
-    if constexpr (W::kShare) {
-        if (warp < W::kOut)
-            ptx::fewer_registers<W::kScoresRegisters>();
-        else if (warp < W::kState)
-            ptx::fewer_registers<W::kOutRegisters>();
-        else if (warp < W::kLoad)
-            ptx::more_registers<W::kStateRegisters>();
-        else
-            ptx::fewer_registers<W::kLoadRegisters>();
-    }
     if (warp < W::kOut && (warp & 3) < 2) {
         // ---- scores to P: lanes are queries; a warp takes 32 of them and 32 keys ----
         const int quarter = warp & 3, half = warp >> 2, i = quarter * 32 + lane;
         if (outputs && half <= quarter) {  // (keys behind all of the queries: zeros)
-            for (int c = 0; c < chunks; ++c) {
-                const int s = stage_of(c), b = c & 1;
+            int s = 0;
+            uint32_t turn = 0;
+            for (int c = 0; c < chunks; ++c, advance(s, turn)) {
+                const int b = c & 1;
                 const uint32_t columns = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                          Col::kScores + C * b + 32 * half;
                 const Decays &d = decays[s];
@@ -494,12 +595,12 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
                 const int before = c - l.p_buffers;
                 const bool ok = (before < 0 || wait(&bar.intra_full[before & 1],
                                                     parity_of(before, 2), kFaultConverter)) &&
-                                wait(&bar.full[s], turn_of(c), kFaultConverter) &&
+                                wait(&bar.full[s], turn, kFaultConverter) &&
                                 wait(&bar.scores_full[b], parity_of(c, 2), kFaultConverter);
                 if (!ok || *abort)
                     break;
                 ptx::tc_fence_after();
-                uint8_t *const row = p_tiles + c % l.p_buffers * l.p + i * kRowBytes;
+                uint8_t *const row = p_tiles + (c & (l.p_buffers - 1)) * l.p + i * kRowBytes;
                 const int swizzle = (i & 7) << 4;
                 const float2 mine = d.sum[i];
 #pragma unroll 1
@@ -525,7 +626,7 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
                 }
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&bar.p_full[b]);
+                arrive(&bar.p_full[b]);
             }
         }
     } else if (warp >= W::kOut && warp < W::kState) {
@@ -588,17 +689,21 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
                 }
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(&bar.y_free[b]);
+            arrive(&bar.y_free[b]);
             if constexpr (sizeof(T) == 2) {
-                __syncwarp();
                 if (aligned & 8) {
                     // 8 values of 8 rows at a time
                     const int col = (lane & 3) * 8;
-#pragma unroll 2
-                    for (int e = lane >> 2; e < len; e += 8) {
-                        const Pack<T, 8> some = *reinterpret_cast<const Pack<T, 8> *>(slice + e * 32 + col);
-                        if (col + 8 <= width)
-                            store_pack<T, 8>(at + e * p.y_stride + col, some);
+#pragma unroll 1
+                    for (int e0 = lane >> 2; e0 < len; e0 += 32) {
+                        Pack<T, 8> some[4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            some[n] = *reinterpret_cast<const Pack<T, 8> *>(slice + (e0 + n * 8) * 32 + col);
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            if (e0 + n * 8 < len && col < width)
+                                store_pack<T, 8>(at + (e0 + n * 8) * p.y_stride + col, some[n]);
                     }
                 } else if (lane < width) {
 #pragma unroll 1
@@ -621,20 +726,20 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
             const int there = run.from ? some : 0;
 #pragma unroll
             for (int n = 0; n < 64; ++n) {
-                h[n] = n < there ? *from : 0.0f;
+                h[n] = load_if(n < there, from);
                 from += p.values;
             }
         }
-        float left = 0.0f;  // of the state, over chunk c
+        int s = 0;
+        uint32_t turn = 0;
         // chunk c: its update joins the state; then w v of the next one, and the state for it
 #pragma unroll 1
         for (int c = -1; c < chunks; ++c) {
-            bool ok = true;
             if (c >= 0) {
-                ok = wait(&bar.update_full, c & 1, kFaultConverter);
-                if (!ok || *abort)
+                if (!wait(&bar.update_full, c & 1, kFaultConverter) || *abort)
                     break;
                 ptx::tc_fence_after();
+                const float left = infos[c % kInfos].all;
 #pragma unroll
                 for (int n0 = 0; n0 < 64; n0 += 16) {
                     uint32_t r[16];
@@ -644,53 +749,22 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
                     for (int n = 0; n < 16; ++n)
                         h[n0 + n] = fmaf(h[n0 + n], left, __uint_as_float(r[n]));
                 }
-                // (the next update may overwrite this one when w v is there)
                 ptx::tc_fence_before();
+                arrive(&bar.update_free);
             }
-            const int next = c + 1;
-            if (next == chunks)
+            if (c + 1 == chunks)
                 break;
-            const int s = stage_of(next);
-            const Decays &d = decays[s];
-            if (!wait(&bar.full[s], turn_of(next), kFaultConverter))
-                break;
-            uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
-            left = d.all;
-#pragma unroll 1
-            for (int n0 = tid; n0 < l.tile_v / 16; n0 += 2 * W::kStates * 32) {
-                float none = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int n = n0 + m * W::kStates * 32;
-                    float f[8];
-                    load_parts<P::kIn>(tile + n * 16, l.tile_v, f);
-                    const float w = d.until[(n >> 3) & (C - 1)];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        none = fmaf(f[e], 0.0f, none);
-                        f[e] *= w;
-                    }
-                    store_parts<kWeighted>(weighted + n * 16, l.tile_v, f);
-                }
-                if (none != 0.0f) {
-#pragma unroll 1
-                    for (int n = n0; n <= n0 + W::kStates * 32; n += W::kStates * 32) {
-                        const int j = (n >> 3) & (C - 1);
-                        not_finite<P::kIn>(tile + n * 16, l.tile_v,
-                                           infos[next % kInfos].first_bad +
-                                               n / (kSlab / 16) * 64 + ((n ^ j) & 7) * 8, j);
-                    }
-                }
+            if (!TMA || !W::kLoads) {
+                if (!weigh(c + 1, s, turn, tid))
+                    break;
+                advance(s, turn);
             }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&bar.weighted_full[next % kWeights]);
             if (!outputs)
                 continue;
             if (c >= 0) {
                 // S of chunk c has been multiplied
-                ok = wait(&bar.inter_full[c % Col::kInters], parity_of(c, Col::kInters),
-                          kFaultConverter);
-                if (!ok || *abort)
+                if (!wait(&bar.inter_full[c % Col::kInters], parity_of(c, Col::kInters),
+                          kFaultConverter) || *abort)
                     break;
                 ptx::tc_fence_after();
             }
@@ -712,14 +786,13 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(&bar.state_full);
+            arrive(&bar.state_full);
         }
         if (run.to && !*abort) {
             float *to = run.to + k0 * p.values + v;
 #pragma unroll
             for (int n = 0; n < 64; ++n) {
-                if (n < some)
-                    *to = h[n];
+                store_if(n < some, to, h[n]);
                 to += p.values;
             }
         }
@@ -736,59 +809,79 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
             const auto along_keys = [&](uint64_t desc, int part, int k) {
                 return desc + part * part_k + (k >> 2) * (kSlab >> 4) + (k & 3) * 2;
             };
+            // scores, intra of the chunk before (with one stage, whose tiles the next scores
+            // want gone: of the same chunk), inter
+            const int lag = l.stages > 1 ? 1 : 0;
+            int s = 0, s_intra = 0;
+            uint32_t turn = 0;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int s = stage_of(c), b = c & 1;
-                // a buffer of scores is free, and so is one of two of inter, when y of the
-                // chunk before in it has been read
-                if (!wait(&bar.full[s], turn_of(c), kFaultMma) ||
-                    (c >= 2 && !wait(&bar.y_free[b], parity_of(c - 2, 2), kFaultMma)))
-                    break;
-                ptx::tc_fence_after();
-                const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(smem + s * l.stage));
-                const uint64_t k_desc = q_desc + P::kIn * part_k;
-                const uint64_t v_desc = ptx::sw128_desc(
-                    ptx::smem_u32(smem + s * l.stage + P::kIn * 2 * l.tile_k), kSlab);
-                const uint32_t scores = tmem + Col::kScores + C * b;
-                multiply<P::kIn, P::kIn>(
-                    leader, steps, [&](int i, int k) { return along_keys(q_desc, i, k); },
-                    [&](int j, int k) { return along_keys(k_desc, j, k); },
-                    [&](uint64_t a, uint64_t b_desc, bool more) {
-                        ptx::mma_f16(scores, a, b_desc, idesc, more);
-                    });
-                if (leader)
-                    ptx::mma_commit(&bar.scores_full[b]);
-                if (!wait(&bar.state_full, c & 1, kFaultMma) ||
-                    (Col::kInters == 1 && c > 0 &&
-                     !wait(&bar.y_free[b ^ 1], parity_of(c - 1, 2), kFaultMma)))
-                    break;
-                ptx::tc_fence_after();
-                const uint32_t inter = tmem + Col::kInter + C * (c % Col::kInters);
-                multiply<P::kMid, P::kIn>(
-                    leader, steps,
-                    [&](int i, int k) { return tmem + Col::kState + i * (KP / 2) + k * 8; },
-                    [&](int j, int k) { return along_keys(q_desc, j, k); },
-                    [&](uint32_t a, uint64_t b_desc, bool more) {
-                        ptx::mma_f16_tmem_a(inter, a, b_desc, idesc, more);
-                    });
-                if (leader)
-                    ptx::mma_commit(&bar.inter_full[c % Col::kInters]);
-                // (w v is there: values that are not finite have left V's tile)
-                if (!wait(&bar.p_full[b], parity_of(c, 2), kFaultMma) ||
-                    !wait(&bar.weighted_full[c % kWeights], parity_of(c, kWeights), kFaultMma))
-                    break;
-                ptx::tc_fence_after();
-                const uint64_t p_desc = p_descs + c % l.p_buffers * (l.p >> 4);
-                multiply<P::kIn, P::kMid>(
-                    leader, C / 16, [&](int i, int k) { return v_desc + i * part_v + k * (2048 >> 4); },
-                    [&](int j, int k) { return p_desc + j * (kSlab >> 4) + k * 2; },
-                    [&](uint64_t a, uint64_t b_desc, bool more) {
-                        ptx::mma_f16(scores, a, b_desc, idesc_v, more);
-                    });
-                if (leader) {
-                    ptx::mma_commit(&bar.intra_full[b]);
-                    ptx::mma_commit(&bar.empty[s]);
+            for (int c = 0; c < chunks + lag; ++c) {
+                uint8_t *const stage = smem + s * l.stage;
+                const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(stage));
+                if (c < chunks) {
+                    // a buffer of scores is free, and so is one of two of inter, when y of the
+                    // chunk before in it has been read
+                    if (!wait(&bar.full[s], turn, kFaultMma) ||
+                        (c >= 2 && !wait(&bar.y_free[c & 1], parity_of(c - 2, 2), kFaultMma)))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint64_t k_desc = q_desc + P::kIn * part_k;
+                    const uint32_t scores = tmem + Col::kScores + C * (c & 1);
+                    multiply<P::kIn, P::kIn>(
+                        leader, steps, [&](int i, int k) { return along_keys(q_desc, i, k); },
+                        [&](int j, int k) { return along_keys(k_desc, j, k); },
+                        [&](uint64_t a, uint64_t b_desc, bool more) {
+                            ptx::mma_f16(scores, a, b_desc, idesc, more);
+                        });
+                    if (leader)
+                        ptx::mma_commit(&bar.scores_full[c & 1]);
                 }
+                const int of = c - lag;
+                if (of >= 0) {
+                    // (w v is there: what is not finite has left V's tile)
+                    if (!wait(&bar.p_full[of & 1], parity_of(of, 2), kFaultMma) ||
+                        !wait(&bar.clean[of % kCleans], parity_of(of, kCleans), kFaultMma))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint64_t p_desc = p_descs + (of & (l.p_buffers - 1)) * (l.p >> 4);
+                    const uint64_t v_desc = ptx::sw128_desc(
+                        ptx::smem_u32(smem + s_intra * l.stage + P::kIn * 2 * l.tile_k), kSlab);
+                    const uint32_t intra = tmem + Col::kScores + C * (of & 1);
+                    multiply<P::kIn, P::kMid>(
+                        leader, C / 16,
+                        [&](int i, int k) { return v_desc + i * part_v + k * (2048 >> 4); },
+                        [&](int j, int k) { return p_desc + j * (kSlab >> 4) + k * 2; },
+                        [&](uint64_t a, uint64_t b_desc, bool more) {
+                            ptx::mma_f16(intra, a, b_desc, idesc_v, more);
+                        });
+                    if (leader) {
+                        ptx::mma_commit(&bar.intra_full[of & 1]);
+                        if (lag)
+                            ptx::mma_commit(&bar.empty[s_intra]);
+                    }
+                }
+                s_intra = s;
+                if (c < chunks) {
+                    if (!wait(&bar.state_full, c & 1, kFaultMma) ||
+                        (Col::kInters == 1 && c > 0 &&
+                         !wait(&bar.y_free[(c - 1) & 1], parity_of(c - 1, 2), kFaultMma)))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint32_t inter = tmem + Col::kInter + C * (c % Col::kInters);
+                    multiply<P::kMid, P::kIn>(
+                        leader, steps,
+                        [&](int i, int k) { return tmem + Col::kState + i * (KP / 2) + k * 8; },
+                        [&](int j, int k) { return along_keys(q_desc, j, k); },
+                        [&](uint32_t a, uint64_t b_desc, bool more) {
+                            ptx::mma_f16_tmem_a(inter, a, b_desc, idesc, more);
+                        });
+                    if (leader) {
+                        ptx::mma_commit(&bar.inter_full[c % Col::kInters]);
+                        if (!lag)
+                            ptx::mma_commit(&bar.empty[s]);
+                    }
+                }
+                advance(s, turn);
             }
             // every product has completed before tensor memory is freed
             if (leader)
@@ -801,25 +894,43 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
         {
             const bool leader = ptx::elect_one();
             constexpr uint32_t idesc = ptx::f16_idesc(128, KP, true, true, true);
-            const uint64_t w_desc = ptx::sw128_desc(ptx::smem_u32(weighted), kSlab);
-            for (int c = 0; c < chunks; ++c) {
-                const int s = stage_of(c);
-                if (!wait(&bar.full[s], turn_of(c), kFaultMma) ||
-                    !wait(&bar.weighted_full[c % kWeights], parity_of(c, kWeights), kFaultMma))
+            const int part_w = l.slabs * (kSlab / 2) >> 4;
+            int s = 0;
+            uint32_t turn = 0;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c, advance(s, turn)) {
+                if (!wait(&bar.full[s], turn, kFaultMma) ||
+                    (c > 0 && !wait(&bar.update_free, (c - 1) & 1, kFaultMma)))
                     break;
-                ptx::tc_fence_after();
                 const uint64_t k_desc = ptx::sw128_desc(
                     ptx::smem_u32(smem + s * l.stage) + P::kIn * l.tile_k, kSlab);
-                multiply<kWeighted, P::kIn>(
-                    leader, C / 16, [&](int i, int k) { return w_desc + i * (l.tile_v >> 4) + k * (2048 >> 4); },
-                    [&](int j, int k) { return k_desc + j * (l.tile_k >> 4) + k * (2048 >> 4); },
-                    [&](uint64_t a, uint64_t b_desc, bool more) {
-                        ptx::mma_f16(tmem + Col::kUpdate, a, b_desc, idesc, more);
-                    });
-                if (leader) {
-                    ptx::mma_commit(&bar.update_full);
-                    ptx::mma_commit(&bar.empty[s]);
+                const uint64_t w_desc = ptx::sw128_desc(ptx::smem_u32(weighted), kSlab / 2);
+                bool ok = true;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    ok = wait(&bar.weighted_full[half], c & 1, kFaultMma);
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after();
+                    const uint64_t a_desc = w_desc + half * (l.weighted >> 5);
+                    const uint64_t b_desc = k_desc + half * (kSlab >> 5);
+                    multiply<kWeighted, P::kIn>(
+                        leader, C / 32, [&](int i, int k) { return a_desc + i * part_w + k * (2048 >> 4); },
+                        [&](int j, int k) { return b_desc + j * (l.tile_k >> 4) + k * (2048 >> 4); },
+                        [&](uint64_t a, uint64_t b, bool more) {
+                            ptx::mma_f16(tmem + Col::kUpdate, a, b, idesc, more);
+                        },
+                        half > 0);
+                    if (leader) {
+                        ptx::mma_commit(&bar.weighted_free[half]);
+                        if (half == 1) {
+                            ptx::mma_commit(&bar.update_full);
+                            ptx::mma_commit(&bar.empty[s]);
+                        }
+                    }
                 }
+                if (!ok)
+                    break;
             }
             if (leader)
                 ptx::mma_commit(&bar.done[1]);
@@ -832,63 +943,91 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
             return t < run.end ? __ldg(p.decay + t * p.decay_stride + head) : 0.0f;
         };
         float g0 = decay_at(0, 2 * lane), g1 = decay_at(0, 2 * lane + 1);
-        double total = 0.0;
-        for (int c = 0; c < chunks; ++c) {
-            const int s = stage_of(c);
+        long long total = 0;
+        bool nan = false;
+        int s = 0, issued = 0;
+        uint32_t turn = 0;
+        for (int c = 0; c < chunks; ++c, advance(s, turn)) {
             const float n0 = decay_at(c + 1, 2 * lane), n1 = decay_at(c + 1, 2 * lane + 1);
-            const bool ok = c < l.stages || wait(&bar.empty[s], turn_of(c) ^ 1, kFaultProducer);
-            if (!ok)
+            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
                 break;
+            // (failure test: nothing is loaded, so the waits for it run out)
+            if (TMA && !test.withhold) {
+                if (lane == 0) {
+                    uint8_t *to = smem + s * l.stage;
+                    const int t0 = run.begin + c * C;
+                    ptx::mbar_arrive_expect_tx(&bar.full[s], (outputs ? 2 : 1) * l.tile_k + l.tile_v);
+#pragma unroll 1
+                    for (int which = outputs ? 0 : 1; which < 3; ++which) {
+                        const int share = which == 0 ? p.q.share : which == 1 ? p.k.share : p.v.share;
+                        const int slabs = which == 2 ? l.slabs : KP / 64;
+#pragma unroll 1
+                        for (int slab = 0; slab < slabs; ++slab)
+                            ptx::tma_load_3d(to + which * l.tile_k + slab * kSlab, &maps.of[which],
+                                             &bar.full[s], (which == 2 ? v0 : 0) + slab * 64,
+                                             head / share, t0);
+                    }
+                }
+                ++issued;
+            }
             total += sum_decays(decays[s], infos[c % kInfos], g0, g1, lane);
-            ptx::mbar_arrive(&bar.full[s]);
+            // (what has left nothing leaves nothing; the sum stays in range)
+            total = max(total, -(1ll << 52));
+            nan |= g0 != g0 || g1 != g1;
+            arrive(&bar.full[s]);
             g0 = n0;
             g1 = n1;
         }
+        if (TMA) {
+            // every load has landed before the CTA's shared memory goes away
+            for (int c = max(issued - l.stages, 0); c < issued; ++c)
+                ptx::mbar_wait_drain(&bar.full[c % l.stages], c / l.stages & 1, fault,
+                                     kDefaultWaitLimitNs);
+        }
+        nan = __any_sync(0xffffffffu, nan);
         if (!outputs && lane == 0 && blockIdx.z == 0)
-            *spans.left_of(p, blockIdx.x, head) = exp2f(static_cast<float>(total));
-    } else if (warp >= W::kLoad && !test.withhold) {  // (failure test: nothing is loaded, so the waits for it run out)
+            *spans.left_of(p, blockIdx.x, head) =
+                nan ? __uint_as_float(0x7fffffffu) : ex2(__ll2float_rn(total) / kOne);
+    } else if (TMA && warp >= W::kLoad) {
+        // ---- w v ----
+        int s = 0;
+        uint32_t turn = 0;
+        for (int c = 0; c < chunks; ++c, advance(s, turn))
+            if (!weigh(c, s, turn, threadIdx.x - W::kLoad * 32))
+                break;
+    } else if (warp >= W::kLoad && !test.withhold) {
         // ---- loaders ----
         const int tid = threadIdx.x - W::kLoad * 32;
-        const auto arrive = [&](int c) {
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&bar.full[stage_of(c)]);
-        };
-        int waiting = -1;  // the chunk whose copies have been asked for and not waited for
-        for (int c = 0; c < chunks; ++c) {
-            const int s = stage_of(c);
-            if (c >= l.stages &&
-                !__all_sync(0xffffffffu, ptx::mbar_try_wait(&bar.empty[s], turn_of(c) ^ 1))) {
-                // nothing more can be asked for yet
-                if (waiting >= 0) {
-                    ptx::cp_async_wait_all();
-                    arrive(waiting);
-                    waiting = -1;
-                }
-                if (!wait(&bar.empty[s], turn_of(c) ^ 1, kFaultProducer))
-                    break;
-            }
-            uint8_t *const at = smem + s * l.stage;
+        int s = 0;
+        uint32_t turn = 0;
+        for (int c = 0; c < chunks; ++c, advance(s, turn)) {
             const long long t0 = run.begin + static_cast<long long>(c) * C;
             const int len = min(run.end - run.begin - c * C, C);
+            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
+                break;
+            uint8_t *const to = smem + s * l.stage;
 #pragma unroll 1
             for (int which = outputs ? 0 : 1; which < 3; ++which) {
                 const HeadRows &m = which == 0 ? p.q : which == 1 ? p.k : p.v;
                 const bool of_v = which == 2;
-                load_tile<T>(at + which * P::kIn * l.tile_k, of_v ? l.tile_v : l.tile_k,
-                             m.row<T>(t0, head) + (of_v ? v0 : 0), m.stride,
-                             aligned >> which & 1, len, of_v ? values : p.keys,
-                             of_v ? l.slabs * 8 : KP / 8, tid);
+                const int width = of_v ? values : p.keys;
+                const T *const from = m.row<T>(t0, head) + (of_v ? v0 : 0);
+                // the next chunk's rows are on their way to L2 meanwhile, two threads a row
+                const int row = C + (tid >> 1);
+                if (c * C + row < run.end - run.begin) {
+                    const char *next = reinterpret_cast<const char *>(from + row * m.stride);
+                    for (int n = (tid & 1) * 128; n < width * static_cast<int>(sizeof(T)); n += 256)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + n));
+                }
+                int units = 1;
+                while (units * 8 < width)
+                    units *= 2;
+                load_tile<T>(to + which * P::kIn * l.tile_k, of_v ? l.tile_v : l.tile_k, from,
+                             m.stride, aligned >> which & 1, len, width, units, tid);
             }
-            ptx::cp_async_commit();
-            if (waiting >= 0) {
-                ptx::cp_async_wait<1>();
-                arrive(waiting);
-            }
-            waiting = c;
+            ptx::fence_proxy_async_smem();
+            arrive(&bar.full[s]);
         }
-        ptx::cp_async_wait_all();
-        if (waiting >= 0)
-            arrive(waiting);
     }
 
     ptx::tc_fence_before();
@@ -899,50 +1038,62 @@ attention_kernel(const AttentionArgs p, const Spans spans, const bool outputs, c
     }
 }
 
-template <typename T, int KP>
-int launch(const AttentionArgs &p, const Spans &spans, bool outputs, cudaStream_t stream)
+template <typename T, int KP, bool TMA>
+int launch(const Maps &maps, int aligned, const AttentionArgs &p, const Spans &spans, bool outputs,
+           cudaStream_t stream)
 {
-    using W = Warps<KP>;
+    using W = Warps<KP, TMA>;
     static SharedMemory memory;
     const Layout l = layout<T, KP>(p.values < 128 ? p.values : 128);
-    int st = memory.allow(attention_kernel<T, KP>, 227 * 1024);
+    int st = memory.allow(attention_kernel<T, KP, TMA>, 227 * 1024);
     if (st != LSTM_OK)
         return st;
-    if (W::kShare) {
-        // warpgroups that ask for more registers than the block has would wait for ever
-        static const int registers = [] {
-            cudaFuncAttributes a;
-            return cudaFuncGetAttributes(&a, attention_kernel<T, KP>) == cudaSuccess ? a.numRegs : 0;
-        }();
-        if (registers != W::kRegisters)
-            return fail(LSTM_E_CUDA, "lstm_linear_attention: %d registers a thread, built for %d",
-                        registers, W::kRegisters);
-    }
     unsigned *fault = fault_word();
     if (!fault)
         return fail(LSTM_E_CUDA, "cannot resolve the device fault word");
     if ((st = check_launch_injection("lstm_linear_attention")))
         return st;
-    const auto in_place = [](const HeadRows &m) {
-        return rows_aligned(m.at, m.stride, sizeof(T)) && m.head_stride * sizeof(T) % 16 == 0;
-    };
-    const bool y_vectors = rows_aligned(p.y, p.y_stride, sizeof(T)) && p.values % 8 == 0;
-    const int aligned = in_place(p.q) | in_place(p.k) << 1 | in_place(p.v) << 2 | y_vectors << 3;
     const dim3 grid(static_cast<unsigned>(spans.tokens ? spans.units : p.seq.count),
                     static_cast<unsigned>(p.heads), static_cast<unsigned>((p.values + 127) / 128));
-    attention_kernel<T, KP><<<grid, W::kThreads, l.total, stream>>>(
-        p, spans, outputs, l, aligned, fault, kernel_test(kTestAttention));
+    attention_kernel<T, KP, TMA><<<grid, W::kThreads, l.total, stream>>>(
+        maps, p, spans, outputs, l, aligned, fault, kernel_test(kTestAttention));
     return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
+}
+
+template <typename T, int KP, bool TMA>
+int launch_passes(const Maps &maps, int aligned, const AttentionArgs &p, const Spans &spans,
+                  cudaStream_t stream)
+{
+    int st;
+    if (spans.tokens && ((st = launch<T, KP, TMA>(maps, aligned, p, spans, false, stream)) ||
+                         (st = launch_attention_join(p, spans, stream))))
+        return st;
+    return launch<T, KP, TMA>(maps, aligned, p, spans, true, stream);
 }
 
 template <typename T, int KP>
 int launch_all(const AttentionArgs &p, const Spans &spans, cudaStream_t stream)
 {
-    int st;
-    if (spans.tokens && ((st = launch<T, KP>(p, spans, false, stream)) ||
-                         (st = launch_attention_join(p, spans, stream))))
-        return st;
-    return launch<T, KP>(p, spans, true, stream);
+    Maps maps = {};
+    const int tokens = p.seq.tokens;
+    int aligned = 0;
+    const auto in_place = [&](const HeadRows &m) {
+        return rows_aligned(m.at, tokens > 1 ? m.stride : 0, sizeof(T)) &&
+               m.head_stride * sizeof(T) % 16 == 0;
+    };
+    aligned = in_place(p.q) | in_place(p.k) << 1 | in_place(p.v) << 2;
+    if (rows_aligned(p.y, tokens > 1 ? p.y_stride : 0, sizeof(T)) && p.values % 8 == 0)
+        aligned |= 8;
+    if constexpr (Parts<T>::kIn == 1) {
+        // (a map that the driver does not make: the rows are loaded by threads)
+        const auto map = [&](CUtensorMap *to, const HeadRows &m, int width) {
+            return encode_heads_map(to, m.at, tokens, p.heads / m.share, width, m.stride, m.head_stride);
+        };
+        if ((aligned & 7) == 7 && tokens > 0 && map(&maps.of[0], p.q, p.keys) &&
+            map(&maps.of[1], p.k, p.keys) && map(&maps.of[2], p.v, p.values))
+            return launch_passes<T, KP, true>(maps, aligned, p, spans, stream);
+    }
+    return launch_passes<T, KP, false>(maps, aligned, p, spans, stream);
 }
 
 template <typename T>

@@ -131,6 +131,11 @@ int encode_store_map(CUtensorMap *map, float *base, long rows, int cols);
 // what a box has beyond the matrix reads as zeros and is not written.
 int encode_box_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, long long rows,
                    long long cols, long long pitch_bytes, int box_rows);
+// Map of 16-bit rows of heads, [tokens][heads][width] with strides in elements (multiples of
+// 8, as the base is of 16 bytes), in boxes of 64 tokens of one head x 64 elements, otherwise
+// as encode_box_map's (bf16).  False: the driver does not make it.
+bool encode_heads_map(CUtensorMap *map, const void *base, long long tokens, int heads, int width,
+                      long long stride, long long head_stride);
 
 // ---- dense heads of the segmentation model (heads.cu) ----------------------
 // W rows of one k-block of the heads' weights (all 128 output columns).
@@ -261,6 +266,14 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 // Global -> this CTA's shared memory, `bytes` (a multiple of 16, both
@@ -441,19 +454,6 @@ __device__ __forceinline__ uint32_t tmem_ld_32x32b_x1(uint32_t taddr)
 __device__ __forceinline__ void tmem_ld_wait()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// Registers a thread of this warpgroup (every warp of it executes this): fewer are given
-// back, more are taken from what the block was launched with.
-template <int N>
-__device__ __forceinline__ void fewer_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void more_registers()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---- clusters / distributed shared memory ----

@@ -497,6 +497,25 @@ int encode_box_map(CUtensorMap *map, CUtensorMapDataType type, const void *base,
     return LSTM_OK;
 }
 
+bool encode_heads_map(CUtensorMap *map, const void *base, long long tokens, int heads, int width,
+                      long long stride, long long head_stride)
+{
+    auto encode = encode_fn();
+    if (!encode)
+        return false;
+    const long long own = (width + 7) / 8 * 8;  // (of what is there once a stride says nothing)
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : own) * 2,
+                                   static_cast<cuuint64_t>(tokens > 1 ? stride : own) * 2};
+    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                  box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 // Every instantiation, for the per-device attributes.
 const void *const kKernels[] = {
