@@ -12,8 +12,9 @@ constexpr int kChunk = 64;   // tokens that the prompts' kernel takes at a time
 constexpr int kSms = 152;    // one block of it on each
 constexpr int kLeastSpan = 4;  // chunks
 // In times of a chunk: what a span's chunk costs beside one of a whole sequence, since its
-// update is made twice, and what the two further launches and the joining cost.
-constexpr double kSpanCost = 1.6, kJoinCost = 8.0;
+// update is made twice; what starting a block costs, twice too; the two further launches;
+// and joining one head's state of one span (128 x 128: written and read twice).
+constexpr double kSpanCost = 1.6, kStartCost = 5.0, kLaunchCost = 2.0, kJoinCost = 0.01;
 
 // Chunks of a span, or 0: sequences are whole.  With few sequences and heads most SMs
 // would idle, and with sequences of unequal length (the longest taken to be twice the mean)
@@ -33,7 +34,8 @@ int span_chunks(int tokens, int heads, int values, int sequences, bool equal_len
     int chunks = 0;
     for (long long spans = 2; spans <= 64 && mean / spans >= kLeastSpan; ++spans) {
         const long long each = (mean + spans - 1) / spans;
-        const double cost = turns(all * spans) * each * kSpanCost + kJoinCost;
+        const double cost = turns(all * spans) * (each * kSpanCost + kStartCost) + kLaunchCost +
+                            kJoinCost * all * spans;
         if (cost < best) {
             best = cost;
             chunks = static_cast<int>(each);

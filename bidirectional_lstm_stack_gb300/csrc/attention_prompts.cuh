@@ -126,12 +126,13 @@ Layout layout(int values)
     const size_t rest = l.weighted + l.staging + kMaxStages * sizeof(Decays) + kInfos * sizeof(Info) +
                         sizeof(Barriers) + 1024;
     const auto bytes = [&] { return l.stages * l.stage + l.p_buffers * l.p + rest; };
-    l.stages = kMaxStages;
-    l.p_buffers = 2;
-    while (l.stages > 1 && bytes() > 227 * 1024)
-        --l.stages;
-    if (bytes() > 227 * 1024)
-        l.p_buffers = 1;
+    // as many stages as there is room for, then a second P
+    for (int n = 2 * kMaxStages + 1; n > 1; --n) {
+        l.stages = n / 2;
+        l.p_buffers = 1 + n % 2;
+        if (bytes() <= 227 * 1024)
+            break;
+    }
     l.total = bytes();
     return l;
 }
@@ -185,9 +186,23 @@ __device__ __forceinline__ void store_parts(uint8_t *at, int apart, const float 
         *reinterpret_cast<uint4 *>(at + k * apart) = make_uint4(r[0][k], r[1][k], r[2][k], r[3][k]);
 }
 
-// The numbers that N units of 16 bytes stand for.
+// fma2 and mul2 that the compiler may put in any order.
+__device__ __forceinline__ Pair free_fma2(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair free_mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The numbers that N units of 16 bytes stand for, in pairs.
 template <int N>
-__device__ __forceinline__ void load_parts(const uint8_t *at, int apart, float (&f)[8])
+__device__ __forceinline__ void load_parts(const uint8_t *at, int apart, Pair (&f)[4])
 {
 #pragma unroll
     for (int k = N - 1; k >= 0; --k) {
@@ -195,9 +210,28 @@ __device__ __forceinline__ void load_parts(const uint8_t *at, int apart, float (
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = k == N - 1 ? low_float(w[i]) : f[2 * i] + low_float(w[i]);
-            f[2 * i + 1] = k == N - 1 ? high_float(w[i]) : f[2 * i + 1] + high_float(w[i]);
+            const Pair some = make_pair(low_float(w[i]), high_float(w[i]));
+            f[i] = k == N - 1 ? some : add2(f[i], some);
         }
+    }
+}
+
+// Four pairs as three units of 16 bytes: the leading 8 bits of each, those of the rest, and
+// what is left.
+__device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4])
+{
+    const Pair minus = make_pair(-1.0f, -1.0f);
+#pragma unroll
+    for (int k = 0; k < kWeighted; ++k) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = split_pair(f[i]);
+            asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r[i]) : "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)));
+            if (k + 1 < kWeighted)
+                f[i] = free_fma2(make_pair(low_float(r[i]), high_float(r[i])), minus, f[i]);
+        }
+        *reinterpret_cast<uint4 *>(at + k * apart) = make_uint4(r[0], r[1], r[2], r[3]);
     }
 }
 
@@ -249,47 +283,50 @@ __device__ __forceinline__ void load_tile(uint8_t *tile, int apart, const T *fro
     }
 }
 
-// A log decay in log2, as a whole number of 2^-40 (of a chunk's sum the 64 tokens need 15 bits
-// above the point): sums are exact, and take no fp64, which this GPU has little of.
-constexpr float kOne = 1099511627776.0f;
-__device__ __forceinline__ long long fixed_decay(float g)
+// A sum that fp32 alone would round too early, as the fp32 number next to it and the rest
+// (error-free transformation of a sum, Knuth).  This GPU has little fp64.
+struct Sum {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum add(Sum a, Sum b)
 {
-    const float hi = g * 1.44269502f, most = fminf(fmaxf(hi, -kMostDecay), kMostDecay);
-    // (log2 e = 1.44269502 + 1.92596303e-8)
-    const float lo = hi == most ? fmaf(g, 1.92596303e-8f, fmaf(g, 1.44269502f, -hi)) : 0.0f;
-    return __float2ll_rn(most * kOne) + __float2ll_rn(lo * kOne);
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float lo = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float hi = s + lo;
+    return {hi, lo - (hi - s)};
+}
+// A log decay in log2 (log2 e = 1.44269502 + 1.92596303e-8), a NaN left as it is.
+__device__ __forceinline__ Sum log2_decay(float g)
+{
+    const float v = g * 1.44269502f;
+    if (fabsf(v) > kMostDecay)
+        return {v < 0.0f ? -kMostDecay : kMostDecay, 0.0f};
+    return {v, fmaf(g, 1.92596303e-8f, fmaf(g, 1.44269502f, -v))};
 }
 
 // The sums of a chunk's log decays, two tokens a lane; returns the whole sum.
-__device__ __forceinline__ long long sum_decays(Decays &d, Info &info, float g0, float g1, int lane)
+__device__ __forceinline__ Sum sum_decays(Decays &d, Info &info, float g0, float g1, int lane)
 {
-    const long long b = fixed_decay(g1);
-    long long sum = fixed_decay(g0) + b;
-#pragma unroll 1
+    const Sum a = log2_decay(g0), b = log2_decay(g1);
+    Sum sum = add(a, b), none = {0.0f, 0.0f};
+#pragma unroll
     for (int m = 1; m < 32; m *= 2) {
-        const long long other = __shfl_up_sync(0xffffffffu, sum, m);
-        if (lane >= m)
-            sum += other;
+        const Sum other = {__shfl_up_sync(0xffffffffu, sum.hi, m), __shfl_up_sync(0xffffffffu, sum.lo, m)};
+        sum = add(sum, lane >= m ? other : none);
     }
-    const long long end = __shfl_sync(0xffffffffu, sum, 31);
-    // a NaN is one to all tokens behind it
-    const unsigned before = (1u << lane) - 1, nan0 = __ballot_sync(0xffffffffu, g0 != g0),
-                   nan1 = __ballot_sync(0xffffffffu, g1 != g1);
-    const auto poison = [](unsigned any) { return any ? __uint_as_float(0x7fffffffu) : 0.0f; };
-    const float all_of = poison(nan0 | nan1);
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const long long c = k ? sum : sum - b;
-        const float of = poison(((nan0 | nan1) & before) | (nan0 >> lane & 1) | (k & nan1 >> lane));
-        const int i = 2 * lane + k;
-        const float hi = __ll2float_rn(c), lo = __ll2float_rn(c - __float2ll_rn(hi)) / kOne;
-        d.sum[i] = make_float2(hi / kOne + of, lo);
-        d.until[i] = ex2(__ll2float_rn(end - c) / kOne) + all_of;
-        info.since[i] = ex2(hi / kOne) * fmaf(0.6931472f, lo, 1.0f) + of;
-    }
+    Sum before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+    const Sum end = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+    const Sum first = add(lane > 0 ? before : none, a);
+    *reinterpret_cast<float4 *>(&d.sum[2 * lane]) = make_float4(first.hi, first.lo, sum.hi, sum.lo);
+    *reinterpret_cast<float2 *>(&d.until[2 * lane]) =
+        make_float2(ex2((end.hi - first.hi) + (end.lo - first.lo)),
+                    ex2((end.hi - sum.hi) + (end.lo - sum.lo)));
+    *reinterpret_cast<float2 *>(&info.since[2 * lane]) =
+        make_float2(ex2(first.hi) * fmaf(0.6931472f, first.lo, 1.0f),
+                    ex2(sum.hi) * fmaf(0.6931472f, sum.lo, 1.0f));
     *reinterpret_cast<int4 *>(&info.first_bad[4 * lane]) = make_int4(C, C, C, C);
     if (lane == 0)
-        info.all = ex2(__ll2float_rn(end) / kOne) + all_of;
+        info.all = ex2(end.hi + end.lo);
     return end;
 }
 
@@ -335,36 +372,15 @@ __device__ __forceinline__ void store_if(bool there, float *to, float v)
                  : "memory");
 }
 
-// ptx::mbar_wait_bounded in as few instructions as it takes: the kernel's warps all run
-// different code, and what of it exceeds the instruction cache is fetched for every chunk.
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                             unsigned *fault, unsigned code, uint64_t limit_ns)
-{
-    uint64_t start = 0;
-#pragma unroll 1
-    while (!ptx::mbar_try_wait(bar, parity)) {
-        const uint64_t now = ptx::globaltimer();
-        if (start == 0)
-            start = now;
-        if (now - start > limit_ns) {
-            atomicOr(fault, code);
-            *abort = 1;
-        }
-        if (*abort)
-            return false;
-    }
-    return true;
-}
-
 // ---- the kernel ------------------------------------------------------------------------------
 // Thread layout, in warpgroups: two of scores' warps (whose spare places take the two issuing
-// warps and the decays' warp), the output warps, the state warps, the loaders.  With TMA the
+// warps, the decays' warp and the one that asks for copies), the output warps, the state warps, the loaders.  With TMA the
 // loaders have nothing to load and write w v in the state warps' stead; where those are eight,
 // they do it themselves, and the block's threads have 96 registers, not 80 (a state of 64
 // numbers a thread wants 90).
 template <int KP, bool TMA>
 struct Warps {
-    static constexpr int kOutIssue = 2, kStateIssue = 3, kDecay = 6;
+    static constexpr int kOutIssue = 2, kStateIssue = 3, kDecay = 6, kCopy = 7;
     static constexpr int kOut = 8;
     static constexpr int kState = 12, kStates = 4 * (KP / 64);
     static constexpr int kLoad = kState + kStates, kLoads = TMA && KP > 64 ? 0 : kLoaders / 32;
@@ -380,6 +396,9 @@ struct Columns {
                          kState = kUpdate + KP;
     static_assert(kState + Parts<T>::kMid * KP / 2 <= 512, "tensor memory");
 };
+
+// Conditions that keep their code out of the way.
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 // D = the products of parts that matter, over `steps` blocks of 16 along the sum (one more
 // where they are odd: the operands are zeros there); a, b: an operand's descriptor for a part
@@ -506,10 +525,11 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         }
     };
     // where a chunk stands in buffers used in turn
-    const auto parity_of = [](int c, int buffers) { return static_cast<uint32_t>(c / buffers) & 1; };
+    const auto parity_of = [](int c, uint32_t buffers) { return static_cast<uint32_t>(c) / buffers & 1; };
+    const unsigned polls = static_cast<unsigned>(test.wait_limit_ns / ptx::kSuspendedNs) + 1;
     // (by all lanes of a warp)
     const auto wait = [&](uint64_t *b, uint32_t parity, unsigned code) {
-        return __all_sync(0xffffffffu, wait_bounded(b, parity, abort, fault, code, test.wait_limit_ns)) != 0;
+        return __all_sync(0xffffffffu, ptx::mbar_wait_suspended(b, parity, abort, code, polls)) != 0;
     };
     // what all lanes did before is there
     const auto arrive = [&](uint64_t *b) {
@@ -523,60 +543,61 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             return false;
         uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
         const Decays &d = decays[s];
-        int *const first_bad = infos[c % kInfos].first_bad;
+        int *const first_bad = infos[c & (kInfos - 1)].first_bad;
         const int len = TMA ? min(run.end - run.begin - c * C, C) : C;
-        if (TMA && len < C) {
+        if (TMA && rare(len < C)) {
             // rows of other tokens came along: none of their keys joins the state
+#pragma unroll 1
             for (int n = tid; n < l.tile_k / 16; n += kWeighers)
                 if ((n >> 3 & (C - 1)) >= len)
                     reinterpret_cast<uint4 *>(tile - l.tile_k)[n] = make_uint4(0, 0, 0, 0);
         }
+        // A thread takes a unit at a time.  Warps of their own write a half when that of the
+        // chunk before has been multiplied; the states' warps know that both have been, since
+        // they have added the update.
+        constexpr bool kOwn = TMA && W::kLoads;
+        constexpr int kHalf = kSlab / 2, kRows = kWeighers / 8;  // rows of a turn
+        const int part = l.slabs * kHalf;
+        uint8_t *at = tile + tid * 16;
+        uint8_t *to = weighted + tid * 16;
+        int j = tid >> 3;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-            // w v of the chunk before has been multiplied
-            if (c > 0 && !wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter))
+            if (kOwn && c > 0 && !wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter))
                 return false;
-            uint8_t *const to = weighted + half * (l.weighted / 2);
 #pragma unroll 1
-            for (int n0 = tid; n0 < l.slabs * 256; n0 += 2 * kWeighers) {
-                float none = 0.0f;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int n = n0 + m * kWeighers;
-                    if (m > 0 && n >= l.slabs * 256)
-                        break;
-                    const int j = half * 32 + (n >> 3 & 31);
-                    uint8_t *const at = tile + (n >> 8) * kSlab + half * (kSlab / 2) + (n & 255) * 16;
-                    float f[8];
-                    load_parts<P::kIn>(at, l.tile_v, f);
-                    if (TMA && j >= len) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = 0.0f;
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(0, 0, 0, 0);
-                    }
-                    const float w = d.until[j];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        none = fmaf(f[e], 0.0f, none);
-                        f[e] *= w;
-                    }
-                    store_parts<kWeighted>(to + n * 16, l.slabs * (kSlab / 2), f);
-                }
-                if (none != 0.0f) {
+            for (int turn = 0; turn < 32 / kRows; ++turn, j += kRows) {
+                const float until = d.until[j];
 #pragma unroll 1
-                    for (int n = n0; n <= n0 + kWeighers && n < l.slabs * 256; n += kWeighers) {
-                        const int j = half * 32 + (n >> 3 & 31);
-                        not_finite<P::kIn>(tile + (n >> 8) * kSlab + half * (kSlab / 2) + (n & 255) * 16,
-                                           l.tile_v, first_bad + (n >> 8) * 64 + ((n ^ j) & 7) * 8, j);
+                for (int slab = 0; slab < l.slabs; ++slab) {
+                    uint8_t *const from = at + slab * kSlab;
+                    Pair f[4], none = make_pair(0.0f, 0.0f);
+                    load_parts<P::kIn>(from, l.tile_v, f);
+                    if (TMA && rare(j >= len)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            f[i] = none;
+                        *reinterpret_cast<uint4 *>(from) = make_uint4(0, 0, 0, 0);
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        none = free_fma2(f[i], make_pair(0.0f, 0.0f), none);
+                        f[i] = free_mul2(f[i], make_pair(until, until));
+                    }
+                    store_three(to + slab * kHalf, part, f);
+                    const float2 any = split_pair(none);
+                    if (rare(any.x != 0.0f || any.y != 0.0f))
+                        not_finite<P::kIn>(from, l.tile_v, first_bad + slab * 64 + ((tid ^ j) & 7) * 8, j);
                 }
+                at += kRows * kRowBytes;
+                to += kRows * kRowBytes;
             }
+            to += l.weighted / 2 - kHalf;
             ptx::fence_proxy_async_smem();
             arrive(&bar.weighted_full[half]);
         }
         if (lane == 0)
-            ptx::mbar_arrive(&bar.clean[c % kCleans]);
+            ptx::mbar_arrive(&bar.clean[c & (kCleans - 1)]);
         return true;
     };
 
@@ -602,7 +623,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 ptx::tc_fence_after();
                 uint8_t *const row = p_tiles + (c & (l.p_buffers - 1)) * l.p + i * kRowBytes;
                 const int swizzle = (i & 7) << 4;
-                const float2 mine = d.sum[i];
+                const Pair mine = *reinterpret_cast<const Pair *>(&d.sum[i]);
+                const Pair minus = make_pair(-1.0f, -1.0f);
 #pragma unroll 1
                 for (int j0 = 0; j0 < 32; j0 += 16) {
                     uint32_t r[16];
@@ -615,11 +637,13 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
 #pragma unroll
                         for (int e = 0; e < 8; e += 2) {
                             const int j = u * 8 + e;
-                            const float4 other = *reinterpret_cast<const float4 *>(&d.sum[at + j]);
-                            const float one = (mine.x - other.x) + (mine.y - other.y);
-                            const float two = (mine.x - other.z) + (mine.y - other.w);
-                            f[e] = j <= i - at ? __uint_as_float(r[j]) * ex2(one) : 0.0f;
-                            f[e + 1] = j + 1 <= i - at ? __uint_as_float(r[j + 1]) * ex2(two) : 0.0f;
+                            const ulonglong2 other =
+                                *reinterpret_cast<const ulonglong2 *>(&d.sum[at + j]);
+                            const float2 one = split_pair(free_fma2(other.x, minus, mine));
+                            const float2 two = split_pair(free_fma2(other.y, minus, mine));
+                            f[e] = j <= i - at ? __uint_as_float(r[j]) * ex2(one.x + one.y) : 0.0f;
+                            f[e + 1] = j + 1 <= i - at ? __uint_as_float(r[j + 1]) * ex2(two.x + two.y)
+                                                       : 0.0f;
                         }
                         store_parts<P::kMid>(row + (((at / 8 + u) << 4) ^ swizzle), kSlab, f);
                     }
@@ -636,15 +660,16 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         T *const first = p.out<T>(run.begin, head) + v0 + quarter * 32;
         T *const slice = reinterpret_cast<T *>(staging) + quarter * (C * 32);
         const int width = values - quarter * 32;  // of this warp's values
+        const Pair scale = make_pair(p.scale, p.scale);
         for (int c = 0; outputs && c < chunks; ++c) {
-            const int b = c & 1, ib = c % Col::kInters;
+            const int b = c & 1, ib = c & (Col::kInters - 1);
             const bool ok = wait(&bar.inter_full[ib], parity_of(c, Col::kInters), kFaultEpilogue) &&
                             wait(&bar.intra_full[b], parity_of(c, 2), kFaultEpilogue);
             if (!ok || *abort)
                 break;
             ptx::tc_fence_after();
             const int len = min(run.end - run.begin - c * C, C);
-            const Info &info = infos[c % kInfos];
+            const Info &info = infos[c & (kInfos - 1)];
             T *const at = first + static_cast<long long>(c) * C * p.y_stride;
             if (width > 0) {
                 // the first token that has a value in this column which is not finite
@@ -662,14 +687,20 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                     float f[16];
 #pragma unroll
                     for (int e = 0; e < 16; e += 4) {
-                        const float4 since = *reinterpret_cast<const float4 *>(&info.since[e0 + e]);
-                        const float some[4] = {since.x, since.y, since.z, since.w};
+                        const ulonglong2 since = *reinterpret_cast<const ulonglong2 *>(&info.since[e0 + e]);
 #pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            f[e + n] = p.scale * fmaf(__uint_as_float(past[e + n]), some[n],
-                                                      __uint_as_float(r[e + n]));
+                        for (int n = 0; n < 4; n += 2) {
+                            const float2 two = split_pair(free_mul2(
+                                scale, free_fma2(make_pair(__uint_as_float(past[e + n]),
+                                                      __uint_as_float(past[e + n + 1])),
+                                            n == 0 ? since.x : since.y,
+                                            make_pair(__uint_as_float(r[e + n]),
+                                                      __uint_as_float(r[e + n + 1])))));
+                            f[e + n] = two.x;
+                            f[e + n + 1] = two.y;
+                        }
                     }
-                    if (!all_good) {
+                    if (rare(!all_good)) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             f[e] = e0 + e >= bad ? __uint_as_float(0x7fffffffu) : f[e];
@@ -719,14 +750,16 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const int v = quarter * 32 + lane, tid = threadIdx.x - W::kState * 32;
         const bool inside = v < values;
-        float h[64];
+        Pair h[32];  // pairs of keys
         const int some = inside ? p.keys - k0 : 0;  // keys of this lane's h
         {
             const float *from = run.from + k0 * p.values + v;
             const int there = run.from ? some : 0;
 #pragma unroll
-            for (int n = 0; n < 64; ++n) {
-                h[n] = load_if(n < there, from);
+            for (int n = 0; n < 64; n += 2) {
+                const float one = load_if(n < there, from);
+                from += p.values;
+                h[n / 2] = make_pair(one, load_if(n + 1 < there, from));
                 from += p.values;
             }
         }
@@ -739,15 +772,17 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 if (!wait(&bar.update_full, c & 1, kFaultConverter) || *abort)
                     break;
                 ptx::tc_fence_after();
-                const float left = infos[c % kInfos].all;
+                const float all = infos[c & (kInfos - 1)].all;
+                const Pair left = make_pair(all, all);
 #pragma unroll
                 for (int n0 = 0; n0 < 64; n0 += 16) {
                     uint32_t r[16];
                     ptx::tmem_ld_32x32b_x16(tmem + lanes + Col::kUpdate + k0 + n0, r);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        h[n0 + n] = fmaf(h[n0 + n], left, __uint_as_float(r[n]));
+                    for (int n = 0; n < 16; n += 2)
+                        h[(n0 + n) / 2] = free_fma2(h[(n0 + n) / 2], left,
+                                               make_pair(__uint_as_float(r[n]), __uint_as_float(r[n + 1])));
                 }
                 ptx::tc_fence_before();
                 arrive(&bar.update_free);
@@ -763,7 +798,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 continue;
             if (c >= 0) {
                 // S of chunk c has been multiplied
-                if (!wait(&bar.inter_full[c % Col::kInters], parity_of(c, Col::kInters),
+                if (!wait(&bar.inter_full[c & (Col::kInters - 1)], parity_of(c, Col::kInters),
                           kFaultConverter) || *abort)
                     break;
                 ptx::tc_fence_after();
@@ -774,7 +809,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     uint32_t parts[P::kMid];
-                    split_pair_parts<P::kMid>(h[2 * (n0 + n)], h[2 * (n0 + n) + 1], parts);
+                    const float2 two = split_pair(h[n0 + n]);
+                    split_pair_parts<P::kMid>(two.x, two.y, parts);
 #pragma unroll
                     for (int part = 0; part < P::kMid; ++part)
                         r[part][n] = parts[part];
@@ -792,7 +828,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             float *to = run.to + k0 * p.values + v;
 #pragma unroll
             for (int n = 0; n < 64; ++n) {
-                store_if(n < some, to, h[n]);
+                const float2 two = split_pair(h[n / 2]);
+                store_if(n < some, to, n % 2 ? two.y : two.x);
                 to += p.values;
             }
         }
@@ -840,7 +877,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 if (of >= 0) {
                     // (w v is there: what is not finite has left V's tile)
                     if (!wait(&bar.p_full[of & 1], parity_of(of, 2), kFaultMma) ||
-                        !wait(&bar.clean[of % kCleans], parity_of(of, kCleans), kFaultMma))
+                        !wait(&bar.clean[of & (kCleans - 1)], parity_of(of, kCleans), kFaultMma))
                         break;
                     ptx::tc_fence_after();
                     const uint64_t p_desc = p_descs + (of & (l.p_buffers - 1)) * (l.p >> 4);
@@ -867,7 +904,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                          !wait(&bar.y_free[(c - 1) & 1], parity_of(c - 1, 2), kFaultMma)))
                         break;
                     ptx::tc_fence_after();
-                    const uint32_t inter = tmem + Col::kInter + C * (c % Col::kInters);
+                    const uint32_t inter = tmem + Col::kInter + C * (c & (Col::kInters - 1));
                     multiply<P::kMid, P::kIn>(
                         leader, steps,
                         [&](int i, int k) { return tmem + Col::kState + i * (KP / 2) + k * 8; },
@@ -876,7 +913,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                             ptx::mma_f16_tmem_a(inter, a, b_desc, idesc, more);
                         });
                     if (leader) {
-                        ptx::mma_commit(&bar.inter_full[c % Col::kInters]);
+                        ptx::mma_commit(&bar.inter_full[c & (Col::kInters - 1)]);
                         if (!lag)
                             ptx::mma_commit(&bar.empty[s]);
                     }
@@ -943,51 +980,50 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             return t < run.end ? __ldg(p.decay + t * p.decay_stride + head) : 0.0f;
         };
         float g0 = decay_at(0, 2 * lane), g1 = decay_at(0, 2 * lane + 1);
-        long long total = 0;
-        bool nan = false;
-        int s = 0, issued = 0;
+        Sum total = {0.0f, 0.0f};
+        int s = 0;
         uint32_t turn = 0;
         for (int c = 0; c < chunks; ++c, advance(s, turn)) {
             const float n0 = decay_at(c + 1, 2 * lane), n1 = decay_at(c + 1, 2 * lane + 1);
             if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
                 break;
-            // (failure test: nothing is loaded, so the waits for it run out)
-            if (TMA && !test.withhold) {
-                if (lane == 0) {
-                    uint8_t *to = smem + s * l.stage;
-                    const int t0 = run.begin + c * C;
-                    ptx::mbar_arrive_expect_tx(&bar.full[s], (outputs ? 2 : 1) * l.tile_k + l.tile_v);
-#pragma unroll 1
-                    for (int which = outputs ? 0 : 1; which < 3; ++which) {
-                        const int share = which == 0 ? p.q.share : which == 1 ? p.k.share : p.v.share;
-                        const int slabs = which == 2 ? l.slabs : KP / 64;
-#pragma unroll 1
-                        for (int slab = 0; slab < slabs; ++slab)
-                            ptx::tma_load_3d(to + which * l.tile_k + slab * kSlab, &maps.of[which],
-                                             &bar.full[s], (which == 2 ? v0 : 0) + slab * 64,
-                                             head / share, t0);
-                    }
-                }
-                ++issued;
-            }
-            total += sum_decays(decays[s], infos[c % kInfos], g0, g1, lane);
-            // (what has left nothing leaves nothing; the sum stays in range)
-            total = max(total, -(1ll << 52));
-            nan |= g0 != g0 || g1 != g1;
+            total = add(total, sum_decays(decays[s], infos[c & (kInfos - 1)], g0, g1, lane));
             arrive(&bar.full[s]);
             g0 = n0;
             g1 = n1;
         }
-        if (TMA) {
-            // every load has landed before the CTA's shared memory goes away
-            for (int c = max(issued - l.stages, 0); c < issued; ++c)
-                ptx::mbar_wait_drain(&bar.full[c % l.stages], c / l.stages & 1, fault,
-                                     kDefaultWaitLimitNs);
-        }
-        nan = __any_sync(0xffffffffu, nan);
         if (!outputs && lane == 0 && blockIdx.z == 0)
-            *spans.left_of(p, blockIdx.x, head) =
-                nan ? __uint_as_float(0x7fffffffu) : ex2(__ll2float_rn(total) / kOne);
+            *spans.left_of(p, blockIdx.x, head) = ex2(total.hi + total.lo);
+    } else if (TMA && warp == W::kCopy && !test.withhold) {  // (failure test: nothing is loaded, so the waits for it run out)
+        // ---- rows by TMA ----
+        const int q_head = head / p.q.share, k_head = head / p.k.share, v_head = head / p.v.share;
+        const uint32_t bytes = (outputs ? 2 : 1) * l.tile_k + l.tile_v;
+        int s = 0, c = 0;
+        uint32_t turn = 0;
+        for (; c < chunks; ++c, advance(s, turn)) {
+            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
+                break;
+            if (lane == 0) {
+                uint64_t *const full = &bar.full[s];
+                uint8_t *const to = smem + s * l.stage;
+                const int t0 = run.begin + c * C;
+                ptx::mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+                for (int slab = 0; slab < KP / 64; ++slab) {
+                    if (outputs)
+                        ptx::tma_load_3d(to + slab * kSlab, &maps.of[0], full, slab * 64, q_head, t0);
+                    ptx::tma_load_3d(to + l.tile_k + slab * kSlab, &maps.of[1], full, slab * 64, k_head, t0);
+                }
+#pragma unroll
+                for (int slab = 0; slab < 2; ++slab)
+                    if (slab < l.slabs)
+                        ptx::tma_load_3d(to + 2 * l.tile_k + slab * kSlab, &maps.of[2], full,
+                                         v0 + slab * 64, v_head, t0);
+            }
+        }
+        // every load has landed before the CTA's shared memory goes away
+        for (int n = max(c - l.stages, 0); n < c; ++n)
+            ptx::mbar_wait_drain(&bar.full[n % l.stages], n / l.stages & 1, fault, kDefaultWaitLimitNs);
     } else if (TMA && warp >= W::kLoad) {
         // ---- w v ----
         int s = 0;
@@ -1032,6 +1068,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
 
     ptx::tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort)
+        atomicOr(fault, static_cast<unsigned>(*abort));
     if (warp == W::kOutIssue) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);

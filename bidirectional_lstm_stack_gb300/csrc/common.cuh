@@ -259,6 +259,33 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// Waits for the phase with `parity`, or until *abort becomes non-zero; false (after joining
+// `code` to *abort) when `polls` polls, each suspended for up to kSuspendedNs, have not met it.
+// Of as few instructions as it takes: in a kernel whose warps all run different code its
+// copies would fill the instruction cache, and each miss there costs more than the wait.
+constexpr unsigned kSuspendedNs = 1000;
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity,
+                                                    volatile int *abort, unsigned code,
+                                                    unsigned polls)
+{
+#pragma unroll 1
+    while (true) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendedNs)
+                     : "memory");
+        if (__builtin_expect(ok, 1))
+            return true;
+        if (*abort || --polls == 0) {
+            *abort |= code;
+            return false;
+        }
+    }
+}
+
 // ---- TMA ----
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int x, int y)
