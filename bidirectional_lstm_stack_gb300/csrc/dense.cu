@@ -21,8 +21,7 @@
 // 16-byte pitches of 16-bit operands that TMA cannot read in place, is a kernel before.
 #include <mutex>
 
-#include "lstm_layers.h"
-#include "ops.cuh"
+#include "dense.cuh"
 
 namespace lstm {
 namespace {
@@ -31,10 +30,11 @@ constexpr int BM = 128;
 constexpr int BK = 64;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int kFewRows = 64;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 constexpr int kParts = 3;      // of an fp32 number
 constexpr int kProducts = 6;   // of two of them
-constexpr int THREADS = 192;
+constexpr int EPILOGUE_WARPS = 8;
+constexpr int THREADS = 64 + EPILOGUE_WARPS * 32;
 constexpr int PRODUCER_WARP = 0, MMA_WARP = 1;
 constexpr int SLICE_BYTES = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out
 
@@ -56,31 +56,14 @@ struct DenseArgs {
 __host__ __device__ constexpr int part_of_x(int p) { return p == 0 ? 2 : p == 1 || p == 3 ? 1 : 0; }
 __host__ __device__ constexpr int part_of_w(int p) { return p == 2 ? 2 : p == 1 || p == 4 ? 1 : 0; }
 
-__device__ __forceinline__ float activate(int kind, float v)
-{
-    switch (kind) {
-    case LSTM_ACT_RELU:
-        return v < 0.0f ? 0.0f : v;  // (NaN stays)
-    case LSTM_ACT_GELU:
-        return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case LSTM_ACT_GELU_TANH:
-        return 0.5f * v * (1.0f + tanhf(0.7978845608028654f * fmaf(0.044715f * v * v, v, v)));
-    case LSTM_ACT_SILU:
-        return v / (1.0f + expf(-v));
-    default:
-        return v;
-    }
-}
-
 template <int BN_, bool SWAP_>
 struct Shape {
     static constexpr int BN = BN_;
     static constexpr bool SWAP = SWAP_;
     static constexpr int B_BYTES = BN * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // few rows: two CTAs an SM
-    static constexpr int DATA_BYTES = SWAP ? 104 * 1024 : 224 * 1024;
-    static constexpr int OUT_BYTES = SWAP ? 0 : 4 * 2 * SLICE_BYTES;
+    static constexpr int DATA_BYTES = 224 * 1024;
+    static constexpr int OUT_BYTES = SWAP ? 0 : EPILOGUE_WARPS * SLICE_BYTES;
     static constexpr int FIT = (DATA_BYTES - OUT_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -88,7 +71,9 @@ struct Shape {
     static constexpr int TMEM_COLS = ACCS * BN < 32 ? 32 : ACCS * BN;
     static constexpr int CW = BN < 32 ? BN : 32;  // columns read at a time
     static constexpr size_t SMEM_BYTES = RING_BYTES + OUT_BYTES + 256 + 1024;
-    static_assert(STAGES >= 4 && BN * BM * 4 <= RING_BYTES, "ring");
+    // a tile's sums on their way to the other CTAs of a cluster, rows of y one after another
+    static constexpr int SUM_ROWS = SWAP ? BN : BM, SUM_COLS = SWAP ? BM : BN, SUM_PITCH = SUM_COLS + 4;
+    static_assert(STAGES >= 4 && SUM_ROWS * SUM_PITCH * 4 <= RING_BYTES, "ring");
     static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
 };
 
@@ -107,7 +92,7 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float (&f)[N])
 }
 
 template <class S, typename T>
-__global__ void __launch_bounds__(THREADS, S::SWAP ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, 1)
 dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
              const __grid_constant__ CUtensorMap y_map, const DenseArgs p, uint32_t idesc,
              long long tiles, int tiles_m, unsigned *fault, KernelTest test)
@@ -133,7 +118,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(&acc_full[a], 1);
-            ptx::mbar_init(&acc_empty[a], 128);
+            ptx::mbar_init(&acc_empty[a], EPILOGUE_WARPS * 32);
         }
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -232,13 +217,15 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
             }
         }
     } else {
-        // epilogue: this warp reads the tensor-memory lanes (rows of the tile) 32q..32q+31
-        const int q = warp & 3;
+        // epilogue: this warp reads the tensor-memory lanes (rows of the tile) 32q..32q+31, of
+        // every other slice of columns
+        const int q = warp & 3, turn = (warp - 2) >> 2;
+        constexpr int TURNS = EPILOGUE_WARPS / 4;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        uint8_t *slices = out_slices + q * 2 * SLICE_BYTES;
+        uint8_t *const buf = out_slices + (warp - 2) * SLICE_BYTES;
         T *const y = static_cast<T *>(p.y);
         const T *const residual = static_cast<const T *>(p.residual);
-        int count = 0, sent = 0;
+        int count = 0;
         for (long long t = first; t < tiles; t += step, ++count) {
             int m0, n0;
             place(t, &m0, &n0);
@@ -249,51 +236,79 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
             const bool ok = __all_sync(0xffffffffu, got) && !*abort_flag;
             ptx::tc_fence_after();
             const uint32_t acc = tmem + lane_base + a * BN;
-            float *const sums = reinterpret_cast<float *>(smem);  // [BN][BM], over the ring
             if (p.split > 1) {
-                // (every load of the ring has landed and been multiplied)
+                // (every load of the ring has landed and been multiplied: the sums take its place)
+                float *const sums = reinterpret_cast<float *>(smem);
                 if (ok) {
 #pragma unroll 1
-                    for (int c = 0; c < BN; c += CW) {
+                    for (int c = turn * CW; c < BN; c += TURNS * CW) {
                         float f[CW];
                         read_columns<CW>(acc + c, f);
+                        if constexpr (S::SWAP) {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            sums[(c + j) * BM + q * 32 + lane] = f[j];
+                            for (int j = 0; j < CW; ++j)
+                                sums[(c + j) * S::SUM_PITCH + q * 32 + lane] = f[j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < CW; j += 4)
+                                *reinterpret_cast<float4 *>(sums + (q * 32 + lane) * S::SUM_PITCH + c + j) =
+                                    make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                        }
                     }
                 }
                 ptx::cluster_arrive_release();
                 ptx::cluster_wait_acquire();
+                if (!ok)
+                    break;
+                // each CTA joins its share of the tile, four numbers of a row at a time, the
+                // parts in their order
+                constexpr int QUADS = S::SUM_COLS / 4, ALL = S::SUM_ROWS * QUADS;
+                const int high = S::SWAP ? p.rows - n0 : p.rows - m0;
+                const int wide = S::SWAP ? p.out - m0 : p.out - n0;
+                const int row0 = S::SWAP ? n0 : m0, col0 = S::SWAP ? m0 : n0;
+                const uint32_t base = ptx::smem_u32(sums);
+                for (int u = part * (ALL / p.split) + static_cast<int>(threadIdx.x) - 64;
+                     u < (part + 1) * (ALL / p.split); u += EPILOGUE_WARPS * 32) {
+                    const int row = u / QUADS, col = u % QUADS * 4;
+                    if (row >= high || col >= wide)
+                        continue;
+                    const uint32_t at = base + (row * S::SUM_PITCH + col) * 4;
+                    float f[4] = {};
+#pragma unroll 4
+                    for (int k = 0; k < p.split; ++k) {
+                        float v[4];
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                                     : "r"(ptx::map_to_rank(at, k)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            f[j] += v[j];
+                    }
+                    const long long r = row0 + row;
+                    const int n = col0 + col, there = min(4, wide - col);
+                    T *const to = y + r * p.y_stride + n;
+                    const T *const res = residual ? residual + r * p.residual_stride + n : nullptr;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < there) {
+                            float v = activate(p.activation, f[j] + (p.bias ? __ldg(p.bias + n + j) : 0.0f));
+                            if (res)
+                                v += Elem<T>::get(res[j]);
+                            to[j] = Elem<T>::put(v);
+                        }
+                }
+                ptx::tc_fence_before();
+                continue;
             }
             if (!ok)
                 break;
-            // columns c0 .. c0 + CW - 1 of the accumulator, over all parts of K
-            const auto fetch = [&](int c0, float (&f)[CW]) {
-                if (p.split == 1) {
-                    read_columns<CW>(acc + c0, f);
-                    return;
-                }
-#pragma unroll
-                for (int j = 0; j < CW; ++j)
-                    f[j] = 0.0f;
-                for (int k = 0; k < p.split; ++k) {
-                    const uint32_t from =
-                        ptx::map_to_rank(ptx::smem_u32(sums + c0 * BM + q * 32 + lane), k);
-#pragma unroll
-                    for (int j = 0; j < CW; ++j) {
-                        float v;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + j * BM * 4));
-                        f[j] += v;
-                    }
-                }
-            };
             if constexpr (S::SWAP) {
                 // a lane's row of the tile is one column of y, its columns are rows of y
                 const int n = m0 + q * 32 + lane;
                 const float bias = p.bias && n < p.out ? __ldg(p.bias + n) : 0.0f;
-                for (int c0 = part * CW; c0 < BN && n0 + c0 < p.rows; c0 += p.split * CW) {
+                for (int c0 = turn * CW; c0 < BN && n0 + c0 < p.rows; c0 += TURNS * CW) {
                     float f[CW];
-                    fetch(c0, f);
+                    read_columns<CW>(acc + c0, f);
 #pragma unroll
                     for (int j = 0; j < CW; ++j) {
                         const long long r = n0 + c0 + j;
@@ -307,18 +322,46 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 }
             } else {
                 constexpr int V = Elem<T>::kVector;
-                const long long r = m0 + q * 32 + lane;
-                // slices of 128 bytes of a row
+                const int r0 = m0 + q * 32;
+                const long long r = r0 + lane;
+                // slices of 128 bytes of a row; 16-byte unit u of row r lies at u ^ (r % 8)
                 constexpr int WIDE = 128 / static_cast<int>(sizeof(T));
-                for (int c0 = part * WIDE; c0 < BN && n0 + c0 < p.out; c0 += p.split * WIDE, ++sent) {
-                    uint8_t *buf = slices + (sent & 1) * SLICE_BYTES;
+                constexpr int TOGETHER = 16;  // numbers a lane has in flight, of WIDE
+                const auto in_slice = [&](int row, int col) {
+                    return reinterpret_cast<T *>(buf + row * 128 + (((col / V) ^ (row & 7)) << 4)) + col % V;
+                };
+                const int high = min(32, p.rows - r0);
+                for (int c0 = turn * WIDE; c0 < BN && n0 + c0 < p.out; c0 += TURNS * WIDE) {
+                    // the store that last used this buffer has read it
+                    if (p.store_boxes) {
+                        if (lane == 0)
+                            ptx::bulk_wait_group_read<0>();
+                        __syncwarp();
+                    }
+                    const int wide = min(WIDE, p.out - (n0 + c0));
+                    if (residual && !p.vectors) {
+                        // row by row, each as its neighbours in memory
+                        const T *from = residual + r0 * p.residual_stride + n0 + c0;
+#pragma unroll 1
+                        for (int k0 = 0; k0 < WIDE; k0 += TOGETHER) {
+                            T v[TOGETHER];
+#pragma unroll
+                            for (int k = 0; k < TOGETHER; ++k) {
+                                const int row = (k0 + k) / (WIDE / 32), col = (k0 + k) % (WIDE / 32) * 32 + lane;
+                                if (row < high && col < wide)
+                                    v[k] = from[row * p.residual_stride + col];
+                            }
+#pragma unroll
+                            for (int k = 0; k < TOGETHER; ++k)
+                                *in_slice((k0 + k) / (WIDE / 32), (k0 + k) % (WIDE / 32) * 32 + lane) = v[k];
+                        }
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int h = 0; h < WIDE; h += CW) {
                         float f[CW];
-                        fetch(c0 + h, f);
+                        read_columns<CW>(acc + c0 + h, f);
                         const int n = n0 + c0 + h;
-                        const T *res = residual ? residual + r * p.residual_stride + n : nullptr;
-                        const bool whole = n + CW <= p.out;
                         if (p.bias) {
 #pragma unroll
                             for (int j = 0; j < CW; ++j)
@@ -329,55 +372,54 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                             for (int j = 0; j < CW; ++j)
                                 f[j] = activate(p.activation, f[j]);
                         }
-                        if (res && r < p.rows) {
-                            if (whole && p.vectors) {
-#pragma unroll
-                                for (int j = 0; j < CW; j += V) {
-                                    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V> *>(res + j);
-#pragma unroll
-                                    for (int i = 0; i < V; ++i)
-                                        f[j + i] += Elem<T>::get(v.v[i]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < CW; ++j)
-                                    if (n + j < p.out)
-                                        f[j] += Elem<T>::get(res[j]);
-                            }
-                        }
-                        if (p.store_boxes) {
-                            if (h == 0) {
-                                // the store that last used this buffer has read it
-                                if (lane == 0)
-                                    ptx::bulk_wait_group_read<1>();
-                                __syncwarp();
-                            }
-                            // 16-byte unit u of the row goes to unit u ^ (row % 8)
+                        if (residual) {
+                            const T *res = residual + r * p.residual_stride + n;
 #pragma unroll
                             for (int j = 0; j < CW; j += V) {
-                                float some[V];
+                                Pack<T, V> v = {};
+                                if (!p.vectors)
+                                    v = *reinterpret_cast<const Pack<T, V> *>(in_slice(lane, h + j));
+                                else if (r < p.rows && n + j < p.out)
+                                    v = *reinterpret_cast<const Pack<T, V> *>(res + j);
 #pragma unroll
                                 for (int i = 0; i < V; ++i)
-                                    some[i] = f[j + i];
-                                const int unit = (h + j) / V;
-                                *reinterpret_cast<Pack<T, V> *>(
-                                    buf + lane * 128 + ((unit ^ (lane & 7)) << 4)) = pack<T, V>(some);
+                                    f[j + i] += Elem<T>::get(v.v[i]);
                             }
-                        } else if (r < p.rows) {
+                        }
 #pragma unroll
-                            for (int j = 0; j < CW; ++j)
-                                if (n + j < p.out)
-                                    y[r * p.y_stride + n + j] = Elem<T>::put(f[j]);
+                        for (int j = 0; j < CW; j += V) {
+                            float some[V];
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                some[i] = f[j + i];
+                            *reinterpret_cast<Pack<T, V> *>(in_slice(lane, h + j)) = pack<T, V>(some);
                         }
                     }
                     if (p.store_boxes) {
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            if (m0 + q * 32 < p.rows)
-                                ptx::tma_store_2d(&y_map, buf, n0 + c0, m0 + q * 32);
+                            if (r0 < p.rows)
+                                ptx::tma_store_2d(&y_map, buf, n0 + c0, r0);
                             ptx::bulk_commit_group();
                         }
+                    } else {
+                        __syncwarp();
+                        T *to = y + r0 * p.y_stride + n0 + c0;
+#pragma unroll 1
+                        for (int k0 = 0; k0 < WIDE; k0 += TOGETHER) {
+                            T v[TOGETHER];
+#pragma unroll
+                            for (int k = 0; k < TOGETHER; ++k)
+                                v[k] = *in_slice((k0 + k) / (WIDE / 32), (k0 + k) % (WIDE / 32) * 32 + lane);
+#pragma unroll
+                            for (int k = 0; k < TOGETHER; ++k) {
+                                const int row = (k0 + k) / (WIDE / 32), col = (k0 + k) % (WIDE / 32) * 32 + lane;
+                                if (row < high && col < wide)
+                                    to[row * p.y_stride + col] = v[k];
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }
@@ -560,11 +602,12 @@ Plan make_plan(int rows, int in, int out, int products)
     } else {
         const long long tall = (rows + BM - 1LL) / BM;
         r.width = 256;
-        while (r.width > 64 && tall * ((out + r.width - 1LL) / r.width) < 152)
+        while (r.width > 64 && tall * ((out + r.width - 1LL) / r.width) < 76)
             r.width /= 2;
         tiles = tall * ((out + r.width - 1LL) / r.width);
     }
-    while (r.split < 8 && tiles * r.split < 152 && kblocks >= 8 * r.split)
+    // (one CTA an SM, whose ring is deep enough to keep its share of the memory busy)
+    while (r.split < 8 && tiles * r.split * 2 <= 152 && kblocks >= 8 * r.split)
         r.split *= 2;
     return r;
 }
@@ -608,7 +651,7 @@ using namespace lstm;
 extern "C" size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w,
                                        long long w_stride, int dtype, int rows, int in, int out)
 {
-    if (rows <= 0 || in <= 0 || out <= 0)
+    if (rows <= kFewestRows || in <= 0 || out <= 0)
         return 0;
     return Operand(x, x_stride, dtype, rows, in).bytes + Operand(w, w_stride, dtype, out, in).bytes;
 }
@@ -643,6 +686,14 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
         return st;
     if (rows == 0)
         return LSTM_OK;
+    if (rows <= kFewestRows) {
+        DeviceGuard guard(device);
+        if (!guard.ok)
+            return fail(LSTM_E_CUDA, "cannot make device %d current", device);
+        return launch_dense_few({x, w, bias, residual, y, x_stride, w_stride, residual_stride,
+                                 y_stride, rows, in, out, activation}, dtype,
+                                static_cast<cudaStream_t>(stream));
+    }
     const Operand ox(x, x_stride, dtype, rows, in), ow(w, w_stride, dtype, out, in);
     if (ox.bytes + ow.bytes > 0 && !workspace)
         return fail(LSTM_E_INVALID, "%s: workspace is null", what);
@@ -682,7 +733,9 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
         return st;
     DenseArgs p = {bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
                    dtype == LSTM_F32 ? kProducts : 1, 1, false, false, 1};
-    p.vectors = !residual || rows_aligned(residual, rows > 1 ? residual_stride : 0, size);
+    // (whole vectors: what lies behind a row's last numbers is not read)
+    p.vectors = residual && rows_aligned(residual, rows > 1 ? residual_stride : 0, size) &&
+                out * size % 16 == 0;
     p.store_boxes = !plan.swap && rows_aligned(y, y_stride, size);
     if (p.store_boxes &&
         (st = encode_box_map(&y_map, map_type(dtype), y, rows, out, y_stride * size, 32)))

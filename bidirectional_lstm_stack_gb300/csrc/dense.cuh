@@ -1,0 +1,45 @@
+// What the files of the dense product share.
+#pragma once
+
+#include "lstm_layers.h"
+#include "ops.cuh"
+
+namespace lstm {
+
+// Up to here rows go without the tensor cores (dense_few.cu).
+constexpr int kFewestRows = 3;
+
+struct FewArgs {
+    const void *x, *w;
+    const float *bias;
+    const void *residual;
+    void *y;
+    long long x_stride, w_stride, residual_stride, y_stride;
+    int rows, in, out;
+    int activation;
+};
+int launch_dense_few(const FewArgs &p, int dtype, cudaStream_t stream);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float activate(int kind, float v)
+{
+    switch (kind) {
+    case LSTM_ACT_RELU:
+        return v < 0.0f ? 0.0f : v;  // (NaN stays)
+    case LSTM_ACT_GELU:
+        return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case LSTM_ACT_GELU_TANH: {
+        // (1 + tanh z) / 2 = 1 / (1 + e^-2z): an exponential and a quotient, where tanhf takes
+        // some forty instructions; an infinite z of -v gives -0
+        const float z = 0.7978845608028654f * fmaf(0.044715f * v * v, v, v);
+        return v * reciprocal(1.0f + ex2(-2.0f * kLog2e * z));
+    }
+    case LSTM_ACT_SILU:
+        return silu(v);
+    default:
+        return v;
+    }
+}
+#endif
+
+}  // namespace lstm
