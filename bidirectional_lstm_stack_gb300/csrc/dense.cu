@@ -148,73 +148,88 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         *m = (static_cast<int>(g) * p.group + static_cast<int>(in_group % tall)) * BM;
         *n = static_cast<int>(in_group / tall) * BN;
     };
-    long long issued = 0;
+    int issued = 0;  // K blocks, as far as they matter at the end: the last STAGES
     int committed = 0;
+    // the ring's next stage, and the parity of its turn (no divisions: a K block takes the
+    // tensor core some 260 to 530 cycles, and one thread has to keep up)
+    int s = 0;
+    uint32_t turn = 0;
+    const auto advance = [&] {
+        if (++s == STAGES) {
+            s = 0;
+            turn ^= 1;
+        }
+    };
 
     if (warp == PRODUCER_WARP) {
         // failure test (`withhold`): nothing is loaded, so the waits for it run out
         if (lane == 0 && !test.withhold) {
             const int a_rows = S::SWAP ? p.out : p.rows, b_rows = S::SWAP ? p.rows : p.out;
-            for (long long t = first; t < tiles && !*abort_flag; t += step) {
+            bool ok = true;
+            for (long long t = first; t < tiles && ok && !*abort_flag; t += step) {
                 int m0, n0;
                 place(t, &m0, &n0);
-                bool ok = true;
-                for (int kb = kb_begin; kb < kb_end; ++kb, ++issued) {
-                    const int s = static_cast<int>(issued % STAGES);
-                    const uint32_t n = static_cast<uint32_t>(issued / STAGES);
-                    if (n > 0 && !ptx::mbar_wait_bounded(&empty[s], (n - 1) & 1, abort_flag, fault,
-                                                         kFaultProducer, test.wait_limit_ns)) {
+                int product = kb_begin / kblocks, k = kb_begin - product * kblocks;
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
+                    // (a stage's first use finds it free)
+                    if (!ptx::mbar_wait_bounded(&empty[s], turn ^ 1, abort_flag, fault,
+                                                kFaultProducer, test.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
-                    const int product = kb / kblocks, k0 = (kb - product * kblocks) * BK;
-                    int ax = 0, bx = 0;  // rows of the parts before these
-                    if (p.products > 1) {
-                        ax = (S::SWAP ? part_of_w(product) : part_of_x(product)) * a_rows;
-                        bx = (S::SWAP ? part_of_x(product) : part_of_w(product)) * b_rows;
+                    int ax = m0, bx = n0;
+                    if (p.products > 1) {  // behind the rows of the parts before these
+                        ax += (S::SWAP ? part_of_w(product) : part_of_x(product)) * a_rows;
+                        bx += (S::SWAP ? part_of_x(product) : part_of_w(product)) * b_rows;
                     }
                     uint8_t *st = smem + s * S::STAGE_BYTES;
                     ptx::mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
-                    ptx::tma_load_2d(st, &a_map, &full[s], k0, ax + m0);
-                    ptx::tma_load_2d(st + A_BYTES, &b_map, &full[s], k0, bx + n0);
+                    ptx::tma_load_2d(st, &a_map, &full[s], k * BK, ax);
+                    ptx::tma_load_2d(st + A_BYTES, &b_map, &full[s], k * BK, bx);
+                    if (++k == kblocks) {
+                        k = 0;
+                        ++product;
+                    }
+                    if (issued < STAGES)
+                        ++issued;
+                    advance();
                 }
-                if (!ok)
-                    break;
             }
         }
     } else if (warp == MMA_WARP) {
-        if (lane == 0) {
-            long long kbi = 0;
-            for (long long t = first; t < tiles && !*abort_flag; t += step) {
-                const int a = committed % S::ACCS;
-                const uint32_t use = static_cast<uint32_t>(committed / S::ACCS);
-                if (use > 0 && !ptx::mbar_wait_bounded(&acc_empty[a], (use - 1) & 1, abort_flag,
-                                                       fault, kFaultMma, test.wait_limit_ns))
+        const bool leader = ptx::elect_one();
+        const uint64_t a_desc = ptx::sw128_desc(ptx::smem_u32(smem));
+        for (long long t = first; t < tiles && !*abort_flag; t += step) {
+            const int a = committed % S::ACCS;
+            const uint32_t use = static_cast<uint32_t>(committed / S::ACCS);
+            bool ok = use == 0 || ptx::mbar_wait_bounded(&acc_empty[a], (use - 1) & 1, abort_flag, fault,
+                                                         kFaultMma, test.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            ptx::tc_fence_after();
+            const uint32_t d = tmem + a * BN;
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+                ok = ptx::mbar_wait_bounded(&full[s], turn, abort_flag, fault, kFaultMma,
+                                            test.wait_limit_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
                 ptx::tc_fence_after();
-                const uint32_t d = tmem + a * BN;
-                bool ok = true;
-                for (int kb = kb_begin; kb < kb_end; ++kb, ++kbi) {
-                    const int s = static_cast<int>(kbi % STAGES);
-                    if (!ptx::mbar_wait_bounded(&full[s], (kbi / STAGES) & 1, abort_flag, fault,
-                                                kFaultMma, test.wait_limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t at = ptx::smem_u32(smem + s * S::STAGE_BYTES);
+                if (leader) {
+                    const uint64_t at = a_desc + s * (S::STAGE_BYTES >> 4);
 #pragma unroll
                     for (int j = 0; j < BK / 16; ++j)
-                        ptx::mma_f16(d, ptx::sw128_desc(at + 32 * j),
-                                     ptx::sw128_desc(at + A_BYTES + 32 * j), idesc,
+                        ptx::mma_f16(d, at + 2 * j, at + (A_BYTES >> 4) + 2 * j, idesc,
                                      kb != kb_begin || j != 0);
                     ptx::mma_commit(&empty[s]);
                 }
-                ptx::mma_commit(&acc_full[a]);  // also when stopping: frees the epilogue
-                ++committed;
-                if (!ok)
-                    break;
+                advance();
             }
+            if (leader)
+                ptx::mma_commit(&acc_full[a]);  // also when stopping: frees the epilogue
+            ++committed;
+            if (!ok)
+                break;
         }
     } else {
         // epilogue: this warp reads the tensor-memory lanes (rows of the tile) 32q..32q+31, of
@@ -446,8 +461,13 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
     __syncthreads();
     if (warp == PRODUCER_WARP && lane == 0) {
         // every load has landed before the CTA's shared memory goes away
-        for (long long k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
-            ptx::mbar_wait_drain(&full[k % STAGES], (k / STAGES) & 1, fault, kDefaultWaitLimitNs);
+        for (; issued > 0; --issued) {
+            if (s == 0) {
+                s = STAGES;
+                turn ^= 1;
+            }
+            ptx::mbar_wait_drain(&full[--s], turn, fault, kDefaultWaitLimitNs);
+        }
     }
     if (warp == MMA_WARP) {
         if (lane == 0) {
