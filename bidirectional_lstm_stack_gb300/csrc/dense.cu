@@ -56,11 +56,13 @@ struct DenseArgs {
 __host__ __device__ constexpr int part_of_x(int p) { return p == 0 ? 2 : p == 1 || p == 3 ? 1 : 0; }
 __host__ __device__ constexpr int part_of_w(int p) { return p == 2 ? 2 : p == 1 || p == 4 ? 1 : 0; }
 
-template <int BN_, bool SWAP_>
+template <int BN_, bool SWAP_, bool PAIR_ = false>
 struct Shape {
     static constexpr int BN = BN_;
-    static constexpr bool SWAP = SWAP_;
-    static constexpr int B_BYTES = BN * BK * 2;
+    static constexpr bool SWAP = SWAP_, PAIR = PAIR_;
+    static constexpr int CTAS = PAIR ? 2 : 1;  // of a tile, 128 lanes of M each
+    static constexpr int B_ROWS = BN / CTAS;
+    static constexpr int B_BYTES = B_ROWS * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int DATA_BYTES = 224 * 1024;
     static constexpr int OUT_BYTES = SWAP ? 0 : EPILOGUE_WARPS * SLICE_BYTES;
@@ -118,7 +120,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(&acc_full[a], 1);
-            ptx::mbar_init(&acc_empty[a], EPILOGUE_WARPS * 32);
+            ptx::mbar_init(&acc_empty[a], EPILOGUE_WARPS * S::CTAS);
         }
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -126,17 +128,29 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         ptx::prefetch_tensormap(&b_map);
     }
     if (warp == MMA_WARP) {
-        ptx::tmem_alloc(tmem_slot, S::TMEM_COLS);
-        ptx::tmem_relinquish();
+        if constexpr (S::PAIR) {
+            ptx::tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_slot, S::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (S::PAIR) {
+        // the peer's barriers are there before anything arrives on them
+        ptx::cluster_arrive_release();
+        ptx::cluster_wait_acquire();
+    }
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const uint32_t rank = S::PAIR ? ptx::cluster_ctarank() : 0;
 
     // this CTA's tiles, and its part of their K blocks
-    const int part = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
-    const long long first = blockIdx.x / p.split, step = gridDim.x / p.split;
+    const int part = !S::PAIR && p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    const int together = S::PAIR ? 2 : p.split;
+    const long long first = blockIdx.x / together, step = gridDim.x / together;
     const int kblocks = (p.in + BK - 1) / BK, all = kblocks * p.products;
     const int kb_begin = static_cast<int>(static_cast<long long>(all) * part / p.split);
     const int kb_end = static_cast<int>(static_cast<long long>(all) * (part + 1) / p.split);
@@ -145,7 +159,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         const long long tiles_n = tiles / tiles_m;
         const long long g = t / (p.group * tiles_n), in_group = t - g * p.group * tiles_n;
         const int tall = min(p.group, tiles_m - static_cast<int>(g) * p.group);
-        *m = (static_cast<int>(g) * p.group + static_cast<int>(in_group % tall)) * BM;
+        *m = ((static_cast<int>(g) * p.group + static_cast<int>(in_group % tall)) * S::CTAS + rank) * BM;
         *n = static_cast<int>(in_group / tall) * BN;
     };
     int issued = 0;  // K blocks, as far as they matter at the end: the last STAGES
@@ -177,15 +191,24 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                         ok = false;
                         break;
                     }
-                    int ax = m0, bx = n0;
+                    int ax = m0, bx = n0 + rank * S::B_ROWS;
                     if (p.products > 1) {  // behind the rows of the parts before these
                         ax += (S::SWAP ? part_of_w(product) : part_of_x(product)) * a_rows;
                         bx += (S::SWAP ? part_of_x(product) : part_of_w(product)) * b_rows;
                     }
                     uint8_t *st = smem + s * S::STAGE_BYTES;
-                    ptx::mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
-                    ptx::tma_load_2d(st, &a_map, &full[s], k * BK, ax);
-                    ptx::tma_load_2d(st + A_BYTES, &b_map, &full[s], k * BK, bx);
+                    if constexpr (S::PAIR) {
+                        // both CTAs' bytes count on the first one's barrier
+                        const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&full[s]), 0);
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(&full[s], 2 * S::STAGE_BYTES);
+                        ptx::tma_load_2d_pair(st, &a_map, bar, k * BK, ax);
+                        ptx::tma_load_2d_pair(st + A_BYTES, &b_map, bar, k * BK, bx);
+                    } else {
+                        ptx::mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
+                        ptx::tma_load_2d(st, &a_map, &full[s], k * BK, ax);
+                        ptx::tma_load_2d(st + A_BYTES, &b_map, &full[s], k * BK, bx);
+                    }
                     if (++k == kblocks) {
                         k = 0;
                         ++product;
@@ -196,6 +219,8 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 }
             }
         }
+    } else if (warp == MMA_WARP && rank > 0) {
+        // (the first CTA of a pair issues for both, and waits for both at the end)
     } else if (warp == MMA_WARP) {
         const bool leader = ptx::elect_one();
         const uint64_t a_desc = ptx::sw128_desc(ptx::smem_u32(smem));
@@ -203,7 +228,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
             const int a = committed % S::ACCS;
             const uint32_t use = static_cast<uint32_t>(committed / S::ACCS);
             bool ok = use == 0 || ptx::mbar_wait_bounded(&acc_empty[a], (use - 1) & 1, abort_flag, fault,
-                                                         kFaultMma, test.wait_limit_ns);
+                                                         kFaultMma, test.wait_limit_ns, S::PAIR);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             ptx::tc_fence_after();
@@ -219,14 +244,14 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                     const uint64_t at = a_desc + s * (S::STAGE_BYTES >> 4);
 #pragma unroll
                     for (int j = 0; j < BK / 16; ++j)
-                        ptx::mma_f16(d, at + 2 * j, at + (A_BYTES >> 4) + 2 * j, idesc,
-                                     kb != kb_begin || j != 0);
-                    ptx::mma_commit(&empty[s]);
+                        ptx::mma_f16<S::CTAS>(d, at + 2 * j, at + (A_BYTES >> 4) + 2 * j, idesc,
+                                              kb != kb_begin || j != 0);
+                    ptx::mma_commit<S::CTAS>(&empty[s]);
                 }
                 advance();
             }
             if (leader)
-                ptx::mma_commit(&acc_full[a]);  // also when stopping: frees the epilogue
+                ptx::mma_commit<S::CTAS>(&acc_full[a]);  // also when stopping: frees the epilogue
             ++committed;
             if (!ok)
                 break;
@@ -439,7 +464,13 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 }
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(&acc_empty[a]);
+            __syncwarp();
+            if (lane == 0) {
+                if (S::PAIR)
+                    ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&acc_empty[a]), 0));
+                else
+                    ptx::mbar_arrive(&acc_empty[a]);
+            }
         }
         if (lane == 0)
             ptx::bulk_wait_group<0>();
@@ -459,8 +490,9 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
 
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == PRODUCER_WARP && lane == 0) {
-        // every load has landed before the CTA's shared memory goes away
+    if (warp == PRODUCER_WARP && lane == 0 && rank == 0) {
+        // every load has landed before the CTA's shared memory goes away (a pair's second CTA
+        // waits for the first below)
         for (; issued > 0; --issued) {
             if (s == 0) {
                 s = STAGES;
@@ -477,8 +509,18 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                                      kDefaultWaitLimitNs);
         }
         __syncwarp();
+    }
+    if (S::PAIR) {
+        __syncthreads();
+        ptx::cluster_arrive_release();
+        ptx::cluster_wait_acquire();
+    }
+    if (warp == MMA_WARP) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, S::TMEM_COLS);
+        if constexpr (S::PAIR)
+            ptx::tmem_dealloc_pair(tmem, S::TMEM_COLS);
+        else
+            ptx::tmem_dealloc(tmem, S::TMEM_COLS);
     }
 }
 
@@ -582,24 +624,25 @@ int launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &y, Den
     if ((st = check_launch_injection("lstm_dense")))
         return st;
     const int down = S::SWAP ? p.out : p.rows, along = S::SWAP ? p.rows : p.out;
-    const int tiles_m = static_cast<int>((down + BM - 1LL) / BM);
+    const int tiles_m = static_cast<int>((down + S::CTAS * BM - 1LL) / (S::CTAS * BM));
     const long long tiles = tiles_m * ((along + S::BN - 1LL) / S::BN);
     p.split = split;
-    p.group = S::SWAP ? 1 : 12;
+    p.group = S::SWAP ? 1 : 12 / S::CTAS;
     cudaLaunchConfig_t cfg = {};
     // few rows: a cluster for each tile; else no more CTAs than run at once
-    const long long ctas = S::SWAP || split > 1 ? tiles * split : tiles < 152 ? tiles : 152;
+    const long long ctas = S::SWAP || split > 1 ? tiles * split
+                                                : S::CTAS * (tiles < 152 / S::CTAS ? tiles : 152 / S::CTAS);
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = S::SMEM_BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attribute;
     attribute.id = cudaLaunchAttributeClusterDimension;
-    attribute.val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+    attribute.val.clusterDim = {static_cast<unsigned>(S::PAIR ? 2 : split), 1, 1};
     cfg.attrs = &attribute;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.numAttrs = S::PAIR || split > 1 ? 1 : 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, dense_kernel<S, T>, a, b, y, p,
-                                          ptx::f16_idesc(BM, S::BN, bf16), tiles, tiles_m, fault,
+                                          ptx::f16_idesc(BM * S::CTAS, S::BN, bf16), tiles, tiles_m, fault,
                                           kernel_test(kTestDense)),
                        "lstm_dense launch");
 }
@@ -609,25 +652,44 @@ struct Plan {
     bool swap;
     int width;
     int split;
+    bool pair;
+    // rows of a box of x and of w
+    int x_rows() const { return swap ? width : BM; }
+    int w_rows() const { return swap ? BM : pair ? width / 2 : width; }
 };
 
 Plan make_plan(int rows, int in, int out, int products)
 {
-    Plan r = {rows <= kFewRows, 0, 1};
+    Plan r = {rows <= kFewRows, 0, 1, false};
     const long long kblocks = (in + BK - 1LL) / BK * products;
     long long tiles;
     if (r.swap) {
         r.width = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
         tiles = (out + BM - 1LL) / BM;
     } else {
+        // What a K block of a tile takes, in cycles: the tensor core's 131 for each 16 of K at a
+        // width of 256 (67 at 128, 51 at 64), or the loads, of which an SM gets 64 bytes a
+        // cycle.  A pair of SMs loads half of w's rows each, 32 KB where an SM alone loads 48,
+        // and so keeps its tensor cores busy.
         const long long tall = (rows + BM - 1LL) / BM;
+        const auto turns = [](long long tiles, int at_once) { return (tiles + at_once - 1) / at_once; };
+        const long long pairs = (rows + 2 * BM - 1LL) / (2 * BM) * ((out + 255LL) / 256);
+        long long best = turns(pairs, 76) * 530;
+        r.pair = true;
         r.width = 256;
-        while (r.width > 64 && tall * ((out + r.width - 1LL) / r.width) < 76)
-            r.width /= 2;
-        tiles = tall * ((out + r.width - 1LL) / r.width);
+        tiles = 2 * pairs;
+        for (const int width : {256, 128, 64}) {
+            const long long n = tall * ((out + width - 1LL) / width);
+            const long long cost = turns(n, 152) * (width == 256 ? 768 : width == 128 ? 512 : 384);
+            if (cost < best) {
+                best = cost;
+                r = {false, width, 1, false};
+                tiles = n;
+            }
+        }
     }
     // (one CTA an SM, whose ring is deep enough to keep its share of the memory busy)
-    while (r.split < 8 && tiles * r.split * 2 <= 152 && kblocks >= 8 * r.split)
+    while (!r.pair && r.split < 8 && tiles * r.split * 2 <= 152 && kblocks >= 8 * r.split)
         r.split *= 2;
     return r;
 }
@@ -646,6 +708,8 @@ int product(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &y, De
             return launch<Shape<64, true>, T>(w, x, y, p, bf16, plan.split, stream);
         }
     }
+    if (plan.pair)
+        return launch<Shape<256, false, true>, T>(x, w, y, p, bf16, 1, stream);
     switch (plan.width) {
     case 64:
         return launch<Shape<64, false>, T>(x, w, y, p, bf16, plan.split, stream);
@@ -747,9 +811,9 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
                                  : encode_box_map(m, type, at, n * parts, in, pitch, box_rows);
     };
     CUtensorMap x_map, w_map, y_map = {};
-    if ((st = map(&x_map, ox, x, x_stride, rows, workspace, plan.swap ? plan.width : BM)) ||
+    if ((st = map(&x_map, ox, x, x_stride, rows, workspace, plan.x_rows())) ||
         (st = map(&w_map, ow, w, w_stride, out, static_cast<char *>(workspace) + ox.bytes,
-                  plan.swap ? BM : plan.width)))
+                  plan.w_rows())))
         return st;
     DenseArgs p = {bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
                    dtype == LSTM_F32 ? kProducts : 1, 1, false, false, 1};
