@@ -236,51 +236,53 @@ __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4]
 }
 
 // ---- loading ------------------------------------------------------------------------------
-// Rows of a head into a tile, `units` units of 16 bytes a row (a power of two up to 16); rows
+// Rows of a head on their way into a tile, 1 << units units of 16 bytes a row (up to 16); rows
 // from `len` and numbers from `width` on are zeros, and what lies behind the units stays.  A
-// thread keeps its unit and goes down the rows, so that swizzle and width are worked out once.
+// thread keeps its unit and goes down the rows, two at a time, so that swizzle and width are
+// worked out once.
+constexpr int kTogether = 2;
 template <typename T>
-__device__ __forceinline__ void load_tile(uint8_t *tile, int apart, const T *from, long long stride,
-                                          bool aligned, int len, int width, int units, int tid)
+__device__ __forceinline__ void read_rows(float (&f)[kTogether][8], const T *from, long long stride,
+                                          bool aligned, int len, int width, int units, int group,
+                                          int tid)
 {
-    constexpr int kTogether = 4;        // rows in flight
-    const int down = kLoaders / units;  // rows of a turn, a multiple of 8
-    const int u = tid & (units - 1), r0 = tid / units;
-    const T *src = from + r0 * stride + u * 8;
-    const long long step = down * stride;
-    uint8_t *dst = tile + (u >> 3) * kSlab + r0 * kRowBytes + (((u & 7) ^ (r0 & 7)) << 4);
+    const int down = kLoaders >> units;  // rows of a turn, a multiple of 8
+    const int u = tid & ((1 << units) - 1), r = (tid >> units) + group * kTogether * down;
+    const T *src = from + r * stride + u * 8;
     const int there = min(max(width - u * 8, 0), 8);
-#pragma unroll 1
-    for (int r = r0; r < C; r += kTogether * down) {
-        float f[kTogether][8];
-        if (aligned && there == 8) {
-            constexpr int V = Elem<T>::kVector;
-#pragma unroll
-            for (int k = 0; k < kTogether; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; j += V) {
-                    Pack<T, V> v = {};
-                    if (r + k * down < len)
-                        v = load_pack<T, V>(src + k * step + j);
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        f[k][j + e] = Elem<T>::get(v.v[e]);
-                }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kTogether; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[k][j] = r + k * down < len && j < there ? Elem<T>::get(src[k * step + j])
-                                                              : 0.0f;
-        }
+    if (aligned && there == 8) {
+        constexpr int V = Elem<T>::kVector;
 #pragma unroll
         for (int k = 0; k < kTogether; ++k)
-            if (r + k * down < C)
-                store_parts<Parts<T>::kIn>(dst + k * down * kRowBytes, apart, f[k]);
-        src += kTogether * step;
-        dst += kTogether * down * kRowBytes;
+#pragma unroll
+            for (int j = 0; j < 8; j += V) {
+                Pack<T, V> v = {};
+                if (r + k * down < len)
+                    v = load_pack<T, V>(src + k * down * stride + j);
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    f[k][j + e] = Elem<T>::get(v.v[e]);
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kTogether; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[k][j] = r + k * down < len && j < there ? Elem<T>::get(src[k * down * stride + j])
+                                                          : 0.0f;
     }
+}
+template <int N>
+__device__ __forceinline__ void write_rows(const float (&f)[kTogether][8], uint8_t *tile, int apart,
+                                           int units, int group, int tid)
+{
+    const int down = kLoaders >> units;
+    const int u = tid & ((1 << units) - 1), r = (tid >> units) + group * kTogether * down;
+    uint8_t *const dst = tile + (u >> 3) * kSlab + r * kRowBytes + (((u & 7) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k)
+        if (r + k * down < C)
+            store_parts<N>(dst + k * down * kRowBytes, apart, f[k]);
 }
 
 // A sum that fp32 alone would round too early, as the fp32 number next to it and the rest
@@ -1032,37 +1034,57 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             if (!weigh(c, s, turn, threadIdx.x - W::kLoad * 32))
                 break;
     } else if (warp >= W::kLoad && !test.withhold) {
-        // ---- loaders ----
-        const int tid = threadIdx.x - W::kLoad * 32;
-        int s = 0;
+        // ---- loaders: a group of rows is read while the one before is written ----
+        const int tid = threadIdx.x - W::kLoad * 32, first = outputs ? 0 : 1;
+        const auto width_of = [&](int which) { return which == 2 ? values : p.keys; };
+        const auto units_of = [&](int which) { return 32 - __clz((width_of(which) + 7) / 8 - 1); };
+        int s = 0, c = 0, which = first, group = 0;
         uint32_t turn = 0;
-        for (int c = 0; c < chunks; ++c, advance(s, turn)) {
-            const long long t0 = run.begin + static_cast<long long>(c) * C;
-            const int len = min(run.end - run.begin - c * C, C);
-            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
-                break;
-            uint8_t *const to = smem + s * l.stage;
+        const auto read = [&](float (&f)[kTogether][8]) {
+            const HeadRows &m = which == 0 ? p.q : which == 1 ? p.k : p.v;
+            const T *const from = m.row<T>(run.begin + static_cast<long long>(c) * C, head) +
+                                  (which == 2 ? v0 : 0);
+            const int len = run.end - run.begin - c * C, width = width_of(which);
+            // the next chunk's rows are on their way to L2 meanwhile, two threads a row
+            const int row = C + (tid >> 1);
+            if (group == 0 && row < len) {
+                const char *next = reinterpret_cast<const char *>(from + row * m.stride);
 #pragma unroll 1
-            for (int which = outputs ? 0 : 1; which < 3; ++which) {
-                const HeadRows &m = which == 0 ? p.q : which == 1 ? p.k : p.v;
-                const bool of_v = which == 2;
-                const int width = of_v ? values : p.keys;
-                const T *const from = m.row<T>(t0, head) + (of_v ? v0 : 0);
-                // the next chunk's rows are on their way to L2 meanwhile, two threads a row
-                const int row = C + (tid >> 1);
-                if (c * C + row < run.end - run.begin) {
-                    const char *next = reinterpret_cast<const char *>(from + row * m.stride);
-                    for (int n = (tid & 1) * 128; n < width * static_cast<int>(sizeof(T)); n += 256)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + n));
-                }
-                int units = 1;
-                while (units * 8 < width)
-                    units *= 2;
-                load_tile<T>(to + which * P::kIn * l.tile_k, of_v ? l.tile_v : l.tile_k, from,
-                             m.stride, aligned >> which & 1, len, width, units, tid);
+                for (int n = (tid & 1) * 128; n < width * static_cast<int>(sizeof(T)); n += 256)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(next + n));
             }
-            ptx::fence_proxy_async_smem();
-            arrive(&bar.full[s]);
+            read_rows<T>(f, from, m.stride, aligned >> which & 1, len, width, units_of(which), group, tid);
+        };
+        // false: there is no further group
+        const auto step = [&](const float (&f)[kTogether][8], float (&next)[kTogether][8]) {
+            const int c0 = c, which0 = which, group0 = group;
+            const int units = units_of(which);
+            if (++group >= 1 << units >> 2) {
+                group = 0;
+                if (++which == 3) {
+                    which = first;
+                    ++c;
+                }
+            }
+            if (c < chunks)
+                read(next);
+            if (which0 == first && group0 == 0 && c0 >= l.stages &&
+                !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
+                return false;
+            write_rows<P::kIn>(f, smem + s * l.stage + which0 * P::kIn * l.tile_k,
+                               which0 == 2 ? l.tile_v : l.tile_k, units, group0, tid);
+            if (c > c0) {
+                ptx::fence_proxy_async_smem();
+                arrive(&bar.full[s]);
+                advance(s, turn);
+            }
+            return c < chunks;
+        };
+        if (chunks > 0) {
+            float one[kTogether][8], two[kTogether][8];
+            read(one);
+            while (step(one, two) && step(two, one)) {
+            }
         }
     }
 

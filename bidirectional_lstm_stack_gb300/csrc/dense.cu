@@ -49,6 +49,7 @@ struct DenseArgs {
     int split;            // CTAs of a cluster, each a part of K
     bool store_boxes;     // y takes TMA stores
     bool vectors;         // the residual's rows start on 16-byte boundaries
+    bool whole;           // so does the bias
     int group;            // tiles down M that run side by side
 };
 
@@ -65,7 +66,8 @@ struct Shape {
     static constexpr int B_BYTES = B_ROWS * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int DATA_BYTES = 224 * 1024;
-    static constexpr int OUT_BYTES = SWAP ? 0 : EPILOGUE_WARPS * SLICE_BYTES;
+    static constexpr int SLICES = PAIR ? 2 : 1;  // a warp's, in turn
+    static constexpr int OUT_BYTES = SWAP ? 0 : EPILOGUE_WARPS * SLICES * SLICE_BYTES;
     static constexpr int FIT = (DATA_BYTES - OUT_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = FIT < kMaxStages ? FIT : kMaxStages;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -262,7 +264,8 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         const int q = warp & 3, turn = (warp - 2) >> 2;
         constexpr int TURNS = EPILOGUE_WARPS / 4;
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        uint8_t *const buf = out_slices + (warp - 2) * SLICE_BYTES;
+        uint8_t *const slices = out_slices + (warp - 2) * S::SLICES * SLICE_BYTES;
+        int sent = 0;
         T *const y = static_cast<T *>(p.y);
         const T *const residual = static_cast<const T *>(p.residual);
         int count = 0;
@@ -367,6 +370,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 // slices of 128 bytes of a row; 16-byte unit u of row r lies at u ^ (r % 8)
                 constexpr int WIDE = 128 / static_cast<int>(sizeof(T));
                 constexpr int TOGETHER = 16;  // numbers a lane has in flight, of WIDE
+                uint8_t *buf = slices;
                 const auto in_slice = [&](int row, int col) {
                     return reinterpret_cast<T *>(buf + row * 128 + (((col / V) ^ (row & 7)) << 4)) + col % V;
                 };
@@ -374,8 +378,9 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 for (int c0 = turn * WIDE; c0 < BN && n0 + c0 < p.out; c0 += TURNS * WIDE) {
                     // the store that last used this buffer has read it
                     if (p.store_boxes) {
+                        buf = slices + (sent++ & (S::SLICES - 1)) * SLICE_BYTES;
                         if (lane == 0)
-                            ptx::bulk_wait_group_read<0>();
+                            ptx::bulk_wait_group_read<S::SLICES - 1>();
                         __syncwarp();
                     }
                     const int wide = min(WIDE, p.out - (n0 + c0));
@@ -402,7 +407,16 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                         float f[CW];
                         read_columns<CW>(acc + c0 + h, f);
                         const int n = n0 + c0 + h;
-                        if (p.bias) {
+                        if (p.bias && p.whole && n + CW <= p.out) {
+#pragma unroll
+                            for (int j = 0; j < CW; j += 4) {
+                                const float4 b = __ldg(reinterpret_cast<const float4 *>(p.bias + n + j));
+                                f[j] += b.x;
+                                f[j + 1] += b.y;
+                                f[j + 2] += b.z;
+                                f[j + 3] += b.w;
+                            }
+                        } else if (p.bias) {
 #pragma unroll
                             for (int j = 0; j < CW; ++j)
                                 f[j] += n + j < p.out ? __ldg(p.bias + n + j) : 0.0f;
@@ -536,61 +550,86 @@ __device__ __forceinline__ float leading(float v, unsigned short *bits)
     return __uint_as_float(u & 0xffff0000u);
 }
 
+// A matrix and its copy (null: none).
+template <typename T>
+struct Copy {
+    const T *from;
+    long long stride, rows;
+    unsigned short *to;
+    bool vectors;  // rows start on 16-byte boundaries
+};
+
+// A thread takes eight numbers of a row, `1 << lanes` threads a row.
 template <typename T>
 __global__ void __launch_bounds__(kCopyThreads)
-operand_kernel(const T *__restrict__ from, long long stride, long long rows, int cols, int pitch,
-               unsigned short *__restrict__ to)
+operand_kernel(const Copy<T> x, const Copy<T> w, int cols, int pitch, int lanes)
 {
-    const long long quads = (cols + 3) / 4, cells = rows * quads;
-    const long long part = rows * pitch;
-    for (long long i = blockIdx.x * static_cast<long long>(kCopyThreads) + threadIdx.x; i < cells;
-         i += static_cast<long long>(gridDim.x) * kCopyThreads) {
-        const long long r = i / quads;
-        const int c = static_cast<int>(i - r * quads) * 4;
-        const T *src = from + r * stride + c;
-        unsigned short *dst = to + r * pitch + c;
-        ushort4 o[kParts];
-        unsigned short *bits[kParts] = {&o[0].x, &o[1].x, &o[2].x};
-        T v[4];
+    const long long rows_x = x.to ? x.rows : 0, rows = rows_x + (w.to ? w.rows : 0);
+    const int lane = threadIdx.x & ((1 << lanes) - 1), down = kCopyThreads >> lanes;
+    for (long long n = blockIdx.x * static_cast<long long>(down) + (threadIdx.x >> lanes); n < rows;
+         n += static_cast<long long>(gridDim.x) * down) {
+        const Copy<T> &m = n < rows_x ? x : w;
+        const long long r = n < rows_x ? n : n - rows_x, part = m.rows * pitch;
+        const T *const from = m.from + r * m.stride;
+        unsigned short *const to = m.to + r * pitch;
+        for (int c = lane * 8; c < cols; c += 8 << lanes) {
+            T v[8];
+            if (m.vectors && c + 8 <= cols) {
+                constexpr int V = 16 / sizeof(T);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = c + j < cols ? src[j] : T();
-        if constexpr (sizeof(T) == 4) {
+                for (int j = 0; j < 8; j += V)
+                    *reinterpret_cast<uint4 *>(v + j) = __ldg(reinterpret_cast<const uint4 *>(from + c + j));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f = v[j];
-                const float lead = leading(f, bits[0] + j);
-                // (an infinity or a NaN has no rest; a NaN's leading bits may be an infinity's)
-                const bool finite = fabsf(f) <= 3.402823466e38f;
-                if (f != f)
-                    bits[0][j] = 0x7fc0;
-                f = finite ? f - lead : 0.0f;
-                f -= leading(f, bits[1] + j);
-                leading(f, bits[2] + j);
+                for (int j = 0; j < 8; ++j)
+                    v[j] = c + j < cols ? from[c + j] : T();
             }
+            if constexpr (sizeof(T) == 4) {
+                uint32_t o[kParts][4];
 #pragma unroll
-            for (int k = 0; k < kParts; ++k)
-                *reinterpret_cast<ushort4 *>(dst + k * part) = o[k];
-        } else {
+                for (int j = 0; j < 8; ++j) {
+                    unsigned short bits[kParts];
+                    float f = v[j];
+                    const float lead = leading(f, &bits[0]);
+                    // (an infinity or a NaN has no rest; a NaN's leading bits may be an infinity's)
+                    const bool finite = fabsf(f) <= 3.402823466e38f;
+                    if (f != f)
+                        bits[0] = 0x7fc0;
+                    f = finite ? f - lead : 0.0f;
+                    f -= leading(f, &bits[1]);
+                    leading(f, &bits[2]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bits[0][j] = *reinterpret_cast<unsigned short *>(&v[j]);
-            *reinterpret_cast<ushort4 *>(dst) = o[0];
+                    for (int k = 0; k < kParts; ++k)
+                        o[k][j / 2] = j % 2 ? o[k][j / 2] | static_cast<uint32_t>(bits[k]) << 16 : bits[k];
+                }
+#pragma unroll
+                for (int k = 0; k < kParts; ++k)
+                    *reinterpret_cast<uint4 *>(to + k * part + c) =
+                        make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+            } else {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = static_cast<uint32_t>(v[2 * j]) | static_cast<uint32_t>(v[2 * j + 1]) << 16;
+                *reinterpret_cast<uint4 *>(to + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
     }
 }
 
 template <typename T>
-int copy_operand(const void *from, long long stride, long long rows, int cols, int pitch, void *to,
-                 cudaStream_t stream)
+int copy_operands(const Copy<T> &x, const Copy<T> &w, int cols, int pitch, cudaStream_t stream)
 {
     const int st = check_launch_injection("lstm_dense");
     if (st != LSTM_OK)
         return st;
-    const long long blocks = (rows * ((cols + 3) / 4) + kCopyThreads - 1) / kCopyThreads;
-    operand_kernel<T><<<static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16), kCopyThreads, 0,
-                        stream>>>(static_cast<const T *>(from), stride, rows, cols, pitch,
-                                  static_cast<unsigned short *>(to));
+    int lanes = 0;
+    while (lanes < 5 && 8 << lanes < cols)
+        ++lanes;
+    const long long rows = (x.to ? x.rows : 0) + (w.to ? w.rows : 0);
+    const long long blocks = (rows + (kCopyThreads >> lanes) - 1) / (kCopyThreads >> lanes);
+    operand_kernel<T><<<static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8), kCopyThreads, 0,
+                        stream>>>(x, w, cols, pitch, lanes);
     return cuda_status(cudaGetLastError(), "lstm_dense launch");
 }
 
@@ -688,8 +727,10 @@ Plan make_plan(int rows, int in, int out, int products)
             }
         }
     }
-    // (one CTA an SM, whose ring is deep enough to keep its share of the memory busy)
-    while (!r.pair && r.split < 8 && tiles * r.split * 2 <= 152 && kblocks >= 8 * r.split)
+    // (one CTA an SM, whose ring is deep enough to keep its share of the memory busy; clusters
+    // of eight such CTAs do not all find room at a time: 128 x 4096 x 1024 takes 15 us in parts
+    // of four, 23 us in parts of eight)
+    while (!r.pair && r.split < 4 && tiles * r.split * 2 <= 152 && kblocks >= 8 * r.split)
         r.split *= 2;
     return r;
 }
@@ -795,28 +836,36 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
     const CUtensorMapDataType type =
         dtype == LSTM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int parts = dtype == LSTM_F32 ? kParts : 1;
-    const auto map = [&](CUtensorMap *m, const Operand &o, const void *at, long long stride,
-                         long long n, void *copy, int box_rows) {
-        int status = LSTM_OK;
-        long long pitch = (n > 1 ? stride : (in + 7) / 8 * 8) * 2;
-        if (o.copied) {
-            if (dtype == LSTM_F32)
-                status = copy_operand<float>(at, stride, n, in, o.pitch, copy, on);
-            else
-                status = copy_operand<unsigned short>(at, stride, n, in, o.pitch, copy, on);
-            at = copy;
-            pitch = o.pitch * 2LL;
-        }
-        return status != LSTM_OK ? status
-                                 : encode_box_map(m, type, at, n * parts, in, pitch, box_rows);
+    // (both rows of `in`, and so of one pitch)
+    void *const x_copy = ox.copied ? workspace : nullptr;
+    void *const w_copy = ow.copied ? static_cast<char *>(workspace) + ox.bytes : nullptr;
+    if (ox.copied || ow.copied) {
+        const auto copy = [&](auto type) {
+            using T = decltype(type);
+            const auto one = [&](const void *from, long long stride, long long n, void *to) {
+                return Copy<T>{static_cast<const T *>(from), stride, n, static_cast<unsigned short *>(to),
+                               rows_aligned(from, n > 1 ? stride : 0, sizeof(T))};
+            };
+            return copy_operands<T>(one(x, x_stride, rows, x_copy), one(w, w_stride, out, w_copy), in,
+                                    ox.pitch, on);
+        };
+        st = dtype == LSTM_F32 ? copy(0.0f) : copy(static_cast<unsigned short>(0));
+        if (st != LSTM_OK)
+            return st;
+    }
+    const auto map = [&](CUtensorMap *m, const void *copy, const void *at, long long stride, long long n,
+                         int box_rows) {
+        const long long own = ox.pitch;  // (of one row the stride says nothing)
+        return encode_box_map(m, type, copy ? copy : at, n * parts, in,
+                              (copy || n == 1 ? own : stride) * 2, box_rows);
     };
     CUtensorMap x_map, w_map, y_map = {};
-    if ((st = map(&x_map, ox, x, x_stride, rows, workspace, plan.x_rows())) ||
-        (st = map(&w_map, ow, w, w_stride, out, static_cast<char *>(workspace) + ox.bytes,
-                  plan.w_rows())))
+    if ((st = map(&x_map, x_copy, x, x_stride, rows, plan.x_rows())) ||
+        (st = map(&w_map, w_copy, w, w_stride, out, plan.w_rows())))
         return st;
     DenseArgs p = {bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
-                   dtype == LSTM_F32 ? kProducts : 1, 1, false, false, 1};
+                   dtype == LSTM_F32 ? kProducts : 1, 1, false, false, false, 1};
+    p.whole = rows_aligned(bias, 0, 4);
     // (whole vectors: what lies behind a row's last numbers is not read)
     p.vectors = residual && rows_aligned(residual, rows > 1 ? residual_stride : 0, size) &&
                 out * size % 16 == 0;

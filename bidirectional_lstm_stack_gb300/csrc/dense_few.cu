@@ -10,7 +10,7 @@
 namespace lstm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kColumns = 4;   // of y, rows of w, a warp takes
 constexpr int kEnough = 152 * 16;  // warps: half of what the SMs hold
 
