@@ -528,10 +528,16 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
     };
     // where a chunk stands in buffers used in turn
     const auto parity_of = [](int c, uint32_t buffers) { return static_cast<uint32_t>(c) / buffers & 1; };
-    const unsigned polls = static_cast<unsigned>(test.wait_limit_ns / ptx::kSuspendedNs) + 1;
-    // (by all lanes of a warp)
+    // By all lanes of a warp.  A wait that runs out leaves a mark, and this thread's further
+    // waits give up at once: its loops go on to their ends, which takes no code, over whatever
+    // the buffers hold.
+    unsigned polls = static_cast<unsigned>(test.wait_limit_ns / ptx::kSuspendedNs) + 2;
     const auto wait = [&](uint64_t *b, uint32_t parity, unsigned code) {
-        return __all_sync(0xffffffffu, ptx::mbar_wait_suspended(b, parity, abort, code, polls)) != 0;
+        if (!ptx::mbar_wait_suspended(b, parity, polls)) {
+            polls = 1;
+            *abort = code;
+        }
+        __syncwarp();
     };
     // what all lanes did before is there
     const auto arrive = [&](uint64_t *b) {
@@ -541,8 +547,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
     };
     // w v of chunk c in two halves, and V's tile without what the products must not meet
     const auto weigh = [&](int c, int s, uint32_t turn, int tid) {
-        if (!wait(&bar.full[s], turn, kFaultConverter))
-            return false;
+        wait(&bar.full[s], turn, kFaultConverter);
         uint8_t *const tile = smem + s * l.stage + P::kIn * 2 * l.tile_k;
         const Decays &d = decays[s];
         int *const first_bad = infos[c & (kInfos - 1)].first_bad;
@@ -565,8 +570,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         int j = tid >> 3;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-            if (kOwn && c > 0 && !wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter))
-                return false;
+            if (kOwn && c > 0)
+                wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter);
 #pragma unroll 1
             for (int turn = 0; turn < 32 / kRows; ++turn, j += kRows) {
                 const float until = d.until[j];
@@ -600,7 +605,6 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         }
         if (lane == 0)
             ptx::mbar_arrive(&bar.clean[c & (kCleans - 1)]);
-        return true;
     };
 
     if (warp < W::kOut && (warp & 3) < 2) {
@@ -616,12 +620,10 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 const Decays &d = decays[s];
                 // (P of an earlier chunk in this buffer has been multiplied)
                 const int before = c - l.p_buffers;
-                const bool ok = (before < 0 || wait(&bar.intra_full[before & 1],
-                                                    parity_of(before, 2), kFaultConverter)) &&
-                                wait(&bar.full[s], turn, kFaultConverter) &&
-                                wait(&bar.scores_full[b], parity_of(c, 2), kFaultConverter);
-                if (!ok || *abort)
-                    break;
+                if (before >= 0)
+                    wait(&bar.intra_full[before & 1], parity_of(before, 2), kFaultConverter);
+                wait(&bar.full[s], turn, kFaultConverter);
+                wait(&bar.scores_full[b], parity_of(c, 2), kFaultConverter);
                 ptx::tc_fence_after();
                 uint8_t *const row = p_tiles + (c & (l.p_buffers - 1)) * l.p + i * kRowBytes;
                 const int swizzle = (i & 7) << 4;
@@ -665,10 +667,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         const Pair scale = make_pair(p.scale, p.scale);
         for (int c = 0; outputs && c < chunks; ++c) {
             const int b = c & 1, ib = c & (Col::kInters - 1);
-            const bool ok = wait(&bar.inter_full[ib], parity_of(c, Col::kInters), kFaultEpilogue) &&
-                            wait(&bar.intra_full[b], parity_of(c, 2), kFaultEpilogue);
-            if (!ok || *abort)
-                break;
+            wait(&bar.inter_full[ib], parity_of(c, Col::kInters), kFaultEpilogue);
+            wait(&bar.intra_full[b], parity_of(c, 2), kFaultEpilogue);
             ptx::tc_fence_after();
             const int len = min(run.end - run.begin - c * C, C);
             const Info &info = infos[c & (kInfos - 1)];
@@ -771,8 +771,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
 #pragma unroll 1
         for (int c = -1; c < chunks; ++c) {
             if (c >= 0) {
-                if (!wait(&bar.update_full, c & 1, kFaultConverter) || *abort)
-                    break;
+                wait(&bar.update_full, c & 1, kFaultConverter);
                 ptx::tc_fence_after();
                 const float all = infos[c & (kInfos - 1)].all;
                 const Pair left = make_pair(all, all);
@@ -792,17 +791,14 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             if (c + 1 == chunks)
                 break;
             if (!TMA || !W::kLoads) {
-                if (!weigh(c + 1, s, turn, tid))
-                    break;
+                weigh(c + 1, s, turn, tid);
                 advance(s, turn);
             }
             if (!outputs)
                 continue;
             if (c >= 0) {
                 // S of chunk c has been multiplied
-                if (!wait(&bar.inter_full[c & (Col::kInters - 1)], parity_of(c, Col::kInters),
-                          kFaultConverter) || *abort)
-                    break;
+                wait(&bar.inter_full[c & (Col::kInters - 1)], parity_of(c, Col::kInters), kFaultConverter);
                 ptx::tc_fence_after();
             }
 #pragma unroll
@@ -860,9 +856,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 if (c < chunks) {
                     // a buffer of scores is free, and so is one of two of inter, when y of the
                     // chunk before in it has been read
-                    if (!wait(&bar.full[s], turn, kFaultMma) ||
-                        (c >= 2 && !wait(&bar.y_free[c & 1], parity_of(c - 2, 2), kFaultMma)))
-                        break;
+                    wait(&bar.full[s], turn, kFaultMma);
+                    if (c >= 2)
+                        wait(&bar.y_free[c & 1], parity_of(c - 2, 2), kFaultMma);
                     ptx::tc_fence_after();
                     const uint64_t k_desc = q_desc + P::kIn * part_k;
                     const uint32_t scores = tmem + Col::kScores + C * (c & 1);
@@ -878,9 +874,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 const int of = c - lag;
                 if (of >= 0) {
                     // (w v is there: what is not finite has left V's tile)
-                    if (!wait(&bar.p_full[of & 1], parity_of(of, 2), kFaultMma) ||
-                        !wait(&bar.clean[of & (kCleans - 1)], parity_of(of, kCleans), kFaultMma))
-                        break;
+                    wait(&bar.p_full[of & 1], parity_of(of, 2), kFaultMma);
+                    wait(&bar.clean[of & (kCleans - 1)], parity_of(of, kCleans), kFaultMma);
                     ptx::tc_fence_after();
                     const uint64_t p_desc = p_descs + (of & (l.p_buffers - 1)) * (l.p >> 4);
                     const uint64_t v_desc = ptx::sw128_desc(
@@ -901,10 +896,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 }
                 s_intra = s;
                 if (c < chunks) {
-                    if (!wait(&bar.state_full, c & 1, kFaultMma) ||
-                        (Col::kInters == 1 && c > 0 &&
-                         !wait(&bar.y_free[(c - 1) & 1], parity_of(c - 1, 2), kFaultMma)))
-                        break;
+                    wait(&bar.state_full, c & 1, kFaultMma);
+                    if (Col::kInters == 1 && c > 0)
+                        wait(&bar.y_free[(c - 1) & 1], parity_of(c - 1, 2), kFaultMma);
                     ptx::tc_fence_after();
                     const uint32_t inter = tmem + Col::kInter + C * (c & (Col::kInters - 1));
                     multiply<P::kMid, P::kIn>(
@@ -938,18 +932,15 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             uint32_t turn = 0;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, advance(s, turn)) {
-                if (!wait(&bar.full[s], turn, kFaultMma) ||
-                    (c > 0 && !wait(&bar.update_free, (c - 1) & 1, kFaultMma)))
-                    break;
+                wait(&bar.full[s], turn, kFaultMma);
+                if (c > 0)
+                    wait(&bar.update_free, (c - 1) & 1, kFaultMma);
                 const uint64_t k_desc = ptx::sw128_desc(
                     ptx::smem_u32(smem + s * l.stage) + P::kIn * l.tile_k, kSlab);
                 const uint64_t w_desc = ptx::sw128_desc(ptx::smem_u32(weighted), kSlab / 2);
-                bool ok = true;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    ok = wait(&bar.weighted_full[half], c & 1, kFaultMma);
-                    if (!ok)
-                        break;
+                    wait(&bar.weighted_full[half], c & 1, kFaultMma);
                     ptx::tc_fence_after();
                     const uint64_t a_desc = w_desc + half * (l.weighted >> 5);
                     const uint64_t b_desc = k_desc + half * (kSlab >> 5);
@@ -968,8 +959,6 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                         }
                     }
                 }
-                if (!ok)
-                    break;
             }
             if (leader)
                 ptx::mma_commit(&bar.done[1]);
@@ -987,8 +976,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         uint32_t turn = 0;
         for (int c = 0; c < chunks; ++c, advance(s, turn)) {
             const float n0 = decay_at(c + 1, 2 * lane), n1 = decay_at(c + 1, 2 * lane + 1);
-            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
-                break;
+            if (c >= l.stages)
+                wait(&bar.empty[s], turn ^ 1, kFaultProducer);
             total = add(total, sum_decays(decays[s], infos[c & (kInfos - 1)], g0, g1, lane));
             arrive(&bar.full[s]);
             g0 = n0;
@@ -1003,7 +992,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         int s = 0, c = 0;
         uint32_t turn = 0;
         for (; c < chunks; ++c, advance(s, turn)) {
-            if (c >= l.stages && !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
+            if (c >= l.stages)
+                wait(&bar.empty[s], turn ^ 1, kFaultProducer);
+            if (polls == 1)  // (nothing is copied over what may be on its way)
                 break;
             if (lane == 0) {
                 uint64_t *const full = &bar.full[s];
@@ -1031,8 +1022,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         int s = 0;
         uint32_t turn = 0;
         for (int c = 0; c < chunks; ++c, advance(s, turn))
-            if (!weigh(c, s, turn, threadIdx.x - W::kLoad * 32))
-                break;
+            weigh(c, s, turn, threadIdx.x - W::kLoad * 32);
     } else if (warp >= W::kLoad && !test.withhold) {
         // ---- loaders: a group of rows is read while the one before is written ----
         const int tid = threadIdx.x - W::kLoad * 32, first = outputs ? 0 : 1;
@@ -1068,9 +1058,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             }
             if (c < chunks)
                 read(next);
-            if (which0 == first && group0 == 0 && c0 >= l.stages &&
-                !wait(&bar.empty[s], turn ^ 1, kFaultProducer))
-                return false;
+            if (which0 == first && group0 == 0 && c0 >= l.stages)
+                wait(&bar.empty[s], turn ^ 1, kFaultProducer);
             write_rows<P::kIn>(f, smem + s * l.stage + which0 * P::kIn * l.tile_k,
                                which0 == 2 ? l.tile_v : l.tile_k, units, group0, tid);
             if (c > c0) {

@@ -265,14 +265,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
-// Waits for the phase with `parity`, or until *abort becomes non-zero; false (after joining
-// `code` to *abort) when `polls` polls, each suspended for up to kSuspendedNs, have not met it.
-// Of as few instructions as it takes: in a kernel whose warps all run different code its
-// copies would fill the instruction cache, and each miss there costs more than the wait.
+// Waits for the phase with `parity`; false when `polls` polls, each suspended for up to
+// kSuspendedNs, have not met it.  Of as few instructions as it takes: in a kernel whose warps
+// all run different code its copies would fill the instruction cache, and each miss there
+// costs more than the wait.
 constexpr unsigned kSuspendedNs = 1000;
-__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity,
-                                                    volatile int *abort, unsigned code,
-                                                    unsigned polls)
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity, unsigned polls)
 {
 #pragma unroll 1
     while (true) {
@@ -285,10 +283,8 @@ __device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t pari
                      : "memory");
         if (__builtin_expect(ok, 1))
             return true;
-        if (*abort || --polls == 0) {
-            *abort |= code;
+        if (--polls == 0)
             return false;
-        }
     }
 }
 
