@@ -376,18 +376,16 @@ __device__ __forceinline__ void store_if(bool there, float *to, float v)
 
 // ---- the kernel ------------------------------------------------------------------------------
 // Thread layout, in warpgroups: two of scores' warps (whose spare places take the two issuing
-// warps, the decays' warp and the one that asks for copies), the output warps, the state warps, the loaders.  With TMA the
-// loaders have nothing to load and write w v in the state warps' stead; where those are eight,
-// they do it themselves, and the block's threads have 96 registers, not 80 (a state of 64
-// numbers a thread wants 90).
+// warps, the decays' warp and the one that asks for copies), the output warps, the state warps,
+// and the loaders, who with TMA have nothing to load and write w v in the state warps' stead.
 template <int KP, bool TMA>
 struct Warps {
     static constexpr int kOutIssue = 2, kStateIssue = 3, kDecay = 6, kCopy = 7;
     static constexpr int kOut = 8;
     static constexpr int kState = 12, kStates = 4 * (KP / 64);
-    static constexpr int kLoad = kState + kStates, kLoads = TMA && KP > 64 ? 0 : kLoaders / 32;
-    static constexpr int kThreads = (kLoad + kLoads) * 32;
-    static constexpr int kWeighers = (TMA && kLoads ? kLoads : kStates) * 32;  // who write w v
+    static constexpr int kLoad = kState + kStates;
+    static constexpr int kThreads = kLoad * 32 + kLoaders;
+    static constexpr int kWeighers = TMA ? kLoaders : kStates * 32;  // who write w v
 };
 // Tensor memory: two buffers of scores (intra goes where its scores were), one or two of
 // inter, the update, and S^T in up to three parts.
@@ -562,7 +560,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         // A thread takes a unit at a time.  Warps of their own write a half when that of the
         // chunk before has been multiplied; the states' warps know that both have been, since
         // they have added the update.
-        constexpr bool kOwn = TMA && W::kLoads;
+        constexpr bool kOwn = TMA;
         constexpr int kHalf = kSlab / 2, kRows = kWeighers / 8;  // rows of a turn
         const int part = l.slabs * kHalf;
         uint8_t *at = tile + tid * 16;
@@ -776,12 +774,12 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 const float all = infos[c & (kInfos - 1)].all;
                 const Pair left = make_pair(all, all);
 #pragma unroll
-                for (int n0 = 0; n0 < 64; n0 += 16) {
-                    uint32_t r[16];
-                    ptx::tmem_ld_32x32b_x16(tmem + lanes + Col::kUpdate + k0 + n0, r);
+                for (int n0 = 0; n0 < 64; n0 += 8) {
+                    uint32_t r[8];
+                    ptx::tmem_ld_32x32b_x8(tmem + lanes + Col::kUpdate + k0 + n0, r);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int n = 0; n < 16; n += 2)
+                    for (int n = 0; n < 8; n += 2)
                         h[(n0 + n) / 2] = free_fma2(h[(n0 + n) / 2], left,
                                                make_pair(__uint_as_float(r[n]), __uint_as_float(r[n + 1])));
                 }
@@ -790,7 +788,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             }
             if (c + 1 == chunks)
                 break;
-            if (!TMA || !W::kLoads) {
+            if (!TMA) {
                 weigh(c + 1, s, turn, tid);
                 advance(s, turn);
             }
