@@ -557,47 +557,55 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                 if ((n >> 3 & (C - 1)) >= len)
                     reinterpret_cast<uint4 *>(tile - l.tile_k)[n] = make_uint4(0, 0, 0, 0);
         }
-        // A thread takes a unit at a time.  Warps of their own write a half when that of the
-        // chunk before has been multiplied; the states' warps know that both have been, since
-        // they have added the update.
+        // A thread takes its units of a half and a slab at a time, rows kRows apart.  Warps of
+        // their own write a half when that of the chunk before has been multiplied; the states'
+        // warps know that both have been, since they have added the update.
         constexpr bool kOwn = TMA;
-        constexpr int kHalf = kSlab / 2, kRows = kWeighers / 8;  // rows of a turn
+        constexpr int kHalf = kSlab / 2, kRows = kWeighers / 8, kTurns = 32 / kRows;
         const int part = l.slabs * kHalf;
-        uint8_t *at = tile + tid * 16;
-        uint8_t *to = weighted + tid * 16;
-        int j = tid >> 3;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             if (kOwn && c > 0)
                 wait(&bar.weighted_free[half], (c - 1) & 1, kFaultConverter);
+            const int j0 = half * 32 + (tid >> 3);
+            float until[kTurns];
+#pragma unroll
+            for (int t = 0; t < kTurns; ++t)
+                until[t] = d.until[j0 + t * kRows];
 #pragma unroll 1
-            for (int turn = 0; turn < 32 / kRows; ++turn, j += kRows) {
-                const float until = d.until[j];
-#pragma unroll 1
-                for (int slab = 0; slab < l.slabs; ++slab) {
-                    uint8_t *const from = at + slab * kSlab;
-                    Pair f[4], none = make_pair(0.0f, 0.0f);
-                    load_parts<P::kIn>(from, l.tile_v, f);
-                    if (TMA && rare(j >= len)) {
+            for (int slab = 0; slab < l.slabs; ++slab) {
+                uint8_t *const from = tile + slab * kSlab + half * kHalf + tid * 16;
+                uint8_t *const to = weighted + half * (l.weighted / 2) + slab * kHalf + tid * 16;
+                Pair f[kTurns][4], none = make_pair(0.0f, 0.0f);
+#pragma unroll
+                for (int t = 0; t < kTurns; ++t) {
+                    load_parts<P::kIn>(from + t * kRows * kRowBytes, l.tile_v, f[t]);
+                    if (TMA && rare(j0 + t * kRows >= len)) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            f[i] = none;
-                        *reinterpret_cast<uint4 *>(from) = make_uint4(0, 0, 0, 0);
+                            f[t][i] = make_pair(0.0f, 0.0f);
+                        *reinterpret_cast<uint4 *>(from + t * kRows * kRowBytes) = make_uint4(0, 0, 0, 0);
                     }
+                }
+#pragma unroll
+                for (int t = 0; t < kTurns; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        none = free_fma2(f[i], make_pair(0.0f, 0.0f), none);
-                        f[i] = free_mul2(f[i], make_pair(until, until));
+                        none = free_fma2(f[t][i], make_pair(0.0f, 0.0f), none);
+                        f[t][i] = free_mul2(f[t][i], make_pair(until[t], until[t]));
                     }
-                    store_three(to + slab * kHalf, part, f);
-                    const float2 any = split_pair(none);
-                    if (rare(any.x != 0.0f || any.y != 0.0f))
-                        not_finite<P::kIn>(from, l.tile_v, first_bad + slab * 64 + ((tid ^ j) & 7) * 8, j);
+#pragma unroll
+                for (int t = 0; t < kTurns; ++t)
+                    store_three(to + t * kRows * kRowBytes, part, f[t]);
+                const float2 any = split_pair(none);
+                if (rare(any.x != 0.0f || any.y != 0.0f)) {
+#pragma unroll 1
+                    for (int t = 0; t < kTurns; ++t)
+                        not_finite<P::kIn>(from + t * kRows * kRowBytes, l.tile_v,
+                                           first_bad + slab * 64 + ((tid ^ j0) & 7) * 8,
+                                           j0 + t * kRows);
                 }
-                at += kRows * kRowBytes;
-                to += kRows * kRowBytes;
             }
-            to += l.weighted / 2 - kHalf;
             ptx::fence_proxy_async_smem();
             arrive(&bar.weighted_full[half]);
         }
