@@ -4,8 +4,8 @@ may lose.
 
 Attention: `size` carries the sum of the terms' absolute values through the same
 recurrence as the state; a term's relative error times it bounds the state's
-error.  A term k v e^c is off by its weight's rounding to two parts of bf16
-(2^-15 at most; 24 bits in fp32), by the exponential, and by sums: at most 64
+error.  A term k v e^c is off by its weight's rounding to three parts of bf16 (24 bits, of
+which products lose two), by the exponential, and by sums: at most 64
 terms of a span are summed in fp32 before they join the state, once a span.  An
 output also takes the state or q.k rounded to one (bf16), two (fp16) or three
 (fp32) parts of bf16.
@@ -17,7 +17,7 @@ import numpy as np
 from .ops import U32, slot_of
 
 PARTS = {"bf16": 2.0 ** -8, "f16": 2.0 ** -15, "f32": 2.0 ** -22}
-WEIGHT = {"bf16": 2.0 ** -15, "f16": 2.0 ** -15, "f32": 2.0 ** -22}
+WEIGHT = 2.0 ** -22
 SUMS = 400  # roundings or truncations of a span's sums and of the exponential
 
 
@@ -43,7 +43,7 @@ def linear_attention(q, k, v, log_decay, scale, spans_, dtype, state=None, slots
                 s = left * s + add
                 size = left * size + np.abs(add)
                 sums = (SUMS + 8 * ((t - a) // 64 + 1)) * U32
-                term = sums if step else WEIGHT[dtype] + sums
+                term = sums if step else WEIGHT + sums
                 mine = q[t, of[0]]
                 y[t] = scale * np.einsum("hk,hkv->hv", mine, s)
                 y_bound[t] = (abs(scale) * (term + (0 if step else PARTS[dtype]) + 2 * sums)

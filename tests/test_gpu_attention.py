@@ -386,3 +386,82 @@ def test_a_wait_that_runs_out_sets_the_fault_word_and_the_next_call_works():
         assert torch.equal(binding.lstm_linear_attention(q, k, v, d), ref)
         torch.cuda.synchronize()
         assert binding.lstm_fault_status() == 0
+
+
+# ---- sequences cut into spans, rows copied in boxes ---------------------------------------------
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("keys,values", [(128, 130), (33, 200), (64, 64)])
+def test_spans_of_unequal_sequences(dtype, keys, values):
+    _check(dtype, [1, 1400, 0, 63, 2100, 64], 2, keys, values, shared=(1, 2, 1), pool=7,
+           slots=[3, 0, 6, 5, -1, 1], resume=[1, 1, 0, 1, 0, 1], layout="slices")
+
+
+@pytest.mark.parametrize("decay", ["head", "each strong", "each forget", "each none", "each grow"])
+def test_spans_and_their_decays(decay):
+    for dtype in ("bf16", "f32"):
+        _check(dtype, [1300], 2, 48, 64, decay=decay, pool=2, slots=[1], resume=[1])
+
+
+def test_spans_start_from_the_slot_that_the_last_one_writes():
+    # (the same slot is read by the first span and written by the last)
+    q, k, v = _inputs("f32", 4000, 2, 64, 64)
+    d = _decays(gen(5), "each", 4000, 2)
+    state = normal(gen(6), 3, 2, 64, 64)
+    start = state.clone()
+    ys = [binding.lstm_linear_attention(q, k, v, d, state=state.copy_(start), slots=_i32([1]),
+                                        resume=_i32([1])).clone() for _ in range(5)]
+    assert all(torch.equal(y, ys[0]) for y in ys[1:])
+    assert torch.equal(state[[0, 2]], start[[0, 2]])
+
+
+@pytest.mark.parametrize("tokens", [130, 3000])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_rows_around_a_sequence_may_hold_anything(tokens, what):
+    q, k, v = _inputs("bf16", tokens + 100, 2, 64, 64)
+    d = _decays(gen(2), "each", tokens + 100, 2)
+    offsets = _i32([50, 50 + tokens - 17])
+    states = []
+    for m in (None, what):
+        if m is not None:
+            for x in (q, k, v, d):
+                x[:50] = m
+                x[50 + tokens - 17:] = m
+        state = torch.zeros(1, 2, 64, 64, device="cuda")
+        y = torch.full((tokens + 100, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        binding.lstm_linear_attention(q, k, v, d, offsets=offsets, state=state, y=y)
+        states.append((y, state))
+    assert torch.equal(states[0][0], states[1][0]) and torch.equal(states[0][1], states[1][1])
+
+
+def test_a_value_that_is_not_finite_far_into_a_cut_sequence():
+    q, k, v = _inputs("bf16", 3000, 2, 64, 64)
+    d = _decays(gen(2), "each", 3000, 2)
+    state = torch.zeros(1, 2, 64, 64, device="cuda")
+    y = binding.lstm_linear_attention(q, k, v, d)
+    v[1777, 1, 7] = float("inf")
+    y2 = binding.lstm_linear_attention(q, k, v, d, state=state)
+    assert torch.equal(y2[:1777], y[:1777]) and torch.equal(y2[:, 0], y[:, 0])
+    others = [c for c in range(64) if c != 7]
+    assert torch.equal(y2[..., others], y[..., others])
+    assert not y2[1777:, 1, 7].isfinite().any() and not state[0, 1, :, 7].isfinite().any()
+
+
+def test_a_workspace_that_is_short_or_missing_is_refused():
+    lib = binding.load()
+    q, k, v = _inputs("bf16", 4000, 1, 64, 64)
+    d, y = torch.zeros(1, device="cuda"), torch.empty(4000, 64, dtype=torch.bfloat16, device="cuda")
+    need = binding.lstm_linear_attention_workspace(4000, 1, 64, 64, 1, True)
+    assert need > 0
+    space = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def call(at, size):
+        return lib.lstm_linear_attention(
+            q.data_ptr(), 64, 64, 1, k.data_ptr(), 64, 64, 1, v.data_ptr(), 64, 64, 1, d.data_ptr(), 0,
+            1.0, binding.LSTM_BF16, 4000, 1, 64, 64, 1, None, None, 0, None, None, y.data_ptr(), 64, at,
+            size, None)
+
+    assert call(None, need) == binding.LSTM_E_INVALID
+    assert call(space.data_ptr(), need - 1) == binding.LSTM_E_LENGTH
+    assert call(space.data_ptr(), need) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y.view(4000, 1, 64), binding.lstm_linear_attention(q, k, v, d))

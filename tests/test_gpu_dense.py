@@ -193,3 +193,66 @@ def test_a_wait_that_runs_out_sets_the_fault_word_and_the_next_call_works(rows):
     assert torch.equal(binding.lstm_dense(x, w), ref)
     torch.cuda.synchronize()
     assert binding.lstm_fault_status() == 0
+
+
+# ---- the ways a product is cut up -----------------------------------------------------------------
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,n_in,n_out", [
+    (5000, 100, 520),    # pairs of SMs, a tile of 256 x 256 each
+    (4865, 72, 515),     # the same, the last tile a row and three columns wide
+    (2000, 136, 1000),   # tiles of one SM
+    (130, 1500, 200),    # parts of K, joined in a cluster
+    (40, 2100, 300),     # few rows, parts of K
+])
+def test_tiles(dtype, rows, n_in, n_out):
+    _check(dtype, rows, n_in, n_out, activation="silu")
+    _check(dtype, rows, n_in, n_out, bias=False, layout="odd")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 2, 3])
+@pytest.mark.parametrize("n_in,n_out", [(1, 1), (31, 5), (256, 3), (257, 64), (4096, 130), (5000, 7)])
+def test_a_row_or_a_few(dtype, rows, n_in, n_out):
+    for layout in ("dense", "slices", "odd"):
+        _check(dtype, rows, n_in, n_out, activation="gelu", layout=layout)
+
+
+def test_pairs_give_the_same_bits_each_time_and_in_place():
+    g = gen(4)
+    x, w = normal(g, 5000, 256, dtype=torch.bfloat16), normal(g, 1024, 256, dtype=torch.bfloat16)
+    r = normal(g, 5000, 1024, dtype=torch.bfloat16)
+    ref = binding.lstm_dense(x, w, residual=r)
+    for _ in range(5):
+        y = r.clone()
+        assert binding.lstm_dense(x, w, residual=y, y=y) is y
+        assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("rows", [2, 5000])
+def test_values_that_are_not_finite_stay_in_their_rows_and_columns(rows):
+    g = gen(5)
+    x, w = normal(g, rows, 200, dtype=torch.bfloat16), normal(g, 600, 200, dtype=torch.bfloat16)
+    ref = binding.lstm_dense(x, w)
+    x[1, 7], w[300, 3] = float("nan"), float("inf")
+    y = binding.lstm_dense(x, w)
+    assert not y[1].isfinite().any() and not y[:, 300].isfinite().any()
+    rows_ok = [r for r in range(rows) if r != 1]
+    cols_ok = [c for c in range(600) if c != 300]
+    assert torch.equal(y[rows_ok][:, cols_ok], ref[rows_ok][:, cols_ok])
+
+
+def test_a_wait_of_a_pair_that_runs_out_sets_the_fault_word_and_the_next_call_works():
+    lib = binding.load()
+    x, w = normal(gen(1), 5000, 512, dtype=torch.bfloat16), normal(gen(2), 512, 512, dtype=torch.bfloat16)
+    ref = binding.lstm_dense(x, w)
+    assert binding.lstm_fault_status() == 0
+    try:
+        assert lib.lstm_test_dense_timeout(1, 1000, 0) == 0
+        binding.lstm_dense(x, w)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.lstm_test_dense_timeout(0, 0, 0) == 0
+    assert binding.lstm_fault_status() != 0
+    assert torch.equal(binding.lstm_dense(x, w), ref)
+    torch.cuda.synchronize()
+    assert binding.lstm_fault_status() == 0
