@@ -6,21 +6,26 @@
 //    tile's two operands through a ring of stages with TMA;
 //  * warp 1 (one thread) issues tcgen05.mma kind::f16, M = 128, into a tensor-memory
 //    accumulator;
-//  * warps 2-5 read a finished accumulator (a lane per row of the tile), add the bias,
-//    apply the activation, add the residual and store.
+//  * warps 2-9 read a finished accumulator (a lane per row of the tile, half of the columns
+//    each), add the bias, apply the activation, add the residual and store.
 // Many rows: M are 128 rows of x and N up to 256 rows of w; one CTA an SM walks over
 // the tiles, and a second accumulator lets a tile's epilogue run under the next tile's
-// products.  Few rows (at most kFewRows): the operands change places, M are 128 rows
-// of w and N the 16 to 64 rows of x, so that a tile's 128 lanes all work and w streams
-// once.  Where a call has fewer tiles than SMs, the CTAs of a cluster take a part of K
-// each and join their sums through distributed shared memory, in the order of the parts.
+// products.  An SM gets 64 bytes a cycle from L2, so a tile of 128 x 256 waits for its
+// loads (48 KB a K block: 768 cycles, of which the products take 524): large products go to
+// pairs of SMs (cta_group::2), which share a tile of 256 x 256 and load half of w's rows
+// each.  2048 x 2048 x 8192 takes 54 us (59 by single SMs), 12288 x 4096 x 4096 272 us (294;
+// at 1.5 PFLOP/s the card runs into its power limit).
+// Few rows (at most kFewRows): the operands change places, M are 128 rows of w and N the 16
+// to 64 rows of x, so that a tile's 128 lanes all work and w streams once (64 x 4096 x 16384:
+// 29 us, 20 at the memory's rate).  Up to three rows go without tensor cores (dense_few.cu).
+// Where a call has fewer tiles than SMs, the CTAs of a cluster take a part of K each, and
+// each then joins its share of the tile's sums through distributed shared memory, in the
+// order of the parts.
 //
 // fp32 goes as bf16: x = x1 + x2 + x3 exactly, each the 8 leading bits of what the ones
 // before it leave, and of the nine products of two numbers' parts the six that reach
 // 2^-24 of the product are summed, the small ones first.  The split, and a copy to
 // 16-byte pitches of 16-bit operands that TMA cannot read in place, is a kernel before.
-#include <mutex>
-
 #include "dense.cuh"
 
 namespace lstm {

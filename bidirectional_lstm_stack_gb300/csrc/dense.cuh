@@ -30,7 +30,7 @@ __device__ __forceinline__ float activate(int kind, float v)
         return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     case LSTM_ACT_GELU_TANH: {
         // (1 + tanh z) / 2 = 1 / (1 + e^-2z): an exponential and a quotient, where tanhf takes
-        // some forty instructions; an infinite z of -v gives -0
+        // some forty instructions; where z is minus infinity the product is -0
         const float z = 0.7978845608028654f * fmaf(0.044715f * v * v, v, v);
         return v * reciprocal(1.0f + ex2(-2.0f * kLog2e * z));
     }

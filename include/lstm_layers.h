@@ -46,12 +46,15 @@ extern "C" {
  *          calls that may run at the same time need one each
  * 1 <= keys <= LSTM_ATTENTION_MAX_KEYS, 1 <= values <=
  * LSTM_ATTENTION_MAX_VALUES, 1 <= heads <= LSTM_ATTENTION_MAX_HEADS.
- * States are fp32, and what a token adds to them is off by 2^-15 of itself at
- * most.  With 16-bit types the products that make y take the state and the
- * products of queries and keys rounded to parts of bf16 (LSTM_BF16: 8 bits,
- * LSTM_F16: 16); with LSTM_F32 everything keeps 24 bits.
+ * States are fp32, and what a token adds to them keeps 24 bits.  With 16-bit
+ * types the products that make y take the state and the products of queries
+ * and keys rounded to parts of bf16 (LSTM_BF16: 8 bits, LSTM_F16: 16); with
+ * LSTM_F32 everything keeps 24 bits.
  * An infinity or a NaN makes what depends on it, itself or through a state,
  * infinite or NaN; tokens before it, other heads and sequences are as without.
+ * Few sequences and heads are cut into spans that run side by side (whence the
+ * workspace): a state's sums are then made in another order, which sizes alone
+ * decide, so that the same call gives the same bits.
  * A wait inside the kernel that does not end within two seconds sets the
  * library's fault word (lstm_fault_status); outputs and states are then
  * unspecified.
@@ -102,7 +105,8 @@ enum {
  * rows, in and out are at most LSTM_DENSE_MAX.
  * Products and sums are fp32, with LSTM_F32 too (each product keeps 24 bits of
  * its factors).  16-bit x and w whose rows all start on 16-byte boundaries are
- * read in place; others, and fp32, go through the workspace first.
+ * read in place, and so is everything up to three rows; others, and fp32, go
+ * through the workspace first.
  * An infinity or a NaN in x or w makes its row's or column's results infinite
  * or NaN.  Waits inside the kernel are bounded as lstm_linear_attention's.
  * Errors: LSTM_E_INVALID, LSTM_E_LENGTH (workspace), LSTM_E_OVERFLOW,
