@@ -98,6 +98,7 @@ struct Info {
     float all;           // e^(c_64)
     float pad[3];
 };
+constexpr int kOrdered = 64;  // sequences that a block puts in order for itself
 constexpr int kInfos = 8;
 // V's tile is clean: its weighing is two chunks ahead of the outputs at most
 constexpr int kCleans = 4;
@@ -117,7 +118,7 @@ struct Barriers {
     uint64_t clean[kCleans], state_full, update_full, update_free;
     uint64_t done[2];
     uint32_t tmem;
-    int abort;
+    int abort, sequence;
 };
 
 template <typename T, int KP>
@@ -439,7 +440,7 @@ __device__ __forceinline__ void multiply(bool leader, int steps, const A &a, con
 template <typename T, int KP, bool TMA>
 __global__ void __launch_bounds__(Warps<KP, TMA>::kThreads, 1)
 attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const Spans spans,
-                 const bool outputs, const Layout l, const int aligned, unsigned *fault, const KernelTest test)
+                 const bool outputs, const bool ordered, const Layout l, const int aligned, unsigned *fault, const KernelTest test)
 {
     using W = Warps<KP, TMA>;
     using Col = Columns<T, KP>;
@@ -458,11 +459,29 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
 
     // (the same for a warp's lanes, and known to be)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int head = blockIdx.y, v0 = blockIdx.z * 128;
-    const int values = min(p.values - v0, 128);
-    int sequence = blockIdx.x, number = 0;
-    if (spans.tokens)
+    const int v0 = blockIdx.z * 128, values = min(p.values - v0, 128);
+    int head = blockIdx.y, sequence = blockIdx.x, number = 0;
+    if (spans.tokens) {
         sequence = tile_owner(p.seq, blockIdx.x, spans.tokens, &number);
+    } else if (ordered) {
+        // the longest sequences' heads go first, so that no long one starts when the others end
+        // (the grid is heads x sequences then)
+        head = blockIdx.x;
+        const auto length = [&](int n) { return sequence_end(p.seq, n) - sequence_begin(p.seq, n); };
+        if (static_cast<int>(threadIdx.x) < p.seq.count) {
+            const int n = threadIdx.x, own = length(n);
+            int rank = 0;
+#pragma unroll 1
+            for (int m = 0; m < p.seq.count; ++m) {
+                const int other = length(m);
+                rank += other > own || (other == own && m < n);
+            }
+            if (rank == static_cast<int>(blockIdx.y))
+                bar.sequence = n;
+        }
+        __syncthreads();
+        sequence = __shfl_sync(0xffffffffu, bar.sequence, 0);
+    }
     const int slot = sequence_slot(p.slots, sequence);
     Run run;
     run.begin = sequence_begin(p.seq, sequence);
@@ -1119,10 +1138,13 @@ int launch(const Maps &maps, int aligned, const AttentionArgs &p, const Spans &s
         return fail(LSTM_E_CUDA, "cannot resolve the device fault word");
     if ((st = check_launch_injection("lstm_linear_attention")))
         return st;
-    const dim3 grid(static_cast<unsigned>(spans.tokens ? spans.units : p.seq.count),
-                    static_cast<unsigned>(p.heads), static_cast<unsigned>((p.values + 127) / 128));
+    const bool ordered = !spans.tokens && p.seq.offsets && p.seq.count > 1 && p.seq.count <= kOrdered;
+    const unsigned units = static_cast<unsigned>(spans.tokens ? spans.units : p.seq.count),
+                   heads = static_cast<unsigned>(p.heads);
+    const dim3 grid(ordered ? heads : units, ordered ? units : heads,
+                    static_cast<unsigned>((p.values + 127) / 128));
     attention_kernel<T, KP, TMA><<<grid, W::kThreads, l.total, stream>>>(
-        maps, p, spans, outputs, l, aligned, fault, kernel_test(kTestAttention));
+        maps, p, spans, outputs, ordered, l, aligned, fault, kernel_test(kTestAttention));
     return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
 }
 
