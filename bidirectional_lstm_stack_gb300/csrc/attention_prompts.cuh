@@ -1106,9 +1106,15 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             return c < chunks;
         };
         if (chunks > 0) {
-            float one[kTogether][8], two[kTogether][8];
-            read(one);
-            while (step(one, two) && step(two, one)) {
+            float now[kTogether][8], next[kTogether][8];
+            read(now);
+#pragma unroll 1
+            while (step(now, next)) {
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        now[k][j] = next[k][j];
             }
         }
     }
