@@ -68,6 +68,8 @@ template <int V>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttentionArgs p,
                                                                       const Spans spans)
 {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int sequence = blockIdx.z, head = blockIdx.y;
     const long long at = (blockIdx.x * static_cast<long long>(kJoinThreads) + threadIdx.x) * V;
     const int begin = sequence_begin(p.seq, sequence);
@@ -199,11 +201,11 @@ int launch_attention_join(const AttentionArgs &p, const Spans &spans, cudaStream
     // (sequences that are cut are few)
     const dim3 grid(static_cast<unsigned>((cells + kJoinThreads * vector - 1) / (kJoinThreads * vector)),
                     static_cast<unsigned>(p.heads), static_cast<unsigned>(p.seq.count));
-    if (vector == 4)
-        attention_join_kernel<4><<<grid, kJoinThreads, 0, stream>>>(p, spans);
-    else
-        attention_join_kernel<1><<<grid, kJoinThreads, 0, stream>>>(p, spans);
-    return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
+    Dependent launch(grid, kJoinThreads, 0, stream);
+    return cuda_status(vector == 4
+                           ? cudaLaunchKernelEx(&launch.config, attention_join_kernel<4>, p, spans)
+                           : cudaLaunchKernelEx(&launch.config, attention_join_kernel<1>, p, spans),
+                       "lstm_linear_attention launch");
 }
 
 }  // namespace lstm

@@ -457,6 +457,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
     Barriers &bar = *reinterpret_cast<Barriers *>(infos + kInfos);
     volatile int *const abort = &bar.abort;
 
+    if (!outputs)
+        ptx::griddep_launch_dependents();  // (the joining)
+    ptx::griddep_wait();
     // (the same for a warp's lanes, and known to be)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int v0 = blockIdx.z * 128, values = min(p.values - v0, 128);
@@ -1149,9 +1152,13 @@ int launch(const Maps &maps, int aligned, const AttentionArgs &p, const Spans &s
                    heads = static_cast<unsigned>(p.heads);
     const dim3 grid(ordered ? heads : units, ordered ? units : heads,
                     static_cast<unsigned>((p.values + 127) / 128));
-    attention_kernel<T, KP, TMA><<<grid, W::kThreads, l.total, stream>>>(
-        maps, p, spans, outputs, ordered, l, aligned, fault, kernel_test(kTestAttention));
-    return cuda_status(cudaGetLastError(), "lstm_linear_attention launch");
+    Dependent launch(grid, W::kThreads, l.total, stream);
+    if (!(spans.tokens && outputs))  // nothing of this call comes before
+        launch.config.numAttrs = 0;
+    return cuda_status(cudaLaunchKernelEx(&launch.config, attention_kernel<T, KP, TMA>, maps, p, spans,
+                                          outputs, ordered, l, aligned, fault,
+                                          kernel_test(kTestAttention)),
+                       "lstm_linear_attention launch");
 }
 
 template <typename T, int KP, bool TMA>

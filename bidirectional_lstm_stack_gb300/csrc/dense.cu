@@ -152,6 +152,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
     }
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();  // (the copies of this call's operands)
     const uint32_t rank = S::PAIR ? ptx::cluster_ctarank() : 0;
 
     // this CTA's tiles, and its part of their K blocks
@@ -569,6 +570,7 @@ template <typename T>
 __global__ void __launch_bounds__(kCopyThreads)
 operand_kernel(const Copy<T> x, const Copy<T> w, int cols, int pitch, int lanes)
 {
+    ptx::griddep_launch_dependents();
     const long long rows_x = x.to ? x.rows : 0, rows = rows_x + (w.to ? w.rows : 0);
     const int lane = threadIdx.x & ((1 << lanes) - 1), down = kCopyThreads >> lanes;
     for (long long n = blockIdx.x * static_cast<long long>(down) + (threadIdx.x >> lanes); n < rows;
@@ -656,7 +658,7 @@ struct Operand {
 // ---- launches ---------------------------------------------------------------------------
 template <class S, typename T>
 int launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &y, DenseArgs &p, bool bf16,
-           int split, cudaStream_t stream)
+           int split, bool copied, cudaStream_t stream)
 {
     static SharedMemory memory;
     int st = memory.allow(dense_kernel<S, T>, S::SMEM_BYTES);
@@ -672,20 +674,17 @@ int launch(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &y, Den
     const long long tiles = tiles_m * ((along + S::BN - 1LL) / S::BN);
     p.split = split;
     p.group = S::SWAP ? 1 : 12 / S::CTAS;
-    cudaLaunchConfig_t cfg = {};
     // few rows: a cluster for each tile; else no more CTAs than run at once
     const long long ctas = S::SWAP || split > 1 ? tiles * split
                                                 : S::CTAS * (tiles < 152 / S::CTAS ? tiles : 152 / S::CTAS);
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = S::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attribute;
-    attribute.id = cudaLaunchAttributeClusterDimension;
-    attribute.val.clusterDim = {static_cast<unsigned>(S::PAIR ? 2 : split), 1, 1};
-    cfg.attrs = &attribute;
-    cfg.numAttrs = S::PAIR || split > 1 ? 1 : 0;
-    return cuda_status(cudaLaunchKernelEx(&cfg, dense_kernel<S, T>, a, b, y, p,
+    Dependent launch(dim3(static_cast<unsigned>(ctas)), THREADS, S::SMEM_BYTES, stream);
+    launch.config.numAttrs = copied ? 1 : 0;  // (else nothing of this call comes before)
+    if (S::PAIR || split > 1) {
+        cudaLaunchAttribute &cluster = launch.attributes[launch.config.numAttrs++];
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim = {static_cast<unsigned>(S::PAIR ? 2 : split), 1, 1};
+    }
+    return cuda_status(cudaLaunchKernelEx(&launch.config, dense_kernel<S, T>, a, b, y, p,
                                           ptx::f16_idesc(BM * S::CTAS, S::BN, bf16), tiles, tiles_m, fault,
                                           kernel_test(kTestDense)),
                        "lstm_dense launch");
@@ -742,27 +741,27 @@ Plan make_plan(int rows, int in, int out, int products)
 
 template <typename T>
 int product(const CUtensorMap &x, const CUtensorMap &w, const CUtensorMap &y, DenseArgs &p,
-            const Plan &plan, bool bf16, cudaStream_t stream)
+            const Plan &plan, bool bf16, bool copied, cudaStream_t stream)
 {
     if (plan.swap) {
         switch (plan.width) {
         case 16:
-            return launch<Shape<16, true>, T>(w, x, y, p, bf16, plan.split, stream);
+            return launch<Shape<16, true>, T>(w, x, y, p, bf16, plan.split, copied, stream);
         case 32:
-            return launch<Shape<32, true>, T>(w, x, y, p, bf16, plan.split, stream);
+            return launch<Shape<32, true>, T>(w, x, y, p, bf16, plan.split, copied, stream);
         default:
-            return launch<Shape<64, true>, T>(w, x, y, p, bf16, plan.split, stream);
+            return launch<Shape<64, true>, T>(w, x, y, p, bf16, plan.split, copied, stream);
         }
     }
     if (plan.pair)
-        return launch<Shape<256, false, true>, T>(x, w, y, p, bf16, 1, stream);
+        return launch<Shape<256, false, true>, T>(x, w, y, p, bf16, 1, copied, stream);
     switch (plan.width) {
     case 64:
-        return launch<Shape<64, false>, T>(x, w, y, p, bf16, plan.split, stream);
+        return launch<Shape<64, false>, T>(x, w, y, p, bf16, plan.split, copied, stream);
     case 128:
-        return launch<Shape<128, false>, T>(x, w, y, p, bf16, plan.split, stream);
+        return launch<Shape<128, false>, T>(x, w, y, p, bf16, plan.split, copied, stream);
     default:
-        return launch<Shape<256, false>, T>(x, w, y, p, bf16, plan.split, stream);
+        return launch<Shape<256, false>, T>(x, w, y, p, bf16, plan.split, copied, stream);
     }
 }
 
@@ -879,5 +878,5 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
         (st = encode_box_map(&y_map, map_type(dtype), y, rows, out, y_stride * size, 32)))
         return st;
     LSTM_WITH_TYPE(dtype, T,
-                   return product<T>(x_map, w_map, y_map, p, plan, dtype != LSTM_F16, on));
+                   return product<T>(x_map, w_map, y_map, p, plan, dtype != LSTM_F16, ox.copied || ow.copied, on));
 }

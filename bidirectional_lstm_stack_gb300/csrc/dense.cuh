@@ -26,8 +26,19 @@ __device__ __forceinline__ float activate(int kind, float v)
     switch (kind) {
     case LSTM_ACT_RELU:
         return v < 0.0f ? 0.0f : v;  // (NaN stays)
-    case LSTM_ACT_GELU:
-        return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case LSTM_ACT_GELU: {
+        // v Phi(v), with erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + p x), off by
+        // 1.5e-7 at most (Abramowitz and Stegun, 7.1.26): twelve instructions, where both
+        // branches of erff take some fifty
+        const float x = fabsf(v) * 0.70710678118654752f;
+        const float t = reciprocal(fmaf(0.3275911f, x, 1.0f));
+        float h = fmaf(t, 1.061405429f, -1.453152027f);
+        h = fmaf(t, h, 1.421413741f);
+        h = fmaf(t, h, -0.284496736f);
+        h = fmaf(t, h, 0.254829592f);
+        h = 0.5f * t * h * ex2(-kLog2e * x * x);
+        return v * (v < 0.0f ? h : 1.0f - h);
+    }
     case LSTM_ACT_GELU_TANH: {
         // (1 + tanh z) / 2 = 1 / (1 + e^-2z): an exponential and a quotient, where tanhf takes
         // some forty instructions; where z is minus infinity the product is -0

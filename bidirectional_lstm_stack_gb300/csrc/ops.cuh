@@ -101,6 +101,26 @@ struct SharedMemory {
     }
 };
 
+// A launch as the programmatic dependent of the kernel before it on the stream: its blocks
+// may start when that kernel's have all asked for it or ended, and call
+// ptx::griddep_wait() before they touch what that kernel reads or writes.
+struct Dependent {
+    cudaLaunchConfig_t config = {};
+    cudaLaunchAttribute attributes[2];
+    Dependent(dim3 grid, dim3 block, size_t shared, cudaStream_t stream)
+    {
+        config.gridDim = grid;
+        config.blockDim = block;
+        config.dynamicSmemBytes = shared;
+        config.stream = stream;
+        attributes[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attributes[0].val.programmaticStreamSerializationAllowed = 1;
+        config.attrs = attributes;
+        config.numAttrs = 1;
+    }
+    Dependent(const Dependent &) = delete;
+};
+
 // ---- sequences and states ------------------------------------------------------
 // The sequences of a packed batch, as lstm_ops.h describes them.
 struct Sequences {
