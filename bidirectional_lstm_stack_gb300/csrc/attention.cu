@@ -14,7 +14,7 @@ constexpr int kLeastSpan = 4;  // chunks
 // In times of a chunk: what a span's chunk costs beside one of a whole sequence, since its
 // update is made twice; what starting a block costs, twice too; the two further launches;
 // and joining one head's state of one span (128 x 128: written and read twice).
-constexpr double kSpanCost = 1.6, kStartCost = 5.0, kLaunchCost = 2.0, kJoinCost = 0.01;
+constexpr double kSpanCost = 1.65, kStartCost = 6.0, kLaunchCost = 2.0, kJoinCost = 0.01;
 
 // Chunks of a span, or 0: sequences are whole.  With few sequences and heads most SMs
 // would idle, and with sequences of unequal length (the longest taken to be twice the mean)

@@ -465,3 +465,40 @@ def test_a_workspace_that_is_short_or_missing_is_refused():
     assert call(space.data_ptr(), need) == 0
     torch.cuda.synchronize()
     assert torch.equal(y.view(4000, 1, 64), binding.lstm_linear_attention(q, k, v, d))
+
+
+def test_a_captured_call_in_spans_reads_what_is_there_when_it_is_replayed():
+    q, k, v = _inputs("bf16", 4000, 2, 64, 64)
+    d = _decays(gen(2), "each", 4000, 2)
+    offsets, slots, resume = _i32([0, 1500, 4000]), _i32([1, 0]), _i32([1, 1])
+    state = torch.zeros(2, 2, 64, 64, device="cuda")
+    y = torch.empty(4000, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert binding.lstm_linear_attention_workspace(4000, 2, 64, 64, 2, False) > 0
+
+    def call():
+        binding.lstm_linear_attention(q, k, v, d, offsets=offsets, state=state, slots=slots,
+                                      resume=resume, y=y)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    g = gen(9)
+    for bounds, again in (([0, 1500, 4000], [1, 1]), ([0, 3990, 4000], [0, 1]), ([7, 7, 3000], [1, 0])):
+        q.copy_(normal(g, 4000, 2, 64))
+        offsets.copy_(_i32(bounds))
+        resume.copy_(_i32(again))
+        state.copy_(normal(g, 2, 2, 64, 64))
+        start = state.clone()
+        graph.replay()
+        replayed = y[bounds[0]:bounds[-1]].clone(), state.clone()
+        state.copy_(start)
+        call()
+        assert torch.equal(replayed[0], y[bounds[0]:bounds[-1]]) and torch.equal(replayed[1], state)
+
+
+@pytest.mark.parametrize("count", [2, 63, 64, 65, 200])
+def test_unequal_sequences_in_any_order(count):
+    # (up to 64 of them each block puts in order, the longest first; equal ones keep theirs)
+    lengths = [(i * 37) % 90 if i % 3 else 50 for i in range(count)]
+    _check("bf16", lengths, 16, 16, 16, pool=count, resume=[i % 2 for i in range(count)])
