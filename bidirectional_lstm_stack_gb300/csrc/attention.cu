@@ -28,7 +28,9 @@ int span_chunks(int tokens, int heads, int values, int sequences, bool equal_len
     if (all > 4 * kSms)
         return 0;
     const long long mean = ((tokens - 1LL) / sequences + 1 + kChunk - 1) / kChunk;
-    const auto turns = [](double units) { return static_cast<double>((static_cast<long long>(units) + kSms - 1) / kSms); };
+    const auto turns = [](double units) {
+        return static_cast<double>((static_cast<long long>(units) + kSms - 1) / kSms);
+    };
     const double longest = static_cast<double>(equal_lengths ? mean : 2 * mean);
     double best = longest > turns(all) * mean ? longest : turns(all) * mean;
     int chunks = 0;

@@ -35,8 +35,8 @@
 // What bounds it: with bf16 and 128 keys and values a chunk's products take the tensor core
 // 1 700 cycles (scores 8 x 51, inter 8 x 35, intra 4 x 51, update 12 x 67), shared memory some
 // 2 600 and the ALU pipe 1 800; the warps' chains, whose instructions exceed the instruction
-// cache, make it 3 980.  16 heads of a prompt of 4096 tokens take 51 us (68 MB: 10 us), four
-// prompts of 16384 tokens 414 us (675 MB: 99 us).  Waits, loops and rare branches are kept
+// cache, make it 3 980.  16 heads of a prompt of 4096 tokens take 50 us (68 MB: 10 us), four
+// prompts of 16384 tokens 420 us (675 MB: 99 us).  Waits, loops and rare branches are kept
 // short for that reason: inlining a wait's clock and messages at its 20 places cost a quarter
 // of the time at 64 keys.
 #pragma once
@@ -169,7 +169,9 @@ __device__ __forceinline__ void split_pair_parts(float x, float y, uint32_t (&r)
     if constexpr (N == 3) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r[k]) : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
+            asm("prmt.b32 %0, %1, %2, 0x7632;"
+                : "=r"(r[k])
+                : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
             x -= low_float(r[k]);
             y -= high_float(r[k]);
         }
@@ -239,7 +241,9 @@ __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = split_pair(f[i]);
-            asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r[i]) : "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)));
+            asm("prmt.b32 %0, %1, %2, 0x7632;"
+                : "=r"(r[i])
+                : "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)));
             if (k + 1 < kWeighted)
                 f[i] = free_fma2(make_pair(low_float(r[i]), high_float(r[i])), minus, f[i]);
         }
@@ -440,7 +444,8 @@ __device__ __forceinline__ void multiply(bool leader, int steps, const A &a, con
 template <typename T, int KP, bool TMA>
 __global__ void __launch_bounds__(Warps<KP, TMA>::kThreads, 1)
 attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const Spans spans,
-                 const bool outputs, const bool ordered, const Layout l, const int aligned, unsigned *fault, const KernelTest test)
+                 const bool outputs, const bool ordered, const Layout l, const int aligned,
+                 unsigned *fault, const KernelTest test)
 {
     using W = Warps<KP, TMA>;
     using Col = Columns<T, KP>;
@@ -1024,8 +1029,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         }
         if (!outputs && lane == 0 && blockIdx.z == 0)
             *spans.left_of(p, blockIdx.x, head) = ex2(total.hi + total.lo);
-    } else if (TMA && warp == W::kCopy && !test.withhold) {  // (failure test: nothing is loaded, so the waits for it run out)
-        // ---- rows by TMA ----
+    } else if (TMA && warp == W::kCopy && !test.withhold) {
+        // ---- rows by TMA (failure test: nothing is loaded, so the waits for it run out) ----
         const int q_head = head / p.q.share, k_head = head / p.k.share, v_head = head / p.v.share;
         const uint32_t bytes = (outputs ? 2 : 1) * l.tile_k + l.tile_v;
         int s = 0, c = 0;

@@ -2,7 +2,8 @@
 //     S = e^g S + k v^T,   y = scale S^T q
 // with S, keys x values fp32 numbers, read and written once: 8 bytes for 5
 // operations, so the states' traffic is all there is (a sequence of 16 heads of
-// 128 x 128 moves 2 MiB).  A block takes a head's S or a tile of its columns.
+// 128 x 128 moves 2 MiB; 256 of them 541 MB in 85 us, 94 % of the measured
+// 6.8 TB/s).  A block takes a head's S or a tile of its columns.
 // A thread keeps one vector of columns and goes down every R-th row, its loads
 // issued before their first use; the R partial sums of each column are joined
 // through shared memory in a fixed order.

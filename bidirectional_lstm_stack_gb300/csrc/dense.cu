@@ -13,7 +13,7 @@
 // products.  An SM gets 64 bytes a cycle from L2, so a tile of 128 x 256 waits for its
 // loads (48 KB a K block: 768 cycles, of which the products take 524): large products go to
 // pairs of SMs (cta_group::2), which share a tile of 256 x 256 and load half of w's rows
-// each.  2048 x 2048 x 8192 takes 54 us (59 by single SMs), 12288 x 4096 x 4096 272 us (294;
+// each.  2048 x 2048 x 8192 takes 54 us (59 by single SMs), 12288 x 4096 x 4096 275 us (294;
 // at 1.5 PFLOP/s the card runs into its power limit).
 // Few rows (at most kFewRows): the operands change places, M are 128 rows of w and N the 16
 // to 64 rows of x, so that a tile's 128 lanes all work and w streams once (64 x 4096 x 16384:
@@ -878,5 +878,6 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
         (st = encode_box_map(&y_map, map_type(dtype), y, rows, out, y_stride * size, 32)))
         return st;
     LSTM_WITH_TYPE(dtype, T,
-                   return product<T>(x_map, w_map, y_map, p, plan, dtype != LSTM_F16, ox.copied || ow.copied, on));
+                   return product<T>(x_map, w_map, y_map, p, plan, dtype != LSTM_F16,
+                                     ox.copied || ow.copied, on));
 }

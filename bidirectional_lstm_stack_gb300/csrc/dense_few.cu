@@ -1,6 +1,6 @@
 // The dense product for a row or a few:  y[r][n] = act(sum_k x[r][k] w[n][k] + bias[n]) +
 // residual[r][n].  w is read once for two operations a number and row, so its traffic is all
-// there is (4096 x 4096 of 16 bits: 33.6 MB, 4.9 us at the measured 6.8 TB/s), and tensor cores
+// there is (4096 x 4096 of 16 bits: 33.6 MB, 4.9 us at the measured 6.8 TB/s; 8.2 us), and tensor cores
 // would only add their set-up: a tile's pipeline has to be filled, its accumulator allocated,
 // read and joined.  A warp takes four rows of w over a part of K, all lanes side by side along
 // a row, and keeps several vectors a lane in flight; the sums of a row's parts are joined in
@@ -10,9 +10,10 @@
 namespace lstm {
 namespace {
 
+// (blocks of 256 threads fill the SMs less evenly: 11 us; two columns a warp: 10 us)
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kColumns = 4;   // of y, rows of w, a warp takes
-constexpr int kEnough = 152 * 16;  // warps: half of what the SMs hold
+constexpr int kEnough = 152 * 16;  // warps; with fewer, rows are shared out among more
 
 template <typename T, int R, int V>
 __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs p, int split)
