@@ -498,8 +498,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
     run.from = run.to && sequence_resumes(p.slots, sequence) ? run.to : nullptr;
     if (spans.tokens) {
         const int count = spans.count(run.end - run.begin);
-        // (a few numbers own no rows; what the last span leaves is made with its outputs)
-        if (number >= count || (!outputs && number == count - 1))
+        // (a few numbers own no rows, those before the first sequence's are negative; what the last
+        // span leaves is made with its outputs)
+        if (number < 0 || number >= count || (!outputs && number == count - 1))
             return;
         if (!outputs) {
             run.from = nullptr;

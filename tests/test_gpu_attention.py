@@ -502,3 +502,35 @@ def test_unequal_sequences_in_any_order(count):
     # (up to 64 of them each block puts in order, the longest first; equal ones keep theirs)
     lengths = [(i * 37) % 90 if i % 3 else 50 for i in range(count)]
     _check("bf16", lengths, 16, 16, 16, pool=count, resume=[i % 2 for i in range(count)])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("again", [0, 1])
+@pytest.mark.parametrize("first,lengths", [
+    (1000, [2500]),        # a cut sequence behind rows of several spans' length
+    (3000, [100]),         # a sequence of one span there
+    (1700, [0, 900, 40]),
+])
+def test_rows_before_the_first_sequence_of_a_call_in_spans(dtype, again, first, lengths):
+    # the same sequences at the front of as many tokens are cut the same way: the same bits
+    tokens, n = 4000, len(lengths)
+    total = sum(lengths)
+    assert binding.lstm_linear_attention_workspace(tokens, 2, 64, 64, n, False) > 0
+    m = [*_inputs(dtype, total, 2, 64, 64), _decays(gen(2), "each", total, 2)]
+    start = normal(gen(3), n + 1, 2, 64, 64)
+    out = []
+    for begin in (0, first):
+        parts = []
+        for x in m:
+            rows = torch.full((tokens, *x.shape[1:]), float("nan"), dtype=x.dtype, device="cuda")
+            rows[begin:begin + total] = x
+            parts.append(rows)
+        y = torch.full((tokens, 2, 64), 3.0, dtype=DTYPES[dtype], device="cuda")
+        state = start.clone()
+        binding.lstm_linear_attention(*parts, state=state, resume=_i32([again] * n), y=y,
+                                      offsets=_i32(np.cumsum([begin] + lengths)))
+        assert (y[:begin] == 3).all() and (y[begin + total:] == 3).all()
+        out.append((y[begin:begin + total], state))
+    assert out[0][0].isfinite().all() and out[0][1].isfinite().all()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert torch.equal(out[1][1][n:], start[n:])
