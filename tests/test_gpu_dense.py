@@ -1,6 +1,8 @@
 """The dense product against its float64 definition: types, sizes that no tile
 divides, activations, residuals, strides and alignment, values that are not
 finite, streams and graphs."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -256,3 +258,21 @@ def test_a_wait_of_a_pair_that_runs_out_sets_the_fault_word_and_the_next_call_wo
     assert torch.equal(binding.lstm_dense(x, w), ref)
     torch.cuda.synchronize()
     assert binding.lstm_fault_status() == 0
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 4, 70, 400])
+def test_gelu_keeps_its_relative_accuracy_far_out(dtype, rows):
+    # The factor Phi(v) is off by: its fit (2^-24), ten roundings of sums that are 2.4 times what
+    # they sum up to at most (2^-24 each, the first ones damped: 4 in all), the reciprocal (2^-23),
+    # the exponential (2^-22), three products (2^-24 each): below 2^-20 of itself.  (v is one
+    # operand of the type, the other is 1: the product is exact.)
+    top = 12.5 if dtype != "f16" else 4.0  # (results below are subnormal)
+    v = torch.linspace(-top, top, 64 * rows, device="cuda").view(rows, 64).to(DTYPES[dtype])
+    got = f64(binding.lstm_dense(v, torch.eye(64, dtype=DTYPES[dtype], device="cuda"), activation="gelu"))
+    x = f64(v)
+    ref = x * 0.5 * np.vectorize(math.erfc)(-x / math.sqrt(2.0))
+    rel = 2.0 ** -20 + torch.finfo(DTYPES[dtype]).eps / 2
+    least = 2.0 ** -25 if dtype == "f16" else 0.0
+    assert (np.abs(got - ref) <= rel * (1 + 2.0 ** -7) * np.abs(ref) + least).all(), np.max(
+        np.abs(got - ref) / (np.abs(ref) + 1e-300))
