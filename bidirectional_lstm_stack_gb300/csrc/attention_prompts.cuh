@@ -150,43 +150,6 @@ Layout layout(int values)
 }
 
 // ---- parts -----------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float low_float(uint32_t pair) { return __uint_as_float(pair << 16); }
-__device__ __forceinline__ float high_float(uint32_t pair)
-{
-    return __uint_as_float(pair & 0xffff0000u);
-}
-// Two numbers as N pairs of parts: each but the last of three cut off (which leaves the
-// rest exact and of no more than 8 bits in the end), those of two rounded to nearest.
-template <int N>
-__device__ __forceinline__ void split_pair_parts(float x, float y, uint32_t (&r)[N])
-{
-    if constexpr (N == 3) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            asm("prmt.b32 %0, %1, %2, 0x7632;"
-                : "=r"(r[k])
-                : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
-            x -= low_float(r[k]);
-            y -= high_float(r[k]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            r[k] = bf16_pair(x, y);
-            if (k + 1 < N) {
-                x -= low_float(r[k]);
-                y -= high_float(r[k]);
-            }
-        }
-    }
-}
-
 // Eight numbers as N units of 16 bytes, `apart` bytes from each other.
 template <int N>
 __device__ __forceinline__ void store_parts(uint8_t *at, int apart, const float (&f)[8])
@@ -230,8 +193,7 @@ __device__ __forceinline__ void load_parts(const uint8_t *at, int apart, Pair (&
     }
 }
 
-// Four pairs as three units of 16 bytes: the leading 8 bits of each, those of the rest, and
-// what is left.
+// Four pairs as three units of 16 bytes, their parts.
 __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4])
 {
     const Pair minus = make_pair(-1.0f, -1.0f);
@@ -241,9 +203,7 @@ __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = split_pair(f[i]);
-            asm("prmt.b32 %0, %1, %2, 0x7632;"
-                : "=r"(r[i])
-                : "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)));
+            r[i] = k == 0 ? bf16_pair_finite(v.x, v.y) : bf16_pair(v.x, v.y);
             if (k + 1 < kWeighted)
                 f[i] = free_fma2(make_pair(low_float(r[i]), high_float(r[i])), minus, f[i]);
         }
@@ -356,9 +316,10 @@ __device__ __forceinline__ void not_finite(uint8_t *at, int apart, int *first_ba
 {
 #pragma unroll 1
     for (int e = 0; e < 8; ++e, at += 2) {
-        // (of a number that is not finite the first part is neither)
-        const unsigned short first = *reinterpret_cast<const unsigned short *>(at);
-        if ((first & 0x7f80) == 0x7f80) {
+        // (of a number that is not finite the first part is neither, the second where an infinity's
+        // first is the largest number)
+        const unsigned short tell = *reinterpret_cast<const unsigned short *>(at + (N == 3 ? apart : 0));
+        if ((tell & 0x7f80) == 0x7f80) {
             atomicMin(first_bad + e, j);
 #pragma unroll
             for (int k = 0; k < N; ++k)

@@ -22,9 +22,9 @@
 // each then joins its share of the tile's sums through distributed shared memory, in the
 // order of the parts.
 //
-// fp32 goes as bf16: x = x1 + x2 + x3 exactly, each the 8 leading bits of what the ones
-// before it leave, and of the nine products of two numbers' parts the six that reach
-// 2^-24 of the product are summed, the small ones first.  The split, and a copy to
+// fp32 goes as bf16: x = x1 + x2 + x3 exactly, each the nearest to what the ones before it
+// leave, and of the nine products of two numbers' parts the six that reach 2^-24 of the
+// product are summed, the small ones first.  The split, and a copy to
 // 16-byte pitches of 16-bit operands that TMA cannot read in place, is a kernel before.
 #include "dense.cuh"
 
@@ -549,13 +549,6 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
 // one, [part][rows][pitch].  The bits between a row's end and its pitch are not read.
 constexpr int kCopyThreads = 256;
 
-__device__ __forceinline__ float leading(float v, unsigned short *bits)
-{
-    const unsigned u = __float_as_uint(v);
-    *bits = static_cast<unsigned short>(u >> 16);
-    return __uint_as_float(u & 0xffff0000u);
-}
-
 // A matrix and its copy (null: none).
 template <typename T>
 struct Copy {
@@ -594,20 +587,22 @@ operand_kernel(const Copy<T> x, const Copy<T> w, int cols, int pitch, int lanes)
             if constexpr (sizeof(T) == 4) {
                 uint32_t o[kParts][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    unsigned short bits[kParts];
-                    float f = v[j];
-                    const float lead = leading(f, &bits[0]);
-                    // (an infinity or a NaN has no rest; a NaN's leading bits may be an infinity's)
-                    const bool finite = fabsf(f) <= 3.402823466e38f;
-                    if (f != f)
-                        bits[0] = 0x7fc0;
-                    f = finite ? f - lead : 0.0f;
-                    f -= leading(f, &bits[1]);
-                    leading(f, &bits[2]);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t parts[kParts];
+                    split_pair_parts<kParts>(v[2 * j], v[2 * j + 1], parts);
+                    // (an infinity has no rest)
+                    const bool lo = fabsf(v[2 * j]) > 3.402823466e38f,
+                               hi = fabsf(v[2 * j + 1]) > 3.402823466e38f;
+                    if (lo || hi) {
+                        const uint32_t keep = (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+                        parts[0] = (parts[0] & keep) |
+                                   (bf16_pair(v[2 * j], v[2 * j + 1]) & ~keep);
+                        parts[1] &= keep;
+                        parts[2] &= keep;
+                    }
 #pragma unroll
                     for (int k = 0; k < kParts; ++k)
-                        o[k][j / 2] = j % 2 ? o[k][j / 2] | static_cast<uint32_t>(bits[k]) << 16 : bits[k];
+                        o[k][j] = parts[k];
                 }
 #pragma unroll
                 for (int k = 0; k < kParts; ++k)

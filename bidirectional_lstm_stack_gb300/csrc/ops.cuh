@@ -356,6 +356,45 @@ __device__ __forceinline__ void silu_pairs(Pair (&v)[K])
         v[k] = mul2(v[k], reciprocal_pair(e[k]));
 }
 
+// ---- parts of bf16 -----------------------------------------------------------------
+// Two numbers rounded to bf16, in one register.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Those beyond bf16's largest number, infinities too, give it.
+__device__ __forceinline__ uint32_t bf16_pair_finite(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float low_float(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float high_float(uint32_t pair)
+{
+    return __uint_as_float(pair & 0xffff0000u);
+}
+// Two numbers as N pairs of parts, each the rest's nearest.  Three are the whole fp32 number (down
+// to 2^-133, where bf16 ends), and the rests have either sign: of two numbers' nine products of
+// parts the three smallest are 2^-24 of the whole at most and point all ways.  (Parts cut off
+// instead of rounded lose 2^-21, always towards zero.)  An infinity's are bf16's largest number,
+// an infinity and a NaN.
+template <int N>
+__device__ __forceinline__ void split_pair_parts(float x, float y, uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        // (fp32 numbers next to the largest would round to infinity)
+        r[k] = N == 3 && k == 0 ? bf16_pair_finite(x, y) : bf16_pair(x, y);
+        if (k + 1 < N) {
+            x -= low_float(r[k]);
+            y -= high_float(r[k]);
+        }
+    }
+}
+
 template <typename F>
 __device__ __forceinline__ float warp_reduce(float v, F f)
 {

@@ -46,10 +46,13 @@ extern "C" {
  *          calls that may run at the same time need one each
  * 1 <= keys <= LSTM_ATTENTION_MAX_KEYS, 1 <= values <=
  * LSTM_ATTENTION_MAX_VALUES, 1 <= heads <= LSTM_ATTENTION_MAX_HEADS.
- * States are fp32, and what a token adds to them keeps 24 bits.  With 16-bit
- * types the products that make y take the state and the products of queries
- * and keys rounded to parts of bf16 (LSTM_BF16: 8 bits, LSTM_F16: 16); with
- * LSTM_F32 everything keeps 24 bits.
+ * States are fp32.  Products are the tensor cores', whose fp32 sums are cut off
+ * below their last bit, of numbers as parts of bf16.  What a token adds to a
+ * state goes as three parts, 24 bits (its decay's exponential is good to 2^-22).
+ * With 16-bit types the products that make y take the state and the products of
+ * queries and keys rounded to parts of bf16 (LSTM_BF16: 8 bits, LSTM_F16: 16).
+ * With LSTM_F32 every factor goes as three parts: a product loses 2^-24 of itself
+ * at most, and what of its factors lies below 2^-133.
  * An infinity or a NaN makes what depends on it, itself or through a state,
  * infinite or NaN; tokens before it, other heads and sequences are as without.
  * Few sequences and heads are cut into spans that run side by side (whence the
@@ -103,8 +106,10 @@ enum {
  *   y        : device [rows][out]
  *   workspace: as lstm_linear_attention's; lstm_dense_workspace(...) bytes
  * rows, in and out are at most LSTM_DENSE_MAX.
- * Products and sums are fp32, with LSTM_F32 too (each product keeps 24 bits of
- * its factors).  16-bit x and w whose rows all start on 16-byte boundaries are
+ * Sums are the tensor cores', in fp32 and cut off below their last bit (up to
+ * three rows: fp32's).  With LSTM_F32 factors go as three parts of bf16: a product
+ * loses 2^-24 of itself at most, and what of its factors lies below 2^-133.
+ * LSTM_ACT_GELU's factor is good to 2^-20 of itself, however small.  16-bit x and w whose rows all start on 16-byte boundaries are
  * read in place, and so is everything up to three rows; others, and fp32, go
  * through the workspace first.
  * An infinity or a NaN in x or w makes its row's or column's results infinite

@@ -534,3 +534,18 @@ def test_rows_before_the_first_sequence_of_a_call_in_spans(dtype, again, first, 
     assert out[0][0].isfinite().all() and out[0][1].isfinite().all()
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
     assert torch.equal(out[1][1][n:], start[n:])
+
+
+def test_products_of_fp32_numbers_keep_their_bits():
+    # Sequences of one token, one key and one value: y is (q k) v and the state k v.  Of a product of
+    # three parts each 2^-24 is left out, and its last sum is cut off below 2^-23 of itself: 1.5 x 2^-23
+    # and a little for each product.
+    g = gen(2)
+    n = 300
+    q, k, v = (1.0 + uniform(g, n, 1, 1) for _ in range(3))
+    for m in (q, k, v):
+        m[:4, 0, 0] = torch.tensor([1.0078124, 1.0039062, 1.9960936, 1.00390612], device="cuda")
+    state = torch.zeros(n, 1, 1, 1, device="cuda")
+    y = binding.lstm_linear_attention(q, k, v, torch.zeros(1, device="cuda"), sequences=n, state=state)
+    for got, ref, off in ((y, f64(q) * f64(k) * f64(v), 2.0 ** -21), (state[..., 0], f64(k) * f64(v), 2.0 ** -22)):
+        assert (np.abs(f64(got) - ref) <= off * ref).all(), np.max(np.abs(f64(got) / ref - 1))

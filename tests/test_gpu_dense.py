@@ -276,3 +276,31 @@ def test_gelu_keeps_its_relative_accuracy_far_out(dtype, rows):
     least = 2.0 ** -25 if dtype == "f16" else 0.0
     assert (np.abs(got - ref) <= rel * (1 + 2.0 ** -7) * np.abs(ref) + least).all(), np.max(
         np.abs(got - ref) / (np.abs(ref) + 1e-300))
+
+
+@pytest.mark.parametrize("rows", [1, 4, 70, 400])
+def test_products_of_fp32_numbers_keep_their_bits(rows):
+    # Of a product of three parts each, 2^-24 is left out; sums are cut off below 2^-23 of
+    # themselves, and those before the last are 2^-7 of it: 1.5 x 2^-23 and a little.
+    g = gen(2)
+    x, w = (1.0 + torch.rand(n, generator=g, device="cuda") for n in (rows, 96))
+    x[0] = w[0] = 1.0078124  # (all ones behind the first eight bits)
+    w[1] = 1.9960936
+    x, w = (m * torch.exp2(torch.randint(-50, 50, m.shape, generator=g, device="cuda")) for m in (x, w))
+    got = f64(binding.lstm_dense(x[:, None], w[:, None]))
+    ref = np.outer(f64(x), f64(w))
+    assert (np.abs(got - ref) <= 2.0 ** -22 * ref).all(), np.max(np.abs(got / ref - 1))
+
+
+@pytest.mark.parametrize("rows", [1, 8, 70, 400])
+def test_fp32_numbers_next_to_the_largest_and_the_smallest(rows):
+    # as above, and a number's parts end at 2^-133: what lies below half of that is lost
+    values = [3.4028234e38, -3.4e38, 3.39e38, 1e-30, 2.0 ** -110 * 1.2345678, 1.2345678e-36, -1.2345678e-38,
+              1e-40]
+    x = torch.zeros(rows, 2, device="cuda")
+    x[:, 0] = torch.tensor((values * 50)[:rows])
+    w = torch.zeros(5, 2, device="cuda")
+    w[:, 0] = torch.tensor([1.0, -0.5, 0.33333334, 0.99999994, 1.2345678e-7])
+    for a, b in ((x, w), (torch.cat([w] * 80)[:max(rows, 4)], x[:8])):
+        got, ref = f64(binding.lstm_dense(a, b)), f64(a) @ f64(b).T
+        assert (np.abs(got - ref) <= 2.0 ** -22 * np.abs(ref) + 2.0 ** -133).all()
