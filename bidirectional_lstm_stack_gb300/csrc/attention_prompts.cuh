@@ -193,7 +193,10 @@ __device__ __forceinline__ void load_parts(const uint8_t *at, int apart, Pair (&
     }
 }
 
-// Four pairs as three units of 16 bytes, their parts.
+// Four pairs as three units of 16 bytes, their parts.  With ROUND they are split_pair_parts'; cut
+// off they have the number's sign, so that a product beyond fp32's range overflows to its side:
+// where the other factor is one part, nothing is left out and rounding gains nothing.
+template <bool ROUND>
 __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4])
 {
     const Pair minus = make_pair(-1.0f, -1.0f);
@@ -203,7 +206,12 @@ __device__ __forceinline__ void store_three(uint8_t *at, int apart, Pair (&f)[4]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 v = split_pair(f[i]);
-            r[i] = k == 0 ? bf16_pair_finite(v.x, v.y) : bf16_pair(v.x, v.y);
+            if (ROUND)
+                r[i] = k == 0 ? bf16_pair_finite(v.x, v.y) : bf16_pair(v.x, v.y);
+            else
+                asm("prmt.b32 %0, %1, %2, 0x7632;"
+                    : "=r"(r[i])
+                    : "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)));
             if (k + 1 < kWeighted)
                 f[i] = free_fma2(make_pair(low_float(r[i]), high_float(r[i])), minus, f[i]);
         }
@@ -596,7 +604,7 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                     }
 #pragma unroll
                 for (int t = 0; t < kTurns; ++t)
-                    store_three(to + t * kRows * kRowBytes, part, f[t]);
+                    store_three<(P::kIn > 1)>(to + t * kRows * kRowBytes, part, f[t]);
                 const float2 any = split_pair(none);
                 if (rare(any.x != 0.0f || any.y != 0.0f)) {
 #pragma unroll 1

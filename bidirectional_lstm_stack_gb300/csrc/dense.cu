@@ -26,6 +26,8 @@
 // leave, and of the nine products of two numbers' parts the six that reach 2^-24 of the
 // product are summed, the small ones first.  The split, and a copy to
 // 16-byte pitches of 16-bit operands that TMA cannot read in place, is a kernel before.
+#include <math_constants.h>
+
 #include "dense.cuh"
 
 namespace lstm {
@@ -44,6 +46,8 @@ constexpr int PRODUCER_WARP = 0, MMA_WARP = 1;
 constexpr int SLICE_BYTES = 32 * 128;  // a warp's 32 rows of 128 bytes on their way out
 
 struct DenseArgs {
+    const void *x, *w;
+    long long x_stride, w_stride;
     const float *bias;
     const void *residual;
     void *y;
@@ -98,6 +102,47 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float (&f)[N])
 #pragma unroll
     for (int i = 0; i < N; ++i)
         f[i] = __uint_as_float(r[i]);
+}
+
+// fp32's own sum where that of the parts is infinite: parts have either sign, so that a product
+// beyond 2^136 overflows to an infinity of either sign before its largest part joins the sum.
+__device__ __forceinline__ float overflowed(const float *x, const float *w, int in)
+{
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < in; ++k)
+        sum = fmaf(__ldg(x + k), __ldg(w + k), sum);
+    return sum;
+}
+// The same for `count` columns of an accumulator, by all lanes of a warp: column c is the sum of
+// rows x + c * dx and w + c * dw, and the lane has `there` of them.  Out of line and back through
+// tensor memory, since this is for few results and takes no register of the others'; its callers
+// read the columns once more in a loop (where the second reading had code of its own, the
+// activations lost a third of their speed).
+__device__ __noinline__ void mend_columns(uint32_t taddr, int count, int there, const float *x,
+                                          const float *w, long long dx, long long dw, int in)
+{
+    for (int c = 0; c < count; ++c) {
+        uint32_t v;
+        ptx::tmem_ld_32x32b_x1(taddr + c, v);
+        ptx::tmem_ld_wait();
+        if (fabsf(__uint_as_float(v)) == CUDART_INF_F && c < there)
+            v = __float_as_uint(overflowed(x + c * dx, w + c * dw, in));
+        __syncwarp();
+        ptx::tmem_st_32x32b_x1(taddr + c, v);
+    }
+    ptx::tmem_st_wait();
+}
+__device__ __forceinline__ bool infinite(float v) { return fabsf(v) == CUDART_INF_F; }
+// of any lane of the warp
+template <int N>
+__device__ __forceinline__ bool any_infinite(const float (&f)[N])
+{
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        any |= infinite(f[j]);
+    return __builtin_expect(__any_sync(0xffffffffu, any), 0);
 }
 
 template <class S, typename T>
@@ -323,6 +368,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                         continue;
                     const uint32_t at = base + (row * S::SUM_PITCH + col) * 4;
                     float f[4] = {};
+                    bool any = false;
 #pragma unroll 4
                     for (int k = 0; k < p.split; ++k) {
                         float v[4];
@@ -330,11 +376,21 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                                      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                                      : "r"(ptx::map_to_rank(at, k)));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int j = 0; j < 4; ++j) {
                             f[j] += v[j];
+                            any |= sizeof(T) == 4 && infinite(v[j]);
+                        }
                     }
                     const long long r = row0 + row;
                     const int n = col0 + col, there = min(4, wide - col);
+                    if (any) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < there && !(fabsf(f[j]) < CUDART_INF_F))
+                                f[j] = overflowed(static_cast<const float *>(p.x) + r * p.x_stride,
+                                                  static_cast<const float *>(p.w) + (n + j) * p.w_stride,
+                                                  p.in);
+                    }
                     T *const to = y + r * p.y_stride + n;
                     const T *const res = residual ? residual + r * p.residual_stride + n : nullptr;
 #pragma unroll
@@ -357,7 +413,19 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 const float bias = p.bias && n < p.out ? __ldg(p.bias + n) : 0.0f;
                 for (int c0 = turn * CW; c0 < BN && n0 + c0 < p.rows; c0 += TURNS * CW) {
                     float f[CW];
-                    read_columns<CW>(acc + c0, f);
+                    bool first = true;
+#pragma unroll 1
+                    while (true) {
+                        read_columns<CW>(acc + c0, f);
+                        if (!(sizeof(T) == 4 && first && any_infinite(f)))
+                            break;
+                        first = false;
+                        const long long r = n0 + c0;
+                        mend_columns(acc + c0, CW, n < p.out ? p.rows - n0 - c0 : 0,
+                                     static_cast<const float *>(p.x) + r * p.x_stride,
+                                     static_cast<const float *>(p.w) + n * p.w_stride, p.x_stride, 0,
+                                     p.in);
+                    }
 #pragma unroll
                     for (int j = 0; j < CW; ++j) {
                         const long long r = n0 + c0 + j;
@@ -410,9 +478,20 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                     }
 #pragma unroll
                     for (int h = 0; h < WIDE; h += CW) {
-                        float f[CW];
-                        read_columns<CW>(acc + c0 + h, f);
                         const int n = n0 + c0 + h;
+                        float f[CW];
+                        bool first = true;
+#pragma unroll 1
+                        while (true) {
+                            read_columns<CW>(acc + c0 + h, f);
+                            if (!(sizeof(T) == 4 && first && any_infinite(f)))
+                                break;
+                            first = false;
+                            mend_columns(acc + c0 + h, CW, r < p.rows ? p.out - n : 0,
+                                         static_cast<const float *>(p.x) + r * p.x_stride,
+                                         static_cast<const float *>(p.w) + n * p.w_stride, 0,
+                                         p.w_stride, p.in);
+                        }
                         if (p.bias && p.whole && n + CW <= p.out) {
 #pragma unroll
                             for (int j = 0; j < CW; j += 4) {
@@ -590,15 +669,16 @@ operand_kernel(const Copy<T> x, const Copy<T> w, int cols, int pitch, int lanes)
                 for (int j = 0; j < 4; ++j) {
                     uint32_t parts[kParts];
                     split_pair_parts<kParts>(v[2 * j], v[2 * j + 1], parts);
-                    // (an infinity has no rest)
-                    const bool lo = fabsf(v[2 * j]) > 3.402823466e38f,
-                               hi = fabsf(v[2 * j + 1]) > 3.402823466e38f;
+                    // An infinity's are 1, 0 and itself: it meets the other number's first part,
+                    // which has that number's sign, and another infinity's 1, but no part that
+                    // happens to be zero.
+                    const bool lo = fabsf(v[2 * j]) == CUDART_INF_F, hi = fabsf(v[2 * j + 1]) == CUDART_INF_F;
                     if (lo || hi) {
                         const uint32_t keep = (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
-                        parts[0] = (parts[0] & keep) |
-                                   (bf16_pair(v[2 * j], v[2 * j + 1]) & ~keep);
+                        parts[2] = (parts[2] & keep) | (bf16_pair(v[2 * j], v[2 * j + 1]) & ~keep);
                         parts[1] &= keep;
-                        parts[2] &= keep;
+                        parts[0] = (parts[0] & keep) |
+                                   (bf16_pair(copysignf(1.0f, v[2 * j]), copysignf(1.0f, v[2 * j + 1])) & ~keep);
                     }
 #pragma unroll
                     for (int k = 0; k < kParts; ++k)
@@ -862,7 +942,7 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
     if ((st = map(&x_map, x_copy, x, x_stride, rows, plan.x_rows())) ||
         (st = map(&w_map, w_copy, w, w_stride, out, plan.w_rows())))
         return st;
-    DenseArgs p = {bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
+    DenseArgs p = {x, w, x_stride, w_stride, bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
                    dtype == LSTM_F32 ? kProducts : 1, 1, false, false, false, 1};
     p.whole = rows_aligned(bias, 0, 4);
     // (whole vectors: what lies behind a row's last numbers is not read)

@@ -53,8 +53,8 @@ extern "C" {
  * queries and keys rounded to parts of bf16 (LSTM_BF16: 8 bits, LSTM_F16: 16).
  * With LSTM_F32 every factor goes as three parts: a product loses 2^-24 of itself
  * at most, and what of its factors lies below 2^-133.
- * An infinity or a NaN makes what depends on it, itself or through a state,
- * infinite or NaN; tokens before it, other heads and sequences are as without.
+ * An infinity or a NaN, or a product beyond fp32, makes what depends on it, itself
+ * or through a state, infinite (of either sign) or NaN; tokens before it, other heads and sequences are as without.
  * Few sequences and heads are cut into spans that run side by side (whence the
  * workspace): a state's sums are then made in another order, which sizes alone
  * decide, so that the same call gives the same bits.
@@ -109,11 +109,13 @@ enum {
  * Sums are the tensor cores', in fp32 and cut off below their last bit (up to
  * three rows: fp32's).  With LSTM_F32 factors go as three parts of bf16: a product
  * loses 2^-24 of itself at most, and what of its factors lies below 2^-133.
- * LSTM_ACT_GELU's factor is good to 2^-20 of itself, however small.  16-bit x and w whose rows all start on 16-byte boundaries are
- * read in place, and so is everything up to three rows; others, and fp32, go
- * through the workspace first.
- * An infinity or a NaN in x or w makes its row's or column's results infinite
- * or NaN.  Waits inside the kernel are bounded as lstm_linear_attention's.
+ * LSTM_ACT_GELU's factor is good to 2^-20 of itself, however small.
+ * 16-bit x and w whose rows all start on 16-byte boundaries are read in place, and
+ * so is everything up to three rows; others, and fp32, go through the workspace
+ * first.
+ * An infinity or a NaN in x or w, and a product beyond fp32, give what fp32 sums
+ * give, infinite or NaN.  Waits inside the kernel are bounded as
+ * lstm_linear_attention's.
  * Errors: LSTM_E_INVALID, LSTM_E_LENGTH (workspace), LSTM_E_OVERFLOW,
  * LSTM_E_DEVICE, LSTM_E_CUDA. */
 size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w, long long w_stride,

@@ -304,3 +304,40 @@ def test_fp32_numbers_next_to_the_largest_and_the_smallest(rows):
     for a, b in ((x, w), (torch.cat([w] * 80)[:max(rows, 4)], x[:8])):
         got, ref = f64(binding.lstm_dense(a, b)), f64(a) @ f64(b).T
         assert (np.abs(got - ref) <= 2.0 ** -22 * np.abs(ref) + 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 70, 400])
+def test_infinities_of_fp32_give_what_one_product_gives(rows):
+    inf = float("inf")
+    values = torch.tensor([inf, -inf, 1.0, -2.0, 0.1, 1e30, -1e-30, 0.0], device="cuda")
+    x, w = torch.zeros(rows, 100, device="cuda"), torch.zeros(8, 100, device="cuda")
+    x[:, 0], w[:, 0] = values.repeat(50)[:rows], values
+    got = binding.lstm_dense(x, w)
+    ref = x[:, :1] * w[:, 0]
+    far = ref.abs() == inf
+    assert torch.equal(got.isnan(), ref.isnan()) and torch.equal(got[far], ref[far])
+    # beside finite products, and two infinities that cancel
+    x, w = normal(gen(1), rows, 100), normal(gen(2), 8, 100)
+    x[0, 40] = inf
+    got = binding.lstm_dense(x, w)
+    assert torch.equal(got[0], torch.copysign(torch.full_like(w[:, 40], inf), w[:, 40]))
+    assert got[1:].isfinite().all()
+    x[0, 41] = torch.copysign(torch.tensor(inf), -w[0, 40] * w[0, 41])
+    assert binding.lstm_dense(x, w)[0, 0].isnan()
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(1, 40, 60), (5, 40, 60), (40, 2100, 300), (70, 40, 60),
+                                             (130, 1500, 200), (2000, 40, 1000), (5000, 40, 520)])
+def test_fp32_products_that_overflow_do_so_to_their_own_side(rows, n_in, n_out):
+    g = gen(7)
+    x, w = (1.0 + torch.rand(n, n_in, generator=g, device="cuda") for n in (rows, n_out))
+    ref = binding.lstm_dense(x, w)
+    x[rows // 2] *= 1e30   # times 1e12 of two columns: far beyond, and to either side
+    w[7] *= 1e12
+    w[n_out - 1] *= -1e25
+    got = binding.lstm_dense(x, w)
+    assert (got[rows // 2, 7], got[rows // 2, n_out - 1]) == (float("inf"), -float("inf"))
+    keep = [c for c in range(n_out) if c not in (7, n_out - 1)]
+    assert got[:, keep].isfinite().all()
+    others = [r for r in range(rows) if r != rows // 2]
+    assert torch.equal(got[others][:, keep], ref[others][:, keep]) and got[others].isfinite().all()
