@@ -396,7 +396,8 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < there) {
-                            float v = activate(p.activation, f[j] + (p.bias ? __ldg(p.bias + n + j) : 0.0f));
+                            const float bias = p.bias ? __ldg(p.bias + n + j) : 0.0f;
+                            float v = activate<sizeof(T) == 4>(p.activation, f[j] + bias);
                             if (res)
                                 v += Elem<T>::get(res[j]);
                             to[j] = Elem<T>::put(v);
@@ -430,7 +431,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                     for (int j = 0; j < CW; ++j) {
                         const long long r = n0 + c0 + j;
                         if (r < p.rows && n < p.out) {
-                            float v = activate(p.activation, f[j] + bias);
+                            float v = activate<sizeof(T) == 4>(p.activation, f[j] + bias);
                             if (residual)
                                 v += Elem<T>::get(residual[r * p.residual_stride + n]);
                             y[r * p.y_stride + n] = Elem<T>::put(v);
@@ -509,7 +510,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                         if (p.activation != LSTM_ACT_NONE) {
 #pragma unroll
                             for (int j = 0; j < CW; ++j)
-                                f[j] = activate(p.activation, f[j]);
+                                f[j] = activate<sizeof(T) == 4>(p.activation, f[j]);
                         }
                         if (residual) {
                             const T *res = residual + r * p.residual_stride + n;
@@ -942,8 +943,8 @@ extern "C" int lstm_dense(const void *x, long long x_stride, const void *w, long
     if ((st = map(&x_map, x_copy, x, x_stride, rows, plan.x_rows())) ||
         (st = map(&w_map, w_copy, w, w_stride, out, plan.w_rows())))
         return st;
-    DenseArgs p = {x, w, x_stride, w_stride, bias, residual, y, residual_stride, y_stride, rows, in, out, activation,
-                   dtype == LSTM_F32 ? kProducts : 1, 1, false, false, false, 1};
+    DenseArgs p = {x, w, x_stride, w_stride, bias, residual, y, residual_stride, y_stride, rows, in,
+                   out, activation, dtype == LSTM_F32 ? kProducts : 1, 1, false, false, false, 1};
     p.whole = rows_aligned(bias, 0, 4);
     // (whole vectors: what lies behind a row's last numbers is not read)
     p.vectors = residual && rows_aligned(residual, rows > 1 ? residual_stride : 0, size) &&

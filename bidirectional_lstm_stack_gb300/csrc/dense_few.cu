@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs p, in
         v += sums[g * split + s][at];
     if (p.bias)
         v += __ldg(p.bias + n);
-    v = activate(p.activation, v);
+    v = activate<sizeof(T) == 4>(p.activation, v);
     if (p.residual)
         v += Elem<T>::get(static_cast<const T *>(p.residual)[r * p.residual_stride + n]);
     static_cast<T *>(p.y)[r * p.y_stride + n] = Elem<T>::put(v);

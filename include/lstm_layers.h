@@ -109,7 +109,8 @@ enum {
  * Sums are the tensor cores', in fp32 and cut off below their last bit (up to
  * three rows: fp32's).  With LSTM_F32 factors go as three parts of bf16: a product
  * loses 2^-24 of itself at most, and what of its factors lies below 2^-133.
- * LSTM_ACT_GELU's factor is good to 2^-20 of itself, however small.
+ * LSTM_ACT_GELU's factor is good to 2^-20 of itself, however small (16-bit types:
+ * 2^-16).
  * 16-bit x and w whose rows all start on 16-byte boundaries are read in place, and
  * so is everything up to three rows; others, and fp32, go through the workspace
  * first.
