@@ -549,3 +549,26 @@ def test_products_of_fp32_numbers_keep_their_bits():
     y = binding.lstm_linear_attention(q, k, v, torch.zeros(1, device="cuda"), sequences=n, state=state)
     for got, ref, off in ((y, f64(q) * f64(k) * f64(v), 2.0 ** -21), (state[..., 0], f64(k) * f64(v), 2.0 ** -22)):
         assert (np.abs(f64(got) - ref) <= off * ref).all(), np.max(np.abs(f64(got) / ref - 1))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("keys,values", [(64, 64), (128, 128), (40, 200)])
+@pytest.mark.parametrize("lengths", [[64], [300, 17], [3000]])
+def test_states_keep_their_bits(dtype, keys, values, lengths):
+    # Of the norm: a weight's exponential is off by 2^-22, and the decays between chunks, of e^-3 and
+    # less, add a twentieth to that; the tensor cores' sums are cut off below 2^-23 of themselves at
+    # the four blocks of 16 tokens that make a chunk's, 2^-21; the sum with the state is rounded once
+    # (2^-24), and a product loses 2^-24: below 2^-20.  (Two parts of w v instead of three would
+    # leave 2^-17 of a term.)
+    tokens, n = sum(lengths), len(lengths)
+    q, k, v = _inputs(dtype, tokens, 2, keys, values)
+    d = torch.full((tokens, 2), -0.05, device="cuda") * (0.9 + 0.2 * uniform(gen(4), tokens, 2))
+    state = torch.zeros(n, 2, keys, values, device="cuda")
+    offsets = np.concatenate([[0], np.cumsum(lengths)])
+    binding.lstm_linear_attention(q, k, v, d, offsets=_i32(offsets), state=state)
+    k, v, d = (x.double() for x in (k, v, d))
+    for s in range(n):
+        a, b = offsets[s], offsets[s + 1]
+        w = torch.exp(d[a:b].flip(0).cumsum(0).flip(0) - d[a:b])
+        ref = torch.einsum("th,thk,thv->hkv", w, k[a:b], v[a:b])
+        assert (state[s].double() - ref).norm() <= 2.0 ** -20 * ref.norm()

@@ -343,3 +343,24 @@ def test_fp32_products_that_overflow_do_so_to_their_own_side(rows, n_in, n_out):
     assert got[:, keep].isfinite().all()
     others = [r for r in range(rows) if r != rows // 2]
     assert torch.equal(got[others][:, keep], ref[others][:, keep]) and got[others].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [2, 5, 40, 200, 5000])
+def test_values_that_are_not_finite_of_every_type_and_through_each_activation(dtype, rows):
+    g, t = gen(1), DTYPES[dtype]
+    x, w = normal(g, rows, 100, dtype=t), normal(g, 150, 100, dtype=t)
+    y = binding.lstm_dense(x, w)
+    x[1, 40], w[70, 99], w[90, 0] = float("inf"), float("nan"), float("-inf")
+    got = binding.lstm_dense(x, w)
+    assert not got[1].isfinite().any() and not got[:, [70, 90]].isfinite().any()
+    keep = torch.ones_like(y, dtype=torch.bool)
+    keep[1] = False
+    keep[:, [70, 90]] = False
+    assert torch.equal(got[keep], y[keep])
+    # of the residual and the bias too, and nothing is hidden by an activation
+    r, b = torch.zeros(rows, 150, dtype=t, device="cuda"), torch.zeros(150, device="cuda")
+    r[0, 5], b[6] = float("nan"), float("nan")
+    for activation in (None, "relu", "gelu", "gelu_tanh", "silu"):
+        got = binding.lstm_dense(x, w, b, activation=activation, residual=r)
+        assert got[0, 5].isnan() and got[:, 6].isnan().all() and got[:, 70].isnan().all()
