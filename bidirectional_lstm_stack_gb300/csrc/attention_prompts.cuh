@@ -6,7 +6,7 @@
 // transposed: tensor-memory lanes are values, so every product has M = 128 lanes and no
 // state ever goes through shared memory.  Per chunk the tensor cores make
 //     scores   Q K^T            [64 queries x 64 keys]   (lanes are queries)
-//     inter    S^T Q^T          [values x 64 queries]    (S^T in tensor memory, bf16)
+//     inter    S^T Q^T          [values x 64 queries]    (S^T in tensor memory)
 //     intra    V^T P^T          [values x 64 queries]    (P: decayed, masked scores)
 //     update   (wV)^T K         [values x keys]          (w_j = e^(c_64 - c_j))
 // and the warps have one task each:
@@ -17,26 +17,27 @@
 //    what separates near tokens;
 //  * 3 warps turn scores into P, 4 others inter and intra into y, a chunk behind;
 //  * 4 or 8 state warps hold S in registers (fp32, a lane per value), add the update and hand
-//    S on as bf16;
+//    S on as parts of bf16;
 //  * with TMA the loaders' warps write w v of the next chunk, else the state warps do;
 //  * two threads issue the products, those of the outputs and those of the states, so that
 //    neither chain waits for the other.
 // Where sequences and heads are fewer than SMs, sequences are cut into spans: a first pass
 // makes what each span adds to a state of zeros (no outputs), a small kernel joins them to
 // the states that the spans start from, and then all spans run side by side.
-// bf16 inputs are exact operands.  P and S are rounded to bf16 for their products (an
-// output of bf16 is rounded as coarsely itself); w v goes as three parts of bf16, so that
-// what joins the state, which is fp32, keeps 24 bits (two parts left 2.4e-6 of it).  fp16
-// goes as two parts of bf16 (exact), so do P and S (which in fp16 itself would overflow);
-// fp32 as three parts (exact), and so do P and S.  Of two factors' parts those products are
-// made that the other roundings leave visible (parts a, b with a + b below the larger number
-// of parts).
+// bf16 inputs are exact operands.  P and S go as two parts of bf16 for their products, 2^-17 of
+// them off, where an output of 16 bits is rounded to 2^-8 or 2^-11 itself (with one part y was off
+// by 2.35e-3 of its norm, 1.66e-3 of which are its own rounding, and a prompt's outputs were not
+// its single tokens'; a chunk took 1.97 us then and takes 2.42).  w v goes as three parts, so that
+// what joins the state, which is fp32, keeps 24 bits (two parts left 2.4e-6 of it).  fp16 inputs
+// are two parts of bf16 (exact; P and S in fp16 itself would overflow); fp32 three parts (exact),
+// and so are P and S.  Of two factors' parts those products are made that the other roundings
+// leave visible (parts a, b with a + b below the larger number of parts).
 //
 // What bounds it: with bf16 and 128 keys and values a chunk's products take the tensor core
-// 1 700 cycles (scores 8 x 51, inter 8 x 35, intra 4 x 51, update 12 x 67), shared memory some
-// 2 600 and the ALU pipe 1 800; the warps' chains, whose instructions exceed the instruction
-// cache, make it 3 980.  16 heads of a prompt of 4096 tokens take 50 us (68 MB: 10 us), four
-// prompts of 16384 tokens 420 us (675 MB: 99 us).  Waits, loops and rare branches are kept
+// 2 180 cycles (scores 8 x 51, inter 16 x 35, intra 8 x 51, update 12 x 67), shared memory some
+// 2 700 and the ALU pipe 2 200; the warps' chains, whose instructions exceed the instruction
+// cache, make it 5 000.  16 heads of a prompt of 4096 tokens take 52 us (68 MB: 10 us), four
+// prompts of 16384 tokens 478 us (675 MB: 99 us).  Waits, loops and rare branches are kept
 // short for that reason: inlining a wait's clock and messages at its 20 places cost a quarter
 // of the time at 64 keys.
 #pragma once
@@ -58,7 +59,7 @@ template <typename T>
 struct Parts;
 template <>
 struct Parts<__nv_bfloat16> {
-    static constexpr int kIn = 1, kMid = 1;
+    static constexpr int kIn = 1, kMid = 2;
 };
 template <>
 struct Parts<__half> {
@@ -100,6 +101,11 @@ struct Info {
 };
 constexpr int kOrdered = 64;  // sequences that a block puts in order for itself
 constexpr int kInfos = 8;
+// Tokens of y that an output warp stores at a time: with 64 there is no room for a third stage at
+// 128 keys and values of bf16 (a chunk takes 2.54 us then, 2.41 so), at 64 keys there is (1.65 us,
+// 1.87 with 32).
+template <int KP>
+constexpr int kOutRows = KP == 128 ? 32 : C;
 // V's tile is clean: its weighing is two chunks ahead of the outputs at most
 constexpr int kCleans = 4;
 
@@ -133,7 +139,7 @@ Layout layout(int values)
     l.weighted = kWeighted * l.tile_v;
     l.p = P::kMid * kSlab;
     // y on its way out, 32 values of a row side by side (fp32 rows are as wide as a warp's store)
-    l.staging = sizeof(T) == 2 ? 4 * C * 32 * 2 : 0;
+    l.staging = sizeof(T) == 2 ? 4 * kOutRows<KP> * 32 * 2 : 0;
     // (products of 128 lanes read past tiles of 64, into the tile behind them)
     const size_t rest = l.weighted + l.staging + kMaxStages * sizeof(Decays) + kInfos * sizeof(Info) +
                         sizeof(Barriers) + 1024;
@@ -676,9 +682,35 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         const int quarter = warp & 3, v = quarter * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         T *const first = p.out<T>(run.begin, head) + v0 + quarter * 32;
-        T *const slice = reinterpret_cast<T *>(staging) + quarter * (C * 32);
+        T *const slice = reinterpret_cast<T *>(staging) + quarter * (kOutRows<KP> * 32);
         const int width = values - quarter * 32;  // of this warp's values
         const Pair scale = make_pair(p.scale, p.scale);
+        // tokens from `begin` on of a chunk of `len`, whose y is in the slice
+        const auto store = [&](T *at, int begin, int len) {
+            __syncwarp();
+            T *const to = at + begin * p.y_stride;
+            const int rows = min(len - begin, kOutRows<KP>);
+            if (aligned & 8) {
+                // 8 values of 8 rows at a time
+                const int col = (lane & 3) * 8;
+#pragma unroll 1
+                for (int e0 = lane >> 2; e0 < rows; e0 += 32) {
+                    Pack<T, 8> some[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        some[n] = *reinterpret_cast<const Pack<T, 8> *>(slice + (e0 + n * 8) * 32 + col);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (e0 + n * 8 < rows && col < width)
+                            store_pack<T, 8>(to + (e0 + n * 8) * p.y_stride + col, some[n]);
+                }
+            } else if (lane < width) {
+#pragma unroll 1
+                for (int e = 0; e < rows; ++e)
+                    to[e * p.y_stride + lane] = slice[e * 32 + lane];
+            }
+            __syncwarp();
+        };
         for (int c = 0; outputs && c < chunks; ++c) {
             const int b = c & 1, ib = c & (Col::kInters - 1);
             wait(&bar.inter_full[ib], parity_of(c, Col::kInters), kFaultEpilogue);
@@ -724,7 +756,9 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
                     if constexpr (sizeof(T) == 2) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            slice[(e0 + e) * 32 + lane] = Elem<T>::put(f[e]);
+                            slice[((e0 & (kOutRows<KP> - 1)) + e) * 32 + lane] = Elem<T>::put(f[e]);
+                        if (kOutRows<KP> < C && (e0 & 16))
+                            store(at, e0 - 16, len);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -737,28 +771,8 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
             }
             ptx::tc_fence_before();
             arrive(&bar.y_free[b]);
-            if constexpr (sizeof(T) == 2) {
-                if (aligned & 8) {
-                    // 8 values of 8 rows at a time
-                    const int col = (lane & 3) * 8;
-#pragma unroll 1
-                    for (int e0 = lane >> 2; e0 < len; e0 += 32) {
-                        Pack<T, 8> some[4];
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            some[n] = *reinterpret_cast<const Pack<T, 8> *>(slice + (e0 + n * 8) * 32 + col);
-#pragma unroll
-                        for (int n = 0; n < 4; ++n)
-                            if (e0 + n * 8 < len && col < width)
-                                store_pack<T, 8>(at + (e0 + n * 8) * p.y_stride + col, some[n]);
-                    }
-                } else if (lane < width) {
-#pragma unroll 1
-                    for (int e = 0; e < len; ++e)
-                        at[e * p.y_stride + lane] = slice[e * 32 + lane];
-                }
-                __syncwarp();
-            }
+            if (sizeof(T) == 2 && kOutRows<KP> == C)
+                store(at, 0, len);
         }
     } else if (warp >= W::kState && warp < W::kLoad) {
         // ---- states: w v, S, and S as an operand ----

@@ -572,3 +572,25 @@ def test_states_keep_their_bits(dtype, keys, values, lengths):
         w = torch.exp(d[a:b].flip(0).cumsum(0).flip(0) - d[a:b])
         ref = torch.einsum("th,thk,thv->hkv", w, k[a:b], v[a:b])
         assert (state[s].double() - ref).norm() <= 2.0 ** -20 * ref.norm()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("keys,values", [(64, 64), (128, 128), (40, 200)])
+@pytest.mark.parametrize("lengths", [[200], [1000, 300]])
+def test_outputs_of_16_bits_are_off_by_their_own_rounding(dtype, keys, values, lengths):
+    # P and S are rounded to two parts of bf16, 2^-17 of themselves, and to either side: of the norm
+    # some 2^-16, for which 2^-12 leaves room, where one part each would add 2^-10.  The rounding's own
+    # norm is known from these outputs' to a few hundredths.
+    tokens = sum(lengths)
+    q, k, v = _inputs(dtype, tokens, 2, keys, values)
+    d = _decays(gen(4), "each", tokens, 2)
+    state = normal(gen(5), len(lengths), 2, keys, values)
+    start = f64(state)
+    offsets = np.concatenate([[0], np.cumsum(lengths)])
+    got = f64(binding.lstm_linear_attention(q, k, v, d, offsets=_i32(offsets), state=state,
+                                            resume=_i32([1] * len(lengths)), scale=0.125))
+    ref = oracle.linear_attention(f64(q), f64(k), f64(v), f64(d), 0.125,
+                                  spans(tokens, len(lengths), offsets), dtype, start, None,
+                                  [1] * len(lengths))[0]
+    rounding = np.linalg.norm(f64(torch.tensor(ref).to(DTYPES[dtype])) - ref)
+    assert np.linalg.norm(got - ref) <= 1.05 * rounding + 2.0 ** -12 * np.linalg.norm(ref)
