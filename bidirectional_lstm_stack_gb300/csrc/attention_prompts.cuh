@@ -99,7 +99,10 @@ struct Info {
     float all;           // e^(c_64)
     float pad[3];
 };
-constexpr int kOrdered = 64;  // sequences that a block puts in order for itself
+// Sequences that a block puts in order for itself, which takes it longer the more there are: 24
+// prompts with 32 heads of 64 x 64 take 101 us (131 as they come), 128 with 16 heads 156 (160); 160
+// would take 190 (173).
+constexpr int kOrdered = 128;
 constexpr int kInfos = 8;
 // Tokens of y that an output warp stores at a time: with 64 there is no room for a third stage at
 // 128 keys and values of bf16 (a chunk takes 2.54 us then, 2.41 so), at 64 keys there is (1.65 us,
@@ -450,14 +453,21 @@ attention_kernel(const __grid_constant__ Maps maps, const AttentionArgs p, const
         // the longest sequences' heads go first, so that no long one starts when the others end
         // (the grid is heads x sequences then)
         head = blockIdx.x;
-        const auto length = [&](int n) { return sequence_end(p.seq, n) - sequence_begin(p.seq, n); };
-        if (static_cast<int>(threadIdx.x) < p.seq.count) {
-            const int n = threadIdx.x, own = length(n);
+        int *const lengths = reinterpret_cast<int *>(smem);
+        const int n = threadIdx.x, count = p.seq.count;
+        const int own = n < count ? sequence_end(p.seq, n) - sequence_begin(p.seq, n) : -1;
+        if (n < kOrdered)
+            lengths[n] = own;
+        __syncthreads();
+        if (n < count) {
             int rank = 0;
-#pragma unroll 1
-            for (int m = 0; m < p.seq.count; ++m) {
-                const int other = length(m);
-                rank += other > own || (other == own && m < n);
+#pragma unroll 2
+            for (int m = 0; m < count; m += 4) {
+                const int4 some = *reinterpret_cast<const int4 *>(lengths + m);
+                const int others[4] = {some.x, some.y, some.z, some.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    rank += others[k] > own || (others[k] == own && m + k < n);
             }
             if (rank == static_cast<int>(blockIdx.y))
                 bar.sequence = n;

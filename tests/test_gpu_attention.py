@@ -594,3 +594,12 @@ def test_outputs_of_16_bits_are_off_by_their_own_rounding(dtype, keys, values, l
                                   [1] * len(lengths))[0]
     rounding = np.linalg.norm(f64(torch.tensor(ref).to(DTYPES[dtype])) - ref)
     assert np.linalg.norm(got - ref) <= 1.05 * rounding + 2.0 ** -12 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("count", [3, 126, 127, 128, 129])
+def test_as_many_unequal_sequences_as_blocks_put_in_order(dtype, count):
+    # (no spans: there are blocks enough; some are equal, some empty)
+    lengths = [(i * 53) % 70 if i % 4 else 33 for i in range(count)]
+    assert binding.lstm_linear_attention_workspace(sum(lengths), 208, 8, 8, count, False) == 0
+    _check(dtype, lengths, 208 if count < 100 else 6, 8, 8, pool=count, resume=[i % 2 for i in range(count)])
