@@ -218,7 +218,7 @@ extern "C" size_t lstm_linear_attention_workspace(int tokens, int heads, int key
                                                   int sequences, int equal_lengths)
 {
     if (heads <= 0 || heads > LSTM_ATTENTION_MAX_HEADS || keys <= 0 || keys > LSTM_ATTENTION_MAX_KEYS ||
-        values <= 0 || values > LSTM_ATTENTION_MAX_VALUES)
+        values <= 0 || values > LSTM_ATTENTION_MAX_VALUES || tokens > kMostTokens)
         return 0;
     size_t bytes;
     plan_spans(tokens, heads, keys, values, sequences, equal_lengths != 0, &bytes);

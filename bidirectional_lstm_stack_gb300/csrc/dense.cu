@@ -856,7 +856,9 @@ using namespace lstm;
 extern "C" size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w,
                                        long long w_stride, int dtype, int rows, int in, int out)
 {
-    if (rows <= kFewestRows || in <= 0 || out <= 0)
+    // (nothing for sizes that the call refuses: no memory is asked for in vain)
+    if (rows <= kFewestRows || in <= 0 || out <= 0 || rows > LSTM_DENSE_MAX || in > LSTM_DENSE_MAX ||
+        out > LSTM_DENSE_MAX)
         return 0;
     return Operand(x, x_stride, dtype, rows, in).bytes + Operand(w, w_stride, dtype, out, in).bytes;
 }

@@ -89,6 +89,18 @@ def test_dense_overflow(lib):
         assert _dense(lib, **{size: (1 << 29) + 1}) == OVERFLOW
 
 
+def test_sizes_that_are_refused_need_no_workspace(lib):
+    assert lib.lstm_dense_workspace(64, 16, 64, 16, 0, 1 << 29, 16, 8) > 0
+    for sizes in (((1 << 29) + 1, 16, 8), (4, (1 << 29) + 1, 8), (4, 16, (1 << 29) + 1), (4, 0, 8), (4, 16, -1),
+                  (-4, 16, 8)):
+        assert lib.lstm_dense_workspace(64, 16, 64, 16, 0, *sizes) == 0
+    most = 0x7fffff00
+    assert binding.lstm_linear_attention_workspace(most, 1, 64, 64, 1, True) > 0
+    for sizes in ((most + 1, 1, 64, 64, 1), (1 << 20, 0, 64, 64, 1), (1 << 20, 1, 129, 64, 1),
+                  (1 << 20, 1, 64, 257, 1), (1 << 20, 1, 64, 64, -1), (-5, 1, 64, 64, 1)):
+        assert binding.lstm_linear_attention_workspace(*sizes, True) == 0
+
+
 # ---- the binding ---------------------------------------------------------------------------------
 def _calls(m):
     z = torch.zeros
