@@ -333,9 +333,8 @@ __device__ __forceinline__ void not_finite(uint8_t *at, int apart, int *first_ba
 {
 #pragma unroll 1
     for (int e = 0; e < 8; ++e, at += 2) {
-        // (of a number that is not finite the first part is neither, the second where an infinity's
-        // first is the largest number)
-        const unsigned short tell = *reinterpret_cast<const unsigned short *>(at + (N == 3 ? apart : 0));
+        // (an infinity's first part of several is the largest number, the second an infinity)
+        const unsigned short tell = *reinterpret_cast<const unsigned short *>(at + (N > 1 ? apart : 0));
         if ((tell & 0x7f80) == 0x7f80) {
             atomicMin(first_bad + e, j);
 #pragma unroll

@@ -380,14 +380,14 @@ __device__ __forceinline__ float high_float(uint32_t pair)
 // to 2^-133, where bf16 ends), and the rests have either sign: of two numbers' nine products of
 // parts the three smallest are 2^-24 of the whole at most and point all ways.  (Parts cut off
 // instead of rounded lose 2^-21, always towards zero.)  An infinity's are bf16's largest number,
-// an infinity and a NaN.
+// an infinity and (of three) a NaN.
 template <int N>
 __device__ __forceinline__ void split_pair_parts(float x, float y, uint32_t (&r)[N])
 {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         // (fp32 numbers next to the largest would round to infinity)
-        r[k] = N == 3 && k == 0 ? bf16_pair_finite(x, y) : bf16_pair(x, y);
+        r[k] = N > 1 && k == 0 ? bf16_pair_finite(x, y) : bf16_pair(x, y);
         if (k + 1 < N) {
             x -= low_float(r[k]);
             y -= high_float(r[k]);

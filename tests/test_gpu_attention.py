@@ -603,3 +603,18 @@ def test_as_many_unequal_sequences_as_blocks_put_in_order(dtype, count):
     lengths = [(i * 53) % 70 if i % 4 else 33 for i in range(count)]
     assert binding.lstm_linear_attention_workspace(sum(lengths), 208, 8, 8, count, False) == 0
     _check(dtype, lengths, 208 if count < 100 else 6, 8, 8, pool=count, resume=[i % 2 for i in range(count)])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_states_next_to_the_largest_number(dtype):
+    # 3.4e38 is beyond bf16's largest number; a query of 2^-14 brings it back
+    state = torch.full((1, 1, 16, 16), 3.4e38, device="cuda")
+    q, k, v = (torch.zeros(3, 1, 16, dtype=DTYPES[dtype], device="cuda") for _ in range(3))
+    q[:, :, 5] = 2.0 ** -14
+    y = binding.lstm_linear_attention(q, k, v, torch.zeros(1, device="cuda"), state=state, resume=_i32([1]),
+                                      scale=2.0 ** -100)
+    assert (state == 3.4e38).all()
+    # (no number of these types is near the type's end: the scale brings it to 2^14)
+    ref = float(torch.tensor(3.4e38).double()) * 2.0 ** -114
+    off = 2.0 ** -15 + torch.finfo(DTYPES[dtype]).eps / 2
+    assert ((y.double() - ref).abs() <= off * ref).all()
