@@ -265,8 +265,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
-// Waits for the phase with `parity`; false when `polls` polls, each suspended for up to
-// kSuspendedNs, have not met it.  Of as few instructions as it takes: in a kernel whose warps
+// Waits for the phase with `parity`; false when `polls` polls, each suspended for some
+// kSuspendedNs, have not met it (the hardware takes that for a hint: 3.7 us each, so that polls
+// for two seconds last seven).  Of as few instructions as it takes: in a kernel whose warps
 // all run different code its copies would fill the instruction cache, and each miss there
 // costs more than the wait.
 constexpr unsigned kSuspendedNs = 1000;

@@ -35,7 +35,9 @@ extern "C" {
  *          h / (heads / q_heads) of q, and so on
  *   log_decay : device fp32, decay_stride 0: [heads], the same for every
  *          token; else [tokens][heads] with that row stride (at least heads).
- *          A value of -infinity forgets the state; values are below 88
+ *          A value of -infinity forgets the state; values are below 88, and so
+ *          is every sum of a sequence's consecutive values (e^88 is beyond fp32:
+ *          y and states may be NaN, even where zeros hide the growth)
  *   y    : device [tokens][heads][values], the heads of a token consecutive
  *          and the tokens y_stride apart (at least heads * values)
  *   state : device [state_slots][heads][keys][values] fp32, or NULL: no
@@ -54,11 +56,12 @@ extern "C" {
  * With LSTM_F32 every factor goes as three parts: a product loses 2^-24 of itself
  * at most, and what of its factors lies below 2^-133.
  * An infinity or a NaN, or a product beyond fp32, makes what depends on it, itself
- * or through a state, infinite (of either sign) or NaN; tokens before it, other heads and sequences are as without.
+ * or through a state, infinite (of either sign) or NaN; tokens before it, other heads
+ * and sequences are as without.
  * Few sequences and heads are cut into spans that run side by side (whence the
  * workspace): a state's sums are then made in another order, which sizes alone
  * decide, so that the same call gives the same bits.
- * A wait inside the kernel that does not end within two seconds sets the
+ * A wait inside the kernel that does not end within some eight seconds sets the
  * library's fault word (lstm_fault_status); outputs and states are then
  * unspecified.
  * Errors: LSTM_E_INVALID (null, sizes, type, stride, device), LSTM_E_LENGTH
@@ -115,8 +118,8 @@ enum {
  * so is everything up to three rows; others, and fp32, go through the workspace
  * first.
  * An infinity or a NaN in x or w, and a product beyond fp32, give what fp32 sums
- * give, infinite or NaN.  Waits inside the kernel are bounded as
- * lstm_linear_attention's.
+ * give, infinite or NaN.  A wait inside the kernel that does not end within two
+ * seconds sets the fault word as lstm_linear_attention's.
  * Errors: LSTM_E_INVALID, LSTM_E_LENGTH (workspace), LSTM_E_OVERFLOW,
  * LSTM_E_DEVICE, LSTM_E_CUDA. */
 size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w, long long w_stride,
