@@ -4,10 +4,10 @@ may lose.
 
 Attention: `size` carries the sum of the terms' absolute values through the same
 recurrence as the state; a term's relative error times it bounds the state's
-error.  A term k v e^c is off by its weight's rounding to three parts of bf16 (24 bits, of
-which products lose two), by the exponential, and by sums: at most 64
+error.  A term k v e^c is off by its weight's rounding to three parts of bf16 (24 bits) and
+its product's smallest parts, by the exponential, and by sums: at most 64
 terms of a span are summed in fp32 before they join the state, once a span.  An
-output also takes the state or q.k rounded to one (bf16), two (fp16) or three
+output also takes the state or q.k rounded to two (16-bit types) or three
 (fp32) parts of bf16.
 """
 import math
@@ -16,7 +16,7 @@ import numpy as np
 
 from .ops import U32, slot_of
 
-PARTS = {"bf16": 2.0 ** -8, "f16": 2.0 ** -15, "f32": 2.0 ** -22}
+PARTS = {"bf16": 2.0 ** -15, "f16": 2.0 ** -15, "f32": 2.0 ** -22}
 WEIGHT = 2.0 ** -22
 SUMS = 400  # roundings or truncations of a span's sums and of the exponential
 

@@ -618,3 +618,27 @@ def test_states_next_to_the_largest_number(dtype):
     ref = float(torch.tensor(3.4e38).double()) * 2.0 ** -114
     off = 2.0 ** -15 + torch.finfo(DTYPES[dtype]).eps / 2
     assert ((y.double() - ref).abs() <= off * ref).all()
+
+
+def _far(rows, *sizes, dtype):
+    """[rows, *sizes] whose last rows lie beyond 2^31 elements."""
+    stride = (1 << 31) // rows + 1024
+    stride -= stride % 8
+    at = torch.empty(rows * stride, dtype=dtype, device="cuda").as_strided(
+        (rows, *sizes), (stride, *([sizes[1], 1] if len(sizes) > 1 else [1])))
+    assert (rows - 1) * stride > 1 << 31
+    return at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_beyond_32_bits_of_elements(dtype):
+    tokens, t = 70001, DTYPES[dtype]
+    m = _inputs(dtype, tokens, 2, 16, 24)
+    d = _decays(gen(2), "each", tokens, 2)
+    offsets = _i32([0, 1000, 35000, tokens])
+    ref = binding.lstm_linear_attention(*m, d, offsets=offsets)
+    y = _far(tokens, 2, 24, dtype=t)
+    assert torch.equal(binding.lstm_linear_attention(*m, d, offsets=offsets, y=y), ref)
+    del y
+    far = [_far(tokens, *x.shape[1:], dtype=t).copy_(x) for x in m[:2]]
+    assert torch.equal(binding.lstm_linear_attention(*far, m[2], d, offsets=offsets), ref)

@@ -364,3 +364,17 @@ def test_values_that_are_not_finite_of_every_type_and_through_each_activation(dt
     for activation in (None, "relu", "gelu", "gelu_tanh", "silu"):
         got = binding.lstm_dense(x, w, b, activation=activation, residual=r)
         assert got[0, 5].isnan() and got[:, 6].isnan().all() and got[:, 70].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_beyond_32_bits_of_elements(dtype):
+    rows, t = 70001, DTYPES[dtype]
+    stride = (1 << 31) // rows + 1024
+    stride -= stride % 8
+    x, w = normal(gen(1), rows, 40, dtype=t), normal(gen(2), 48, 40, dtype=t)
+    r = normal(gen(3), rows, 48, dtype=t)
+    ref = binding.lstm_dense(x, w, residual=r)
+    far = torch.empty(rows * stride, dtype=t, device="cuda")
+    y = far.as_strided((rows, 48), (stride, 1)).copy_(r)
+    assert torch.equal(binding.lstm_dense(x, w, residual=y, y=y), ref)
+    assert torch.equal(binding.lstm_dense(far.as_strided((rows, 40), (stride, 1)).copy_(x), w, residual=r), ref)
