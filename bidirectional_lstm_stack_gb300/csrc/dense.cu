@@ -215,6 +215,10 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
         *m = ((static_cast<int>(g) * p.group + static_cast<int>(in_group % tall)) * S::CTAS + rank) * BM;
         *n = static_cast<int>(in_group / tall) * BN;
     };
+    // What a tile takes counts beside the limit: with a K of millions its products outlast any, and
+    // so do fp32 sums that are made again.
+    const uint64_t limit_ns =
+        test.wait_limit_ns + static_cast<uint64_t>(kb_end - kb_begin) * (sizeof(T) == 4 ? 1000000 : 10000);
     int issued = 0;  // K blocks, as far as they matter at the end: the last STAGES
     int committed = 0;
     // the ring's next stage, and the parity of its turn (no divisions: a K block takes the
@@ -240,7 +244,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     // (a stage's first use finds it free)
                     if (!ptx::mbar_wait_bounded(&empty[s], turn ^ 1, abort_flag, fault,
-                                                kFaultProducer, test.wait_limit_ns)) {
+                                                kFaultProducer, limit_ns)) {
                         ok = false;
                         break;
                     }
@@ -281,14 +285,14 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
             const int a = committed % S::ACCS;
             const uint32_t use = static_cast<uint32_t>(committed / S::ACCS);
             bool ok = use == 0 || ptx::mbar_wait_bounded(&acc_empty[a], (use - 1) & 1, abort_flag, fault,
-                                                         kFaultMma, test.wait_limit_ns, S::PAIR);
+                                                         kFaultMma, limit_ns, S::PAIR);
             if (!__all_sync(0xffffffffu, ok))
                 break;
             ptx::tc_fence_after();
             const uint32_t d = tmem + a * BN;
             for (int kb = kb_begin; kb < kb_end; ++kb) {
                 ok = ptx::mbar_wait_bounded(&full[s], turn, abort_flag, fault, kFaultMma,
-                                            test.wait_limit_ns);
+                                            limit_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
@@ -325,7 +329,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
             place(t, &m0, &n0);
             const int a = count % S::ACCS;
             const bool got = ptx::mbar_wait_bounded(&acc_full[a], (count / S::ACCS) & 1, abort_flag,
-                                                    fault, kFaultEpilogue, test.wait_limit_ns);
+                                                    fault, kFaultEpilogue, limit_ns);
             // tcgen05.ld is warp-collective: continue only if every lane may
             const bool ok = __all_sync(0xffffffffu, got) && !*abort_flag;
             ptx::tc_fence_after();

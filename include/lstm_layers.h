@@ -120,7 +120,8 @@ enum {
  * first.
  * An infinity or a NaN in x or w, and a product beyond fp32, give what fp32 sums
  * give, infinite or NaN.  A wait inside the kernel that does not end within two
- * seconds sets the fault word as lstm_linear_attention's.
+ * seconds (and what a sum over K takes) sets the fault word as
+ * lstm_linear_attention's.
  * Errors: LSTM_E_INVALID, LSTM_E_LENGTH (workspace), LSTM_E_OVERFLOW,
  * LSTM_E_DEVICE, LSTM_E_CUDA. */
 size_t lstm_dense_workspace(const void *x, long long x_stride, const void *w, long long w_stride,

@@ -378,3 +378,23 @@ def test_rows_beyond_32_bits_of_elements(dtype):
     y = far.as_strided((rows, 48), (stride, 1)).copy_(r)
     assert torch.equal(binding.lstm_dense(x, w, residual=y, y=y), ref)
     assert torch.equal(binding.lstm_dense(far.as_strided((rows, 40), (stride, 1)).copy_(x), w, residual=r), ref)
+
+
+@pytest.mark.parametrize("rows", [4, 70])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sum_may_take_longer_than_a_wait(rows, dtype):
+    # a tile of this K takes milliseconds, the limit is one
+    lib = binding.load()
+    n_in = 1 << 22 if dtype == "bf16" else 1 << 20
+    x = torch.ones(rows, n_in, dtype=DTYPES[dtype], device="cuda")
+    w = torch.full((1, n_in), 2.0 ** -20, dtype=DTYPES[dtype], device="cuda")
+    assert binding.lstm_fault_status() == 0
+    try:
+        assert lib.lstm_test_dense_timeout(0, 1000, 0) == 0
+        y = binding.lstm_dense(x, w)
+        torch.cuda.synchronize()
+    finally:
+        assert lib.lstm_test_dense_timeout(0, 0, 0) == 0
+    assert binding.lstm_fault_status() == 0
+    # (powers of two: every partial sum is exact)
+    assert (y == n_in * 2.0 ** -20).all()
