@@ -162,10 +162,15 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
     uint64_t *acc_empty = acc_full + 2;       // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    // of a pair's first CTA: the K blocks that the second one has asked for, and that it asks for
+    // no more
+    volatile uint32_t *peer_total = tmem_slot + 2;
+    uint64_t *peer_done = reinterpret_cast<uint64_t *>(tmem_slot + 4);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        ptx::mbar_init(peer_done, 1);
         for (int s = 0; s < STAGES; ++s) {
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
@@ -220,6 +225,7 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
     const uint64_t limit_ns =
         test.wait_limit_ns + static_cast<uint64_t>(kb_end - kb_begin) * (sizeof(T) == 4 ? 1000000 : 10000);
     int issued = 0;  // K blocks, as far as they matter at the end: the last STAGES
+    uint32_t total = 0;
     int committed = 0;
     // the ring's next stage, and the parity of its turn (no divisions: a K block takes the
     // tensor core some 260 to 530 cycles, and one thread has to keep up)
@@ -272,9 +278,17 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
                     }
                     if (issued < STAGES)
                         ++issued;
+                    ++total;
                     advance();
                 }
             }
+        }
+        if (S::PAIR && lane == 0 && rank > 0) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                             ptx::map_to_rank(ptx::smem_u32(const_cast<uint32_t *>(peer_total)), 0)),
+                         "r"(total)
+                         : "memory");
+            ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(peer_done), 0));
         }
     } else if (warp == MMA_WARP && rank > 0) {
         // (the first CTA of a pair issues for both, and waits for both at the end)
@@ -596,7 +610,18 @@ dense_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ 
     __syncthreads();
     if (warp == PRODUCER_WARP && lane == 0 && rank == 0) {
         // every load has landed before the CTA's shared memory goes away (a pair's second CTA
-        // waits for the first below)
+        // waits for the first below; where this one stopped earlier, what the other asked for
+        // alone counts too)
+        if constexpr (S::PAIR) {
+            ptx::mbar_wait_drain(peer_done, 0, fault, limit_ns + kDefaultWaitLimitNs);
+            if (ptx::mbar_try_wait_cluster(peer_done, 0))
+                for (int more = static_cast<int>(*peer_total - total); more > 0; --more) {
+                    ptx::mbar_arrive_expect_tx(&full[s], S::STAGE_BYTES);
+                    if (issued < STAGES)
+                        ++issued;
+                    advance();
+                }
+        }
         for (; issued > 0; --issued) {
             if (s == 0) {
                 s = STAGES;
