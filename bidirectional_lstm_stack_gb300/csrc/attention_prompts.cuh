@@ -33,10 +33,10 @@
 // and so are P and S.  Of two factors' parts those products are made that the other roundings
 // leave visible (parts a, b with a + b below the larger number of parts).
 //
-// What bounds it: with bf16 and 128 keys and values a chunk's products take the tensor core
-// 2 180 cycles (scores 8 x 51, inter 16 x 35, intra 8 x 51, update 12 x 67), shared memory some
-// 2 700 and the ALU pipe 2 200; the warps' chains, whose instructions exceed the instruction
-// cache, make it 5 000.  16 heads of a prompt of 4096 tokens take 52 us (68 MB: 10 us), four
+// What bounds it: with bf16 and 128 keys and values a chunk's products keep the tensor core busy
+// for 1 790 cycles, its instructions the ALU pipe for 1 780; the warps' chains, whose instructions
+// exceed the instruction cache, make it 5 000.  fp16 and fp32 wait for their loaders (13.4 and
+// 14.2 us a chunk).  16 heads of a prompt of 4096 tokens take 52 us (68 MB: 10 us), four
 // prompts of 16384 tokens 478 us (675 MB: 99 us).  Waits, loops and rare branches are kept
 // short for that reason: inlining a wait's clock and messages at its 20 places cost a quarter
 // of the time at 64 keys.
