@@ -105,7 +105,7 @@ struct Info {
 constexpr int kOrdered = 128;
 constexpr int kInfos = 8;
 // Tokens of y that an output warp stores at a time: with 64 there is no room for a third stage at
-// 128 keys and values of bf16 (a chunk takes 2.54 us then, 2.41 so), at 64 keys there is (1.65 us,
+// 128 keys and values of bf16 (a chunk takes 2.54 us then, 2.42 so), at 64 keys there is (1.65 us,
 // 1.87 with 32).
 template <int KP>
 constexpr int kOutRows = KP == 128 ? 32 : C;

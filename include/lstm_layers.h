@@ -52,8 +52,8 @@ extern "C" {
  * below their last bit, of numbers as parts of bf16.  What a token adds to a
  * state goes as three parts, 24 bits (its decay's exponential is good to 2^-22).
  * With 16-bit types the products that make y take the state and the products of
- * queries and keys rounded to 16 bits (two parts of bf16), and LSTM_F16 leaves 2^-17
- * of a product out.
+ * queries and keys rounded to 16 bits (two parts of bf16), and LSTM_F16 leaves 2^-16
+ * of a product out at most.
  * With LSTM_F32 every factor goes as three parts: a product loses 2^-24 of itself
  * at most, and what of its factors lies below 2^-133.
  * An infinity or a NaN, or a product beyond fp32, makes what depends on it, itself
